@@ -29,6 +29,13 @@ streams default to torch's current stream):
   (``acquire``, ``submit_rs``, ``flush``).
 * ``Prefetcher``: ZeRO-3 fetch and prefetch of full parameters into per-rank
   arenas (``fetch``, ``full``, ``release``, ``stats``).
+* ``zr_layernorm_fwd(x, rows, cols, y, weight, bias, ...)`` and
+  ``zr_layernorm_bwd(dy, x, rows, cols, mean, rstd, weight, dx=..., dweight=...,
+  dbias=...)``: layer norm, whose parameter gradients may be slices of the flat
+  gradient; x may be an 8-bit checkpoint.
+* ``zr_ckpt_pack``, ``zr_ckpt_unpack``, ``zr_ckpt_wgrad``: 8-bit activation
+  checkpoints (uint8 buffers of ``zr_ckpt_bytes(rows, cols)``), and a linear
+  layer's weight gradient from the checkpoint of its input.
 * Host only: ``zr_pf_plan``, ``zr_plan_buckets``, ``zr_cost_*``.
 
 Example: eight ranks' bf16 gradients of N elements reduced into fp32
@@ -54,8 +61,9 @@ LIB_PATH = os.environ.get("ZR_LIBRARY") or os.path.join(_HERE, "libzr.so")
 (ZR_OK, ZR_ERR_INVALID, ZR_ERR_ALIGN, ZR_ERR_ALIAS, ZR_ERR_UNSUPPORTED, ZR_ERR_WORKSPACE, ZR_ERR_HIP,
  ZR_ERR_NOMEM) = range(8)
 ZR_BF16, ZR_FP32 = 0, 1
+ZR_CKPT_E4M3, ZR_CKPT_INT8 = 2, 3
 ZR_ORDER_RING, ZR_ORDER_FREE, ZR_ORDER_RING_WIRE = 0, 1, 2
-ZR_AVERAGE, ZR_ACCUMULATE = 1, 2
+ZR_AVERAGE, ZR_ACCUMULATE, ZR_ADD_DX = 1, 2, 4
 ZR_MAX_RANKS, ZR_MAX_ELEMS = 64, 1 << 40
 ZR_NOALLOC_TABLE_BYTES = 1 << 20
 STATUS_NAMES = {0: "ZR_OK", 1: "ZR_ERR_INVALID", 2: "ZR_ERR_ALIGN", 3: "ZR_ERR_ALIAS",
@@ -71,11 +79,13 @@ FLAT_PLAN_EXPORTS = ("zr_flatten_plan_create", "zr_flatten_plan_launch", "zr_fla
                      "zr_flatten_plan_destroy")
 PF_EXPORTS = ("zr_pf_create", "zr_pf_fetch", "zr_pf_release", "zr_pf_full", "zr_pf_get_stats",
               "zr_pf_destroy", "zr_pf_plan")
+NORM_EXPORTS = ("zr_ckpt_pack", "zr_ckpt_unpack", "zr_layernorm_fwd", "zr_layernorm_bwd", "zr_ckpt_wgrad",
+                "zr_ckpt_bytes", "zr_layernorm_workspace_bytes", "zr_ckpt_wgrad_workspace_bytes")
 EXPORTS = ("zr_last_error", "zr_version", "zr_workspace_bytes", "zr_flatten_bucket", "zr_reduce_scatter_avg",
            "zr_reduce_scatter_frags", "zr_all_gather", "zr_allreduce", "zr_plan_buckets", "zr_sched_create",
            "zr_sched_acquire", "zr_sched_submit_rs", "zr_sched_flush",
            "zr_sched_destroy", "zr_reduce_scatter_frags_noalloc") + COST_EXPORTS + PF_EXPORTS + \
-    RSF_PLAN_EXPORTS + FLAT_PLAN_EXPORTS + RS_PLAN_EXPORTS
+    RSF_PLAN_EXPORTS + FLAT_PLAN_EXPORTS + RS_PLAN_EXPORTS + NORM_EXPORTS
 
 
 class ZrError(RuntimeError):
@@ -171,6 +181,19 @@ def lib() -> ctypes.CDLL:
         L.zr_pf_plan.argtypes = [_cfgp, _i32, ctypes.POINTER(zr_pf_stats)]
         for f in EXPORTS[3:]:
             getattr(L, f).restype = ctypes.c_int
+        _f = ctypes.c_float
+        L.zr_ckpt_pack.argtypes = [_vp, _i32, _i64, _i64, _i64, _vp, _i32, _vp]
+        L.zr_ckpt_unpack.argtypes = [_vp, _i32, _i64, _i64, _vp, _i32, _i64, _vp]
+        L.zr_layernorm_fwd.argtypes = [_vp, _i32, _i64, _i64, _i64, _vp, _vp, _i32, _f, _vp, _i32, _i64, _vp,
+                                       _vp, _vp, _vp, _i32, _vp]
+        L.zr_layernorm_bwd.argtypes = [_vp, _i32, _i64, _vp, _i32, _i64, _i64, _i64, _vp, _i32, _vp, _vp, _vp,
+                                       _i32, _i64, _vp, _vp, _i32, _i32, _vp, _sz, _vp]
+        L.zr_ckpt_wgrad.argtypes = [_vp, _i32, _i64, _vp, _i32, _i64, _i64, _i64, _vp, _i32, _i64, _vp, _i32,
+                                    _vp, _sz, _vp]
+        L.zr_ckpt_bytes.argtypes = L.zr_layernorm_workspace_bytes.argtypes = [_i64, _i64]
+        L.zr_ckpt_wgrad_workspace_bytes.argtypes = [_i64, _i64, _i64]
+        for f in NORM_EXPORTS[5:]:
+            getattr(L, f).restype = _sz
         _d = ctypes.c_double
         for f in ("zr_cost_ring_allreduce", "zr_cost_ring_reduce_scatter",
                   "zr_cost_tree_allreduce", "zr_cost_naive_allreduce"):
@@ -673,3 +696,172 @@ class Prefetcher:
             self.close()
         except Exception:
             pass
+
+
+# ------------------------------------------- layer norm and 8-bit checkpoints
+def _matrix(x, rows: int, cols: int, dtype, ld, name: str):
+    """(address, dtype, row stride) of a rows x cols matrix: a torch tensor of
+    that shape whose rows are contiguous, or an address with its dtype (and
+    row stride, if not cols)."""
+    if x is None:
+        return 0, ZR_BF16, cols
+    if isinstance(x, int):
+        if dtype is None:
+            raise ValueError(f"{name} is an address: its dtype is needed")
+        return x, _dtype(dtype), cols if ld is None else ld
+    if dtype is not None and _dtype(dtype) != _dtype(x):
+        raise ValueError(f"{name} is {x.dtype}, not what its dtype argument says")
+    if tuple(x.shape) != (rows, cols):
+        if x.dim() == 2 or x.numel() != rows * cols or not x.is_contiguous():
+            raise ValueError(f"{name} is not {rows} x {cols}")
+        stride = cols
+    elif cols > 1 and x.stride(1) != 1:
+        raise ValueError(f"{name} has rows that are not contiguous")
+    else:
+        stride = x.stride(0) if rows > 1 else max(cols, x.stride(0))
+    if ld is not None and ld != stride and rows > 1:
+        raise ValueError(f"{name} has a row stride of {stride}, not {ld}")
+    return x.data_ptr(), _dtype(x), stride
+
+
+def _vector(x, n: int, dtype, name: str):
+    """(address, dtype) of n contiguous elements; (0, None) of None."""
+    if x is None:
+        return 0, None
+    if isinstance(x, int):
+        return x, _dtype(dtype) if dtype is not None else None
+    if dtype is not None and _dtype(dtype) != _dtype(x):
+        raise ValueError(f"{name} is {x.dtype}, not what its dtype argument says")
+    if x.numel() != n or not x.is_contiguous():
+        raise ValueError(f"{name} is not {n} contiguous elements")
+    return x.data_ptr(), _dtype(x)
+
+
+def _one_dtype(pairs, default: int, what: str) -> int:
+    found = {dt for _, dt in pairs if dt is not None}
+    if len(found) > 1:
+        raise ValueError(f"{what} are of different dtypes")
+    return found.pop() if found else default
+
+
+def _ckpt(x, rows: int, cols: int, name: str) -> int:
+    """Address of a checkpoint: a contiguous tensor of one-byte elements, of
+    zr_ckpt_bytes(rows, cols) of them at least, or an address."""
+    if x is None or isinstance(x, int):
+        return x or 0
+    if x.element_size() != 1 or not x.is_contiguous() or x.numel() < zr_ckpt_bytes(rows, cols):
+        raise ValueError(f"{name} is not a contiguous buffer of zr_ckpt_bytes({rows}, {cols}) bytes")
+    return x.data_ptr()
+
+
+def _run_on(stream, *xs) -> int:
+    """The stream's handle, for a call on these buffers: tensors must be on the
+    GPU that the stream is on (torch's current stream: on the current GPU)."""
+    import torch
+    here = None
+    for x in xs:
+        x = x[0] if isinstance(x, tuple) else x
+        if x is None or isinstance(x, int):
+            continue
+        if not x.is_cuda:
+            raise ValueError("a tensor is not on the GPU")
+        if here is None:
+            here = x.device
+        if x.device != here:
+            raise ValueError(f"tensors on {here} and {x.device}")
+    if here is not None:
+        on = torch.cuda.current_device()
+        if here.index != on or (stream is not None and not isinstance(stream, int) and stream.device != here):
+            raise ValueError(f"the tensors are on {here}, the current GPU is {on}: make theirs current, and its stream")
+    return _stream(stream)
+
+
+def zr_ckpt_bytes(rows: int, cols: int) -> int:
+    return lib().zr_ckpt_bytes(rows, cols)
+
+
+def zr_layernorm_workspace_bytes(rows: int, cols: int) -> int:
+    return lib().zr_layernorm_workspace_bytes(rows, cols)
+
+
+def zr_ckpt_wgrad_workspace_bytes(rows: int, out_cols: int, in_cols: int) -> int:
+    return lib().zr_ckpt_wgrad_workspace_bytes(rows, out_cols, in_cols)
+
+
+def zr_ckpt_pack(x, rows: int, cols: int, ckpt, format: int = ZR_CKPT_E4M3, dtype=None, ld=None,
+                 stream=None) -> None:
+    """x (rows x cols, bf16 or fp32) into the checkpoint buffer `ckpt`."""
+    px, dt, ldx = _matrix(x, rows, cols, dtype, ld, "x")
+    _check(lib().zr_ckpt_pack(px, dt, rows, cols, ldx, _ckpt(ckpt, rows, cols, "ckpt"), format,
+                              _run_on(stream, x, ckpt)))
+
+
+def zr_ckpt_unpack(ckpt, rows: int, cols: int, x, format: int = ZR_CKPT_E4M3, dtype=None, ld=None,
+                   stream=None) -> None:
+    """The values of a checkpoint into x (rows x cols, bf16 or fp32)."""
+    px, dt, ldx = _matrix(x, rows, cols, dtype, ld, "x")
+    _check(lib().zr_ckpt_unpack(_ckpt(ckpt, rows, cols, "ckpt"), format, rows, cols, px, dt, ldx,
+                                _run_on(stream, x, ckpt)))
+
+
+def _source(x, rows, cols, x_dtype, ld):
+    """(address, dtype, row stride) of a norm's input: values, or a checkpoint
+    (x_dtype its format)."""
+    if x_dtype in (ZR_CKPT_E4M3, ZR_CKPT_INT8):
+        return _ckpt(x, rows, cols, "x"), x_dtype, cols
+    return _matrix(x, rows, cols, x_dtype, ld, "x")
+
+
+def zr_layernorm_fwd(x, rows: int, cols: int, y=None, weight=None, bias=None, eps: float = 1e-5, mean=None,
+                     rstd=None, ckpt_x=None, ckpt_y=None, ckpt_format: int = ZR_CKPT_E4M3, x_dtype=None,
+                     y_dtype=None, param_dtype=None, ld_x=None, ld_y=None, stream=None) -> None:
+    """Layer norm of x's rows into y; mean and rstd (fp32), if given, receive
+    the statistics, ckpt_x and ckpt_y the 8-bit checkpoints of x and y. With
+    x_dtype a checkpoint format, x is a checkpoint. y_dtype: of y, and with y
+    None, what ckpt_y's values are rounded to (default bf16)."""
+    px, xd, ldx = _source(x, rows, cols, x_dtype, ld_x)
+    if y is None:
+        py, yd, ldy = 0, ZR_BF16 if y_dtype is None else _dtype(y_dtype), cols
+    else:
+        py, yd, ldy = _matrix(y, rows, cols, y_dtype, ld_y, "y")
+    w, b = _vector(weight, cols, param_dtype, "weight"), _vector(bias, cols, param_dtype, "bias")
+    _check(lib().zr_layernorm_fwd(px, xd, rows, cols, ldx, w[0], b[0], _one_dtype((w, b), ZR_FP32, "weight and bias"),
+                                  eps, py, yd, ldy, _vector(mean, rows, ZR_FP32, "mean")[0],
+                                  _vector(rstd, rows, ZR_FP32, "rstd")[0], _ckpt(ckpt_x, rows, cols, "ckpt_x"),
+                                  _ckpt(ckpt_y, rows, cols, "ckpt_y"), ckpt_format,
+                                  _run_on(stream, x, y, weight, bias, mean, rstd, ckpt_x, ckpt_y)))
+
+
+def zr_layernorm_bwd(dy, x, rows: int, cols: int, mean, rstd, weight=None, dx=None, dweight=None, dbias=None,
+                     accumulate: bool = False, add_dx: bool = False, workspace=None, dy_dtype=None, x_dtype=None,
+                     dx_dtype=None, param_dtype=None, grad_dtype=None, ld_dy=None, ld_x=None, ld_dx=None,
+                     stream=None) -> None:
+    """Gradients of zr_layernorm_fwd: of its input (dx, added to with add_dx)
+    and of its weight and bias (dweight, dbias, added to with accumulate, with
+    a workspace of zr_layernorm_workspace_bytes)."""
+    pdy, dyd, lddy = _matrix(dy, rows, cols, dy_dtype, ld_dy, "dy")
+    px, xd, ldx = _source(x, rows, cols, x_dtype, ld_x)
+    pdx, dxd, lddx = _matrix(dx, rows, cols, dx_dtype, ld_dx, "dx")
+    w = _vector(weight, cols, param_dtype, "weight")
+    gw, gb = _vector(dweight, cols, grad_dtype, "dweight"), _vector(dbias, cols, grad_dtype, "dbias")
+    ws, wsb = _workspace(workspace)
+    _check(lib().zr_layernorm_bwd(pdy, dyd, lddy, px, xd, ldx, rows, cols, w[0], _one_dtype((w,), ZR_FP32, "weight"),
+                                  _vector(mean, rows, ZR_FP32, "mean")[0], _vector(rstd, rows, ZR_FP32, "rstd")[0],
+                                  pdx, dxd, lddx, gw[0], gb[0], _one_dtype((gw, gb), ZR_FP32, "dweight and dbias"),
+                                  (ZR_ACCUMULATE if accumulate else 0) | (ZR_ADD_DX if add_dx else 0), ws, wsb,
+                                  _run_on(stream, dy, x, mean, rstd, weight, dx, dweight, dbias, workspace)))
+
+
+def zr_ckpt_wgrad(dy, ckpt, rows: int, out_cols: int, in_cols: int, dw, dbias=None, format: int = ZR_CKPT_E4M3,
+                  accumulate: bool = False, workspace=None, dy_dtype=None, grad_dtype=None, ld_dy=None, ld_dw=None,
+                  stream=None) -> None:
+    """dw (out_cols x in_cols) and dbias of a linear layer from its output's
+    gradient dy (rows x out_cols) and its input's checkpoint."""
+    pdy, dyd, lddy = _matrix(dy, rows, out_cols, dy_dtype, ld_dy, "dy")
+    pdw, gd, lddw = _matrix(dw, out_cols, in_cols, grad_dtype, ld_dw, "dw")
+    gb = _vector(dbias, out_cols, grad_dtype if isinstance(dbias, int) else None, "dbias")
+    ws, wsb = _workspace(workspace)
+    _check(lib().zr_ckpt_wgrad(pdy, dyd, lddy, _ckpt(ckpt, rows, in_cols, "ckpt"), format, rows, out_cols, in_cols,
+                               pdw, _one_dtype(((pdw, gd), gb), gd, "dw and dbias"), lddw, gb[0],
+                               ZR_ACCUMULATE if accumulate else 0, ws, wsb,
+                               _run_on(stream, dy, ckpt, dw, dbias, workspace)))

@@ -302,6 +302,111 @@ zr_status validate_ag(int K, const void* const* shards, void* const* fulls, zr_d
     return ok();
 }
 
+namespace {
+
+// ------------------------------------------- layer norm and checkpoints
+constexpr int64_t kMaxCols = (int64_t)1 << 30;
+
+bool fmt_valid(int dt) { return dt == ZR_CKPT_E4M3 || dt == ZR_CKPT_INT8; }
+int64_t pitch_of(int64_t cols) { return (cols + 31) / 32 * 32; }
+// rows x ld, ld rounded up to whole blocks, within 2^40.
+bool size_valid(int64_t rows, int64_t ld) { return rows >= 0 && ld >= 1 && rows <= kMaxElems / pitch_of(ld); }
+
+// A strided matrix's bytes: `rows` spans of `width`, `pitch` apart.
+struct Mat {
+    uintptr_t lo;
+    int64_t rows, pitch, width;
+    const char* name;
+};
+
+// Two matrices share a byte. Matrices of one pitch may interleave (column
+// slices of one buffer); otherwise their whole extents are compared.
+bool mats_overlap(const Mat& a, const Mat& b) {
+    const Range ra{a.lo, a.lo + (uintptr_t)((a.rows - 1) * a.pitch + a.width)};
+    const Range rb{b.lo, b.lo + (uintptr_t)((b.rows - 1) * b.pitch + b.width)};
+    if (!overlaps(ra, rb)) return false;
+    if (a.pitch != b.pitch || a.rows < 2 || b.rows < 2) return true;
+    const int64_t gap = b.lo >= a.lo ? (int64_t)((b.lo - a.lo) % (uintptr_t)a.pitch)
+                                     : (a.pitch - (int64_t)((a.lo - b.lo) % (uintptr_t)a.pitch)) % a.pitch;
+    return gap < a.width || gap + b.width > a.pitch;
+}
+
+// Buffers of a call: outputs must be disjoint from each other and from the
+// inputs, but for the pairs that `same` allows at equal address and shape.
+struct Buffers {
+    std::vector<Mat> in, out;
+
+    static zr_status check(const void* p, int64_t es, const char* name) {
+        if (!p) return fail(ZR_ERR_INVALID, "%s is NULL", name);
+        if ((uintptr_t)p & (uintptr_t)(es - 1))
+            return fail(ZR_ERR_ALIGN, "%s=%p is not aligned to %lld bytes", name, p, (long long)es);
+        return ok();
+    }
+    // A rows x cols matrix of elements of es bytes with row stride ld.
+    zr_status matrix(bool output, const void* p, int64_t es, int64_t rows, int64_t cols, int64_t ld, const char* name) {
+        if (ld < cols) return fail(ZR_ERR_INVALID, "ld of %s (%lld) is below %lld", name, (long long)ld, (long long)cols);
+        if (!size_valid(rows, ld)) return fail(ZR_ERR_INVALID, "%s is larger than 2^40 elements", name);
+        if (rows == 0) return ok();
+        ZR_TRY(check(p, es, name));
+        (output ? out : in).push_back(Mat{(uintptr_t)p, rows, ld * es, cols * es, name});
+        return ok();
+    }
+    zr_status vector(bool output, const void* p, int64_t es, int64_t n, const char* name) {
+        if (n == 0) return ok();
+        ZR_TRY(check(p, es, name));
+        (output ? out : in).push_back(Mat{(uintptr_t)p, 1, n * es, n * es, name});
+        return ok();
+    }
+    zr_status ckpt(bool output, const void* p, int64_t rows, int64_t cols, const char* name) {
+        if (!size_valid(rows, cols)) return fail(ZR_ERR_INVALID, "%s is larger than 2^40 elements", name);
+        if (rows == 0) return ok();
+        ZR_TRY(check(p, 16, name));
+        const int64_t bytes = rows * (pitch_of(cols) / 32 * 33);
+        (output ? out : in).push_back(Mat{(uintptr_t)p, 1, bytes, bytes, name});
+        return ok();
+    }
+    // in_place: this output may be an input of the same address, row stride and width
+    zr_status disjoint(const char* in_place) const {
+        for (size_t i = 0; i < out.size(); ++i) {
+            for (size_t j = i + 1; j < out.size(); ++j)
+                if (mats_overlap(out[i], out[j]))
+                    return fail(ZR_ERR_ALIAS, "%s and %s overlap", out[i].name, out[j].name);
+            for (const Mat& m : in) {
+                if (!mats_overlap(out[i], m)) continue;
+                if (in_place && !std::strcmp(out[i].name, in_place) && out[i].lo == m.lo && out[i].rows == m.rows &&
+                    out[i].pitch == m.pitch && out[i].width == m.width &&
+                    (!std::strcmp(m.name, "x") || !std::strcmp(m.name, "dy")))
+                    continue;
+                return fail(ZR_ERR_ALIAS, "%s overlaps %s", out[i].name, m.name);
+            }
+        }
+        return ok();
+    }
+};
+
+zr_status check_cols(int64_t rows, int64_t cols, const char* name) {
+    if (rows < 0) return fail(ZR_ERR_INVALID, "rows=%lld is negative", (long long)rows);
+    if (cols < 1 || cols > kMaxCols) return fail(ZR_ERR_INVALID, "%s=%lld not in [1, 2^30]", name, (long long)cols);
+    return ok();
+}
+
+// The kernels' library is the one that is loaded (not a build of this layer alone).
+template <class F>
+zr_status have(F* f, const char* what) {
+    if (!f) return fail(ZR_ERR_HIP, "%s: built without kernels", what);
+    return ok();
+}
+
+zr_status need_workspace(Buffers& b, const void* ws, size_t ws_bytes, size_t need) {
+    if (need == 0) return ok();
+    if (!ws || ws_bytes < need)
+        return fail(ZR_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu bytes needed", ws ? ws_bytes : 0,
+                    need);
+    return b.vector(true, ws, 4, (int64_t)(need / 4), "workspace");
+}
+
+}  // namespace
+
 // The prefetch coordinator's configuration; `buffers` also checks the shard
 // and arena tables (zr_pf_plan needs only the sizes and the trace).
 zr_status validate_pf(const zr_pf_config* c, bool buffers) {
@@ -911,6 +1016,167 @@ zr_status zr_plan_buckets(int n, const int64_t* numels, int64_t cap, int32_t* bu
     }
     *n_buckets = b + 1;
     return ok();
+}
+
+size_t zr_ckpt_bytes(int64_t rows, int64_t cols) {
+    if (cols < 1 || cols > kMaxCols || !size_valid(rows, cols)) return 0;
+    return (size_t)rows * (size_t)(pitch_of(cols) / 32 * 33);
+}
+
+zr_status zr_ckpt_pack(const void* x, zr_dtype dt, int64_t rows, int64_t cols, int64_t ld, void* ckpt, zr_dtype format,
+                       void* stream) {
+    return zr::guarded([&]() -> zr_status {
+        if (!dt_valid(dt) || !fmt_valid(format))
+            return fail(ZR_ERR_UNSUPPORTED, "dtype %d to format %d not supported", (int)dt, (int)format);
+        ZR_TRY(check_cols(rows, cols, "cols"));
+        Buffers b;
+        ZR_TRY(b.matrix(false, x, dt_bytes(dt), rows, cols, ld, "x"));
+        ZR_TRY(b.ckpt(true, ckpt, rows, cols, "ckpt"));
+        ZR_TRY(b.disjoint(nullptr));
+        if (rows == 0) return ok();
+        ZR_TRY(have(launch_ckpt_pack, "checkpoint pack"));
+        return launched(launch_ckpt_pack(x, dt, rows, cols, ld, format, ckpt, (hipStream_t)stream), (hipStream_t)stream,
+                        "checkpoint pack launch");
+    });
+}
+
+zr_status zr_ckpt_unpack(const void* ckpt, zr_dtype format, int64_t rows, int64_t cols, void* x, zr_dtype dt, int64_t ld,
+                         void* stream) {
+    return zr::guarded([&]() -> zr_status {
+        if (!dt_valid(dt) || !fmt_valid(format))
+            return fail(ZR_ERR_UNSUPPORTED, "format %d to dtype %d not supported", (int)format, (int)dt);
+        ZR_TRY(check_cols(rows, cols, "cols"));
+        Buffers b;
+        ZR_TRY(b.ckpt(false, ckpt, rows, cols, "ckpt"));
+        ZR_TRY(b.matrix(true, x, dt_bytes(dt), rows, cols, ld, "x"));
+        ZR_TRY(b.disjoint(nullptr));
+        if (rows == 0) return ok();
+        ZR_TRY(have(launch_ckpt_unpack, "checkpoint unpack"));
+        return launched(launch_ckpt_unpack(ckpt, format, rows, cols, x, dt, ld, (hipStream_t)stream),
+                        (hipStream_t)stream, "checkpoint unpack launch");
+    });
+}
+
+zr_status zr_layernorm_fwd(const void* x, zr_dtype x_dt, int64_t rows, int64_t cols, int64_t ld_x, const void* weight,
+                           const void* bias, zr_dtype param_dt, float eps, void* y, zr_dtype y_dt, int64_t ld_y,
+                           float* mean, float* rstd, void* ckpt_x, void* ckpt_y, zr_dtype ckpt_format, void* stream) {
+    return zr::guarded([&]() -> zr_status {
+        const bool held = fmt_valid(x_dt);
+        if ((!dt_valid(x_dt) && !held) || !dt_valid(param_dt) || !dt_valid(y_dt))
+            return fail(ZR_ERR_UNSUPPORTED, "dtypes x %d, parameters %d, y %d not supported", (int)x_dt, (int)param_dt,
+                        (int)y_dt);
+        if ((ckpt_x || ckpt_y) && !fmt_valid(ckpt_format))
+            return fail(ZR_ERR_UNSUPPORTED, "checkpoint format %d not supported", (int)ckpt_format);
+        if (held && ckpt_x) return fail(ZR_ERR_INVALID, "ckpt_x is given for an x that is a checkpoint");
+        ZR_TRY(check_cols(rows, cols, "cols"));
+        if (!(eps >= 0.0f && eps <= 3.4e38f)) return fail(ZR_ERR_INVALID, "eps=%g is not >= 0 and finite", (double)eps);
+        if (!y && !mean && !rstd && !ckpt_x && !ckpt_y) return fail(ZR_ERR_INVALID, "no output is given");
+        Buffers b;
+        ZR_TRY(held ? b.ckpt(false, x, rows, cols, "x") : b.matrix(false, x, dt_bytes(x_dt), rows, cols, ld_x, "x"));
+        if (weight) ZR_TRY(b.vector(false, weight, dt_bytes(param_dt), cols, "weight"));
+        if (bias) ZR_TRY(b.vector(false, bias, dt_bytes(param_dt), cols, "bias"));
+        if (y) ZR_TRY(b.matrix(true, y, dt_bytes(y_dt), rows, cols, ld_y, "y"));
+        if (mean) ZR_TRY(b.vector(true, mean, 4, rows, "mean"));
+        if (rstd) ZR_TRY(b.vector(true, rstd, 4, rows, "rstd"));
+        if (ckpt_x) ZR_TRY(b.ckpt(true, ckpt_x, rows, cols, "ckpt_x"));
+        if (ckpt_y) ZR_TRY(b.ckpt(true, ckpt_y, rows, cols, "ckpt_y"));
+        ZR_TRY(b.disjoint(!held && x_dt == y_dt ? "y" : nullptr));
+        if (rows == 0) return ok();
+        ZR_TRY(have(launch_layernorm_fwd, "layer norm"));
+        NormFwd f{};
+        f.x = x; f.weight = weight; f.bias = bias;
+        f.x_dt = x_dt; f.param_dt = param_dt; f.y_dt = y_dt; f.ckpt_format = ckpt_format;
+        f.rows = rows; f.cols = cols; f.ld_x = ld_x; f.ld_y = ld_y;
+        f.eps = eps;
+        f.y = y; f.ckpt_x = ckpt_x; f.ckpt_y = ckpt_y;
+        f.mean = mean; f.rstd = rstd;
+        return launched(launch_layernorm_fwd(f, (hipStream_t)stream), (hipStream_t)stream, "layer norm launch");
+    });
+}
+
+size_t zr_layernorm_workspace_bytes(int64_t rows, int64_t cols) {
+    if (cols < 1 || cols > kMaxCols || !size_valid(rows, cols)) return 0;
+    return (size_t)layernorm_strips(rows, cols) * 2 * (size_t)cols * sizeof(float);
+}
+
+zr_status zr_layernorm_bwd(const void* dy, zr_dtype dy_dt, int64_t ld_dy, const void* x, zr_dtype x_dt, int64_t ld_x,
+                           int64_t rows, int64_t cols, const void* weight, zr_dtype param_dt, const float* mean,
+                           const float* rstd, void* dx, zr_dtype dx_dt, int64_t ld_dx, void* dweight, void* dbias,
+                           zr_dtype grad_dt, int flags, void* workspace, size_t ws_bytes, void* stream) {
+    return zr::guarded([&]() -> zr_status {
+        const bool held = fmt_valid(x_dt);
+        if ((!dt_valid(x_dt) && !held) || !dt_valid(dy_dt) || !dt_valid(param_dt) || !dt_valid(dx_dt) ||
+            !dt_valid(grad_dt))
+            return fail(ZR_ERR_UNSUPPORTED, "dtypes dy %d, x %d, parameters %d, dx %d, gradients %d not supported",
+                        (int)dy_dt, (int)x_dt, (int)param_dt, (int)dx_dt, (int)grad_dt);
+        if (flags & ~(ZR_ACCUMULATE | ZR_ADD_DX)) return fail(ZR_ERR_INVALID, "flags=%d has unknown bits", flags);
+        ZR_TRY(check_cols(rows, cols, "cols"));
+        if (!dx && !dweight && !dbias) return fail(ZR_ERR_INVALID, "no output is given");
+        Buffers b;
+        ZR_TRY(b.matrix(false, dy, dt_bytes(dy_dt), rows, cols, ld_dy, "dy"));
+        ZR_TRY(held ? b.ckpt(false, x, rows, cols, "x") : b.matrix(false, x, dt_bytes(x_dt), rows, cols, ld_x, "x"));
+        if (weight) ZR_TRY(b.vector(false, weight, dt_bytes(param_dt), cols, "weight"));
+        ZR_TRY(b.vector(false, mean, 4, rows, "mean"));
+        ZR_TRY(b.vector(false, rstd, 4, rows, "rstd"));
+        if (dx) ZR_TRY(b.matrix(true, dx, dt_bytes(dx_dt), rows, cols, ld_dx, "dx"));
+        if (dweight) ZR_TRY(b.vector(true, dweight, dt_bytes(grad_dt), cols, "dweight"));
+        if (dbias) ZR_TRY(b.vector(true, dbias, dt_bytes(grad_dt), cols, "dbias"));
+        if (dweight || dbias)
+            ZR_TRY(need_workspace(b, workspace, ws_bytes, zr_layernorm_workspace_bytes(rows, cols)));
+        // in place only where the elements are of one type
+        for (const Mat& m : b.in)
+            if (dx && (uintptr_t)dx == m.lo &&
+                ((!std::strcmp(m.name, "dy") && dx_dt != dy_dt) || (!std::strcmp(m.name, "x") && dx_dt != x_dt)))
+                return fail(ZR_ERR_ALIAS, "dx is %s but of another type", m.name);
+        ZR_TRY(b.disjoint("dx"));
+        if (rows == 0 && !dweight && !dbias) return ok();
+        ZR_TRY(have(launch_layernorm_bwd, "layer norm backward"));
+        NormBwd f{};
+        f.dy = dy; f.x = x; f.weight = weight; f.mean = mean; f.rstd = rstd;
+        f.dy_dt = dy_dt; f.x_dt = x_dt; f.param_dt = param_dt; f.dx_dt = dx_dt; f.grad_dt = grad_dt;
+        f.rows = rows; f.cols = cols; f.ld_dy = ld_dy; f.ld_x = ld_x; f.ld_dx = ld_dx;
+        f.dx = dx; f.dweight = dweight; f.dbias = dbias;
+        f.accumulate = (flags & ZR_ACCUMULATE) != 0; f.add_dx = (flags & ZR_ADD_DX) != 0;
+        f.workspace = workspace;
+        return launched(launch_layernorm_bwd(f, (hipStream_t)stream), (hipStream_t)stream, "layer norm backward launch");
+    });
+}
+
+size_t zr_ckpt_wgrad_workspace_bytes(int64_t rows, int64_t out_cols, int64_t in_cols) {
+    if (out_cols < 1 || out_cols > kMaxCols || in_cols < 1 || in_cols > kMaxCols || !size_valid(rows, out_cols) ||
+        !size_valid(rows, in_cols) || !size_valid(out_cols, in_cols))
+        return 0;
+    const int splits = wgrad_cut(rows, out_cols, in_cols).splits;
+    return splits > 1 ? (size_t)splits * (size_t)(out_cols * in_cols + out_cols) * sizeof(float) : 0;
+}
+
+zr_status zr_ckpt_wgrad(const void* dy, zr_dtype dy_dt, int64_t ld_dy, const void* ckpt, zr_dtype format, int64_t rows,
+                        int64_t out_cols, int64_t in_cols, void* dw, zr_dtype grad_dt, int64_t ld_dw, void* dbias,
+                        int flags, void* workspace, size_t ws_bytes, void* stream) {
+    return zr::guarded([&]() -> zr_status {
+        if (!dt_valid(dy_dt) || !fmt_valid(format) || !dt_valid(grad_dt))
+            return fail(ZR_ERR_UNSUPPORTED, "dtypes dy %d, checkpoint %d, gradients %d not supported", (int)dy_dt,
+                        (int)format, (int)grad_dt);
+        if (flags & ~ZR_ACCUMULATE) return fail(ZR_ERR_INVALID, "flags=%d has unknown bits", flags);
+        ZR_TRY(check_cols(rows, out_cols, "out_cols"));
+        ZR_TRY(check_cols(rows, in_cols, "in_cols"));
+        Buffers b;
+        ZR_TRY(b.matrix(false, dy, dt_bytes(dy_dt), rows, out_cols, ld_dy, "dy"));
+        ZR_TRY(b.ckpt(false, ckpt, rows, in_cols, "ckpt"));
+        ZR_TRY(b.matrix(true, dw, dt_bytes(grad_dt), out_cols, in_cols, ld_dw, "dw"));
+        if (dbias) ZR_TRY(b.vector(true, dbias, dt_bytes(grad_dt), out_cols, "dbias"));
+        ZR_TRY(need_workspace(b, workspace, ws_bytes, zr_ckpt_wgrad_workspace_bytes(rows, out_cols, in_cols)));
+        ZR_TRY(b.disjoint(nullptr));
+        ZR_TRY(have(launch_ckpt_wgrad, "weight gradient"));
+        Wgrad w{};
+        w.dy = dy; w.ckpt = ckpt;
+        w.dy_dt = dy_dt; w.format = format; w.grad_dt = grad_dt;
+        w.rows = rows; w.out = out_cols; w.in = in_cols; w.ld_dy = ld_dy; w.ld_dw = ld_dw;
+        w.dw = dw; w.dbias = dbias;
+        w.accumulate = (flags & ZR_ACCUMULATE) != 0;
+        w.workspace = workspace;
+        return launched(launch_ckpt_wgrad(w, (hipStream_t)stream), (hipStream_t)stream, "weight gradient launch");
+    });
 }
 
 }  // extern "C"

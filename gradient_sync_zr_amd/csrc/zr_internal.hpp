@@ -169,4 +169,76 @@ int flat_plan_launch_count(const FlatPlan* plan);
 hipError_t flat_plan_launch(const FlatPlan* plan, hipStream_t stream);
 void flat_plan_free(FlatPlan* plan);
 
+// Layer norm and 8-bit checkpoints. The launches are declared weak so that a
+// build of the C-ABI layer alone (argument validation, no kernels) links; its
+// calls then report that the kernels are missing.
+#define ZR_KERNELS __attribute__((weak))
+
+struct NormFwd {
+    const void *x, *weight, *bias;
+    zr_dtype x_dt, param_dt, y_dt, ckpt_format;
+    int64_t rows, cols, ld_x, ld_y;
+    float eps;
+    void *y, *ckpt_x, *ckpt_y;
+    float *mean, *rstd;
+};
+ZR_KERNELS hipError_t launch_layernorm_fwd(const NormFwd& f, hipStream_t stream);
+
+struct NormBwd {
+    const void *dy, *x, *weight;
+    const float *mean, *rstd;
+    zr_dtype dy_dt, x_dt, param_dt, dx_dt, grad_dt;
+    int64_t rows, cols, ld_dy, ld_x, ld_dx;
+    void *dx, *dweight, *dbias;
+    int accumulate, add_dx;
+    void* workspace;  // layernorm_strips(rows, cols) * 2 * cols floats
+};
+ZR_KERNELS hipError_t launch_layernorm_bwd(const NormBwd& f, hipStream_t stream);
+// Strips of rows that a backward pass leaves partial parameter gradients of:
+// one block each, as many as the chip holds at once, and no more than there
+// are steps of rows (a block takes 16, 4 or 1 rows at once).
+inline int layernorm_strips(int64_t rows, int64_t cols) {
+    const int64_t per = cols <= 128 ? 16 : (cols <= 1024 ? 4 : 1), n = (rows + per - 1) / per;
+    const int64_t most = tuning().max_grid < 512 ? tuning().max_grid : 512;
+    return (int)(n < most ? n : most);
+}
+
+ZR_KERNELS hipError_t launch_ckpt_pack(const void* x, zr_dtype dt, int64_t rows, int64_t cols, int64_t ld, zr_dtype fmt,
+                                       void* ckpt, hipStream_t stream);
+ZR_KERNELS hipError_t launch_ckpt_unpack(const void* ckpt, zr_dtype fmt, int64_t rows, int64_t cols, void* x,
+                                         zr_dtype dt, int64_t ld, hipStream_t stream);
+
+// How a weight gradient is cut: tiles of dW, one per block, and parts that the
+// sum over rows is split into (each of `span` rows) where the tiles alone do
+// not fill the chip's 512 places (two blocks per CU).
+constexpr int kWgradTile = 128;
+struct WgradCut {
+    int splits;
+    int64_t span;
+};
+inline WgradCut wgrad_cut(int64_t rows, int64_t out, int64_t in) {
+    const int64_t tiles = ((out + kWgradTile - 1) / kWgradTile) * ((in + kWgradTile - 1) / kWgradTile);
+    int64_t splits = 512 / tiles;
+    const int64_t most = rows / 128;  // a part is two slabs of rows at least
+    if (splits > most) splits = most;
+    if (splits > 64) splits = 64;
+    if (splits < 1) splits = 1;
+    WgradCut c;
+    c.span = ((rows + splits - 1) / splits + 63) / 64 * 64;
+    if (c.span < 64) c.span = 64;
+    c.splits = (int)((rows + c.span - 1) / c.span);
+    if (c.splits < 1) c.splits = 1;
+    return c;
+}
+
+struct Wgrad {
+    const void *dy, *ckpt;
+    zr_dtype dy_dt, format, grad_dt;
+    int64_t rows, out, in, ld_dy, ld_dw;
+    void *dw, *dbias;
+    int accumulate;
+    void* workspace;  // splits > 1: splits * (out * in + out) floats
+};
+ZR_KERNELS hipError_t launch_ckpt_wgrad(const Wgrad& w, hipStream_t stream);
+
 }  // namespace zr

@@ -1,0 +1,360 @@
+// Weight and bias gradient of a linear layer whose input was kept as an 8-bit
+// checkpoint:
+//     dW[o, i] = sum over rows t of dY[t, o] * X[t, i],   db[o] = sum dY[t, o]
+//
+// A matrix product whose two operands both have the summed index outermost. A
+// block computes a BM x BN tile of dW from slabs of BK rows: dY's slab goes to
+// LDS as it is, the checkpoint's is decoded to bf16 on the way (every held
+// value is exact in bf16), and both are read back transposed, 4 rows of one
+// column per lane and instruction (ds_read_b64_tr_b16), as the operands of
+// v_mfma_f32_32x32x16_bf16. Sums are fp32. fp32 dY is cut into three bf16
+// terms that add up to it exactly (8 mantissa bits each), so its product with
+// the checkpoint keeps fp32 accuracy on the bf16 matrix units.
+//
+// LDS rows are a multiple of 256 bytes, so the four rows that one transposed
+// read touches would lie in the same banks; each row's 64-byte windows are
+// exchanged by the row's number modulo 4, which spreads the read over all 64.
+//
+// Two slabs in LDS alternate: the next slab's loads are issued before the
+// current one is multiplied and land in registers meanwhile.
+//
+// When dW has fewer tiles than the chip has places for blocks, the rows are
+// split too; the parts go to the workspace in fp32 and a second kernel joins
+// them in order, so results do not change from run to run.
+#include <hip/hip_runtime.h>
+
+#include "zr_ckpt.hpp"
+#include "zr_internal.hpp"
+
+namespace zr {
+namespace {
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
+
+struct WgradArgs {
+    const void* dy;
+    const char* codes;
+    const uint8_t* scales;
+    float* part;  // splits > 1: [splits][out * in + out]
+    void *dw, *db;
+    int64_t rows, out, in, ld_dy, ld_dw, pitch, span;
+    int grad_dt, accumulate, tiles_m, tiles_n, splits;
+};
+
+// 16 codes of one block as 16 bf16 values (8 words).
+template <int FMT>
+__device__ __forceinline__ void decode16(const u32x4& q, uint32_t s, uint32_t w[8]) {
+    const float scale = ckpt_scale(s);
+    const uint32_t c[4] = {q.x, q.y, q.z, q.w};
+    if constexpr (FMT == kE4m3) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            w[2 * k] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[k], scale, false));
+            w[2 * k + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[k], scale, true));
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const uint32_t h = c[k >> 1] >> (16 * (k & 1));
+            const float a = (float)(int)(int8_t)h * scale, b = (float)(int)(int8_t)(h >> 8) * scale;
+            // exact in bf16: the upper halves are the values
+            w[k] = __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
+        }
+    }
+}
+
+// Three bf16 terms (upper halves of a word each) that add up to v: each takes
+// the next 8 mantissa bits. An infinity has one term.
+__device__ __forceinline__ void split3(float v, uint32_t t[3]) {
+    const uint32_t u = __float_as_uint(v);
+    t[0] = u & 0xFFFF0000u;
+    const bool inf = (u & 0x7FFFFFFFu) == 0x7F800000u;
+    const float r = inf ? 0.0f : v - __uint_as_float(t[0]);
+    t[1] = __float_as_uint(r) & 0xFFFF0000u;
+    const float r2 = r - __uint_as_float(t[1]);
+    t[2] = __float_as_uint(r2) & 0xFFFF0000u;
+}
+
+// Which tile and part a block's item is: consecutive items of one XCD (blocks
+// are dealt to the 8 XCDs in turn) take neighbouring tiles, so that their
+// slabs meet in that XCD's L2.
+__device__ __forceinline__ void item_place(const WgradArgs& a, int64_t item, int64_t total, int* tm, int* tn, int* part) {
+    const int64_t x = item % 8, i = item / 8, q = total / 8, r = total % 8;
+    const int64_t at = (x < r ? x * (q + 1) : r * (q + 1) + (x - r) * q) + i;
+    const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
+    *part = (int)(at / tiles);
+    const int64_t t = at % tiles;
+    constexpr int GM = 8;
+    const int64_t per = (int64_t)GM * a.tiles_n;
+    const int64_t group = t / per, in_group = t % per;
+    const int first = (int)(group * GM);
+    const int gm = a.tiles_m - first < GM ? a.tiles_m - first : GM;
+    *tm = first + (int)(in_group % gm);
+    *tn = (int)(in_group / gm);
+}
+
+template <int DD, int FMT, int BM, int BN, int WM, int WN, int BK>
+__global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void wgrad_kernel(WgradArgs a) {
+    constexpr int T = (BM / WM) * (BN / WN) * 64;  // threads
+    constexpr int P = DD == kFp32 ? 3 : 1;         // bf16 terms of dY
+    constexpr int PA = BM * 2, PB = BN * 2;        // LDS row bytes
+    constexpr int CA = BM / 8, CB = BN / 16;       // chunks per row: 8 of dY, 16 codes
+    constexpr int NA = BK * CA / T, NB = BK * CB / T;
+    constexpr int MT = WM / 32, NT = WN / 32;
+    static_assert(BK * CA % T == 0 && BK * CB % T == 0 && T % CA == 0, "whole chunks per thread");
+    constexpr int SA = BK * PA, SB = BK * PB, STAGE = P * SA + SB;
+    __shared__ __attribute__((aligned(1024))) char lds[2 * STAGE];
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int wm = wave / (BN / WN), wn = wave % (BN / WN);
+    const int64_t total = (int64_t)a.tiles_m * a.tiles_n * a.splits;
+
+    // This lane's place in a transposed read: 16 lanes hold 4 rows of 16
+    // columns and get one column each.
+    const int r4 = (lane >> 2) & 3, rbase = (lane >> 5) * 8 + r4;
+    int offA[MT], offB[NT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+        offA[m] = rbase * PA + (((wm * WM + m * 32) * 2) ^ (r4 << 6)) + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+        offB[n] = P * SA + rbase * PB + (((wn * WN + n * 32) * 2) ^ (r4 << 6)) + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
+
+    for (int64_t item = blockIdx.x; item < total; item += gridDim.x) {
+        int tm, tn, part;
+        item_place(a, item, total, &tm, &tn, &part);
+        const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
+        const int64_t kb = part * a.span, ke = kb + a.span < a.rows ? kb + a.span : a.rows;
+        const bool bias = a.db && tn == 0;
+
+        f32x16 acc[MT][NT];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) acc[m][n][e] = 0.0f;
+        float sums[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+
+        Raw8<DD> ra[NA];
+        u32x4 rb[NB];
+        uint32_t rs[NB];
+        auto fetch = [&](int64_t k) {
+#pragma unroll
+            for (int j = 0; j < NA; ++j) {
+                const int id = tid + j * T;
+                const int64_t row = k + id / CA, col = m0 + (id % CA) * 8;
+                const int64_t left = row < ke ? a.out - col : 0;
+                const int n = left >= 8 ? 8 : (left > 0 ? (int)left : 0);
+                ra[j] = load8<DD>({(const char*)a.dy + row * a.ld_dy * (DD == kBf16 ? 2 : 4), nullptr}, (int)col, n);
+            }
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+                const int id = tid + j * T;
+                const int64_t row = k + id / CB, col = n0 + (id % CB) * 16;
+                rb[j] = u32x4{0, 0, 0, 0};
+                rs[j] = 127;
+                if (row < ke && col < a.pitch) {
+                    rb[j] = *(const u32x4*)(a.codes + row * a.pitch + col);
+                    rs[j] = a.scales[row * (a.pitch / kCkptBlock) + col / kCkptBlock];
+                }
+            }
+        };
+        auto stage = [&](char* buf) {
+#pragma unroll
+            for (int j = 0; j < NA; ++j) {
+                const int id = tid + j * T, t = id / CA, c = id % CA;
+                char* at = buf + t * PA + ((c * 16) ^ ((t & 3) << 6));
+                if constexpr (DD == kBf16) {
+                    *(u32x4*)at = ra[j].v;
+                } else {
+                    float f[8];
+                    uint32_t w[3][4];
+                    widen8(ra[j], f);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t lo[3], hi[3];
+                        split3(f[2 * e], lo);
+                        split3(f[2 * e + 1], hi);
+#pragma unroll
+                        for (int p = 0; p < 3; ++p) w[p][e] = (lo[p] >> 16) | hi[p];
+                    }
+#pragma unroll
+                    for (int p = 0; p < 3; ++p) *(u32x4*)(at + p * SA) = u32x4{w[p][0], w[p][1], w[p][2], w[p][3]};
+                }
+                if (bias) {
+                    float f[8];
+                    widen8(ra[j], f);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) sums[e] += f[e];
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+                const int id = tid + j * T, t = id / CB, c = id % CB;
+                uint32_t w[8];
+                decode16<FMT>(rb[j], rs[j], w);
+                char* at = buf + P * SA + t * PB;
+                *(u32x4*)(at + ((c * 32) ^ ((t & 3) << 6))) = u32x4{w[0], w[1], w[2], w[3]};
+                *(u32x4*)(at + ((c * 32 + 16) ^ ((t & 3) << 6))) = u32x4{w[4], w[5], w[6], w[7]};
+            }
+        };
+        auto operand = [&](const char* at, int pitch) {
+            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)at);
+            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(at + 4 * pitch));
+            return __builtin_bit_cast(bf16x8, (s16x8)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        };
+        auto multiply = [&](const char* buf) {
+#pragma unroll
+            for (int k = 0; k < BK; k += 16) {
+                bf16x8 fb[NT];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) fb[n] = operand(buf + offB[n] + k * PB, PB);
+#pragma unroll
+                for (int p = 0; p < P; ++p) {
+                    bf16x8 fa[MT];
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) fa[m] = operand(buf + offA[m] + p * SA + k * PA, PA);
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[m], fb[n], acc[m][n], 0, 0, 0);
+                }
+            }
+        };
+
+        if (kb < ke) {
+            fetch(kb);
+            stage(lds);
+            __syncthreads();
+            int cur = 0;
+            for (int64_t k = kb; k < ke; k += BK) {
+                const bool more = k + BK < ke;
+                if (more) fetch(k + BK);
+                multiply(lds + cur * STAGE);
+                if (more) stage(lds + (cur ^ 1) * STAGE);
+                __syncthreads();
+                cur ^= 1;
+            }
+        }
+
+        // D's layout: lane & 31 is the column, element e the row
+        // (e / 4) * 8 + (lane / 32) * 4 + e % 4.
+        float* const mine = a.splits > 1 ? a.part + (int64_t)part * (a.out * a.in + a.out) : nullptr;
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int64_t o = m0 + wm * WM + m * 32 + (e >> 2) * 8 + (lane >> 5) * 4 + (e & 3);
+                    const int64_t i = n0 + wn * WN + n * 32 + (lane & 31);
+                    if (o >= a.out || i >= a.in) continue;
+                    const float v = acc[m][n][e];
+                    if (mine) {
+                        mine[o * a.in + i] = v;
+                    } else if (a.grad_dt == kBf16) {
+                        uint16_t* p = (uint16_t*)a.dw + o * a.ld_dw + i;
+                        store_elem(p, a.accumulate ? load_elem(p) + v : v);
+                    } else {
+                        float* p = (float*)a.dw + o * a.ld_dw + i;
+                        store_elem(p, a.accumulate ? load_elem(p) + v : v);
+                    }
+                }
+        if (bias) {  // the threads that hold the same 8 columns
+            float* s = (float*)lds;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[(tid / CA) * BM + (tid % CA) * 8 + e] = sums[e];
+            __syncthreads();
+            for (int c = tid; c < BM; c += T) {
+                float v = 0.0f;
+#pragma unroll
+                for (int r = 0; r < T / CA; ++r) v += s[r * BM + c];
+                const int64_t o = m0 + c;
+                if (o < a.out) {
+                    if (mine) {
+                        mine[a.out * a.in + o] = v;
+                    } else if (a.grad_dt == kBf16) {
+                        uint16_t* p = (uint16_t*)a.db + o;
+                        store_elem(p, a.accumulate ? load_elem(p) + v : v);
+                    } else {
+                        float* p = (float*)a.db + o;
+                        store_elem(p, a.accumulate ? load_elem(p) + v : v);
+                    }
+                }
+            }
+            __syncthreads();
+        }
+    }
+}
+
+// Sums the parts, in order. Items are runs of 1024 columns of a row of dW,
+// and after them runs of db.
+__global__ __launch_bounds__(kThreads) void wgrad_join_kernel(WgradArgs a) {
+    const int64_t segs = (a.in + 1023) / 1024, bsegs = a.db ? (a.out + 1023) / 1024 : 0;
+    const int64_t stride = a.out * a.in + a.out;
+    for (int64_t item = blockIdx.x; item < a.out * segs + bsegs; item += gridDim.x) {
+        const bool bias = item >= a.out * segs;
+        const int64_t o = bias ? a.out : item / segs;
+        const int64_t c0 = (bias ? item - a.out * segs : item % segs) * 1024, end = bias ? a.out : a.in;
+        const float* src = a.part + o * a.in;
+        char* dst = bias ? (char*)a.db : (char*)a.dw + o * a.ld_dw * (a.grad_dt == kBf16 ? 2 : 4);
+        for (int64_t c = c0 + threadIdx.x; c < end && c < c0 + 1024; c += kThreads) {
+            float v = 0.0f;
+            for (int s = 0; s < a.splits; ++s) v += src[s * stride + c];
+            if (a.grad_dt == kBf16) {
+                uint16_t* p = (uint16_t*)dst + c;
+                store_elem(p, a.accumulate ? load_elem(p) + v : v);
+            } else {
+                float* p = (float*)dst + c;
+                store_elem(p, a.accumulate ? load_elem(p) + v : v);
+            }
+        }
+    }
+}
+
+template <int DD, int FMT>
+hipError_t run(const WgradArgs& a, hipStream_t stream) {
+    const int64_t total = (int64_t)a.tiles_m * a.tiles_n * a.splits;
+    const int grid = grid_for(total);
+    wgrad_kernel<DD, FMT, kWgradTile, kWgradTile, 64, 64, DD == kBf16 ? 64 : 32><<<grid, 256, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_ckpt_wgrad(const Wgrad& w, hipStream_t stream) {
+    const WgradCut cut = wgrad_cut(w.rows, w.out, w.in);
+    WgradArgs a{};
+    a.dy = w.dy;
+    a.pitch = ckpt_pitch(w.in);
+    a.codes = (const char*)w.ckpt;
+    a.scales = (const uint8_t*)w.ckpt + w.rows * a.pitch;
+    a.part = (float*)w.workspace;
+    a.dw = w.dw;
+    a.db = w.dbias;
+    a.rows = w.rows; a.out = w.out; a.in = w.in; a.ld_dy = w.ld_dy; a.ld_dw = w.ld_dw;
+    a.span = cut.span;
+    a.grad_dt = w.grad_dt; a.accumulate = w.accumulate;
+    a.tiles_m = (int)((w.out + kWgradTile - 1) / kWgradTile);
+    a.tiles_n = (int)((w.in + kWgradTile - 1) / kWgradTile);
+    a.splits = cut.splits;
+    hipError_t e;
+    const bool e4m3 = w.format == ZR_CKPT_E4M3;
+    if (w.dy_dt == ZR_BF16)
+        e = e4m3 ? run<kBf16, kE4m3>(a, stream) : run<kBf16, kInt8>(a, stream);
+    else
+        e = e4m3 ? run<kFp32, kE4m3>(a, stream) : run<kFp32, kInt8>(a, stream);
+    if (e != hipSuccess || a.splits == 1) return e;
+    const int64_t items = w.out * ((w.in + 1023) / 1024) + (a.db ? (w.out + 1023) / 1024 : 0);
+    wgrad_join_kernel<<<grid_for(items), kThreads, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace zr

@@ -112,6 +112,8 @@ typedef enum {
 typedef enum {
     ZR_BF16 = 0,
     ZR_FP32 = 1,
+    ZR_CKPT_E4M3 = 2, /* 8-bit activation checkpoints: only the norm and checkpoint */
+    ZR_CKPT_INT8 = 3, /* calls below take these */
     ZR_DTYPE_MIN_ = -2147483647 - 1,
     ZR_DTYPE_MAX_ = 2147483647
 } zr_dtype;
@@ -544,6 +546,127 @@ zr_status zr_pf_destroy(zr_pf* pf);
  * counters (peak live elements, arena peak, ...). Uses only the sizes, the
  * trace, the caps and arena_numel of cfg; pointers and streams may be NULL. */
 zr_status zr_pf_plan(const zr_pf_config* cfg, int iterations, zr_pf_stats* out);
+
+/* ------------------------------------- layer norm and 8-bit checkpoints
+ * The operators of a rank's forward and backward pass whose weight gradients
+ * land where the reduction reads them: dweight, dbias and dw are plain
+ * element-aligned addresses, so a rank's flat gradient (or a fragment) at a
+ * parameter's offset serves, and ZR_ACCUMULATE adds a later micro-step into it.
+ *
+ * A rows x cols tensor is row-major with a row stride ld >= cols (elements);
+ * rows and elements need only element alignment (16-byte rows are fastest).
+ * 0 <= rows, 1 <= cols <= 2^30, rows * (ld rounded up to 32) <= 2^40.
+ *
+ * An 8-bit activation checkpoint holds a rows x cols tensor in one buffer of
+ * zr_ckpt_bytes(rows, cols) bytes, 16-byte aligned: the codes, rows of
+ * P = 32 * ceil(cols / 32) bytes, and behind them the exponents, rows of
+ * P / 32 bytes. Columns 32k .. 32k + 31 of a row are a block with one exponent
+ * byte 127 + e; a code's value is its e4m3 (ZR_CKPT_E4M3: 448 at most, codes
+ * 0x7F and 0xFF are not written) or two's complement (ZR_CKPT_INT8) value
+ * times 2^e, where e is the smallest integer >= -124 with
+ * max|x| <= M * 2^e, M = 448 or 127. Codes are rounded to nearest, ties to
+ * even, from the exact x * 2^-e; padding codes are 0. So |held - x| is at most
+ * max(2^-4 |x|, 2^(e-10)) in e4m3 and 2^(e-1) in int8, and every held value is
+ * exact in bf16. A block with a NaN or an infinity has exponent byte 255 and
+ * decodes to NaN throughout. Values that would round past the largest finite
+ * fp32 keep the largest held one below it. e4m3 keeps the sign of a zero.
+ *
+ * Results do not change from run to run (no atomics), and the calls enqueue
+ * kernels only, so they can be captured. */
+
+/* Bytes of a checkpoint; 0 for sizes out of range. Host only. */
+size_t zr_ckpt_bytes(int64_t rows, int64_t cols);
+
+/* x (dt ZR_BF16 or ZR_FP32, row stride ld) into a checkpoint and back;
+ * format ZR_CKPT_E4M3 or ZR_CKPT_INT8. Unpacking to bf16 is exact. The
+ * buffers must not overlap (ZR_ERR_ALIAS). */
+zr_status zr_ckpt_pack(const void* x, zr_dtype dt, int64_t rows, int64_t cols, int64_t ld,
+                       void* ckpt, zr_dtype format, void* stream);
+zr_status zr_ckpt_unpack(const void* ckpt, zr_dtype format, int64_t rows, int64_t cols, void* x,
+                         zr_dtype dt, int64_t ld, void* stream);
+
+/*
+ * Layer norm, forward. For every row:
+ *     mean = sum(x) / cols, var = sum((x - mean)^2) / cols,
+ *     rstd = 1 / sqrt(var + eps), y = (x - mean) * rstd * weight + bias
+ * in fp32, rounded once to y's type.
+ *
+ *  x          x_dt ZR_BF16 or ZR_FP32 with row stride ld_x, or a checkpoint
+ *             (x_dt its format; ld_x ignored): the recomputation of a
+ *             checkpointed forward pass
+ *  weight, bias   cols elements of param_dt (ZR_BF16 or ZR_FP32), or NULL (1, 0)
+ *  eps        >= 0, finite
+ *  y          y_dt ZR_BF16 or ZR_FP32, row stride ld_y; or NULL
+ *  mean, rstd fp32, rows elements; each may be NULL
+ *  ckpt_x     NULL, or a checkpoint that receives x (x not itself one)
+ *  ckpt_y     NULL, or a checkpoint that receives y as rounded to y_dt
+ *             (with y NULL too): the input of the linear layer behind the norm
+ *  ckpt_format    of ckpt_x and ckpt_y
+ * At least one output; outputs overlap neither each other nor an input, but
+ * y may be x (same address, type and row stride).
+ */
+zr_status zr_layernorm_fwd(const void* x, zr_dtype x_dt, int64_t rows, int64_t cols, int64_t ld_x,
+                           const void* weight, const void* bias, zr_dtype param_dt, float eps,
+                           void* y, zr_dtype y_dt, int64_t ld_y, float* mean, float* rstd,
+                           void* ckpt_x, void* ckpt_y, zr_dtype ckpt_format, void* stream);
+
+/* Bytes of workspace of zr_layernorm_bwd for dweight or dbias (none without
+ * them); 0 for sizes out of range. Host only. */
+size_t zr_layernorm_workspace_bytes(int64_t rows, int64_t cols);
+
+#define ZR_ADD_DX 4 /* dx = old dx + the norm's */
+
+/*
+ * Layer norm, backward. With xh = (x - mean) * rstd and g = dy * weight:
+ *     dx      = rstd * (g - sum(g) / cols - xh * sum(g * xh) / cols)
+ *     dweight = sum over rows of dy * xh, dbias = sum over rows of dy
+ * in fp32, each rounded once to its type.
+ *
+ *  dy, x      dy_dt ZR_BF16 or ZR_FP32; x as in the forward pass (values or a
+ *             checkpoint)
+ *  mean, rstd fp32, rows elements, of the forward pass
+ *  dx         dx_dt ZR_BF16 or ZR_FP32, or NULL. dx may be dy or x (same
+ *             address, type and row stride)
+ *  dweight, dbias   cols elements of grad_dt; each may be NULL
+ *  flags      ZR_ACCUMULATE: dweight and dbias are added to (old + new in
+ *             fp32); ZR_ADD_DX: dx is added to, as where a residual stream's
+ *             gradient passes by the norm
+ *  workspace  4-byte aligned, zr_layernorm_workspace_bytes(rows, cols) bytes,
+ *             if dweight or dbias is given (ZR_ERR_WORKSPACE). Calls on one
+ *             stream may share it; calls, or captured graphs, that may run at
+ *             the same time must not
+ * rows == 0: dx is untouched, dweight and dbias become 0 (or stay).
+ */
+zr_status zr_layernorm_bwd(const void* dy, zr_dtype dy_dt, int64_t ld_dy, const void* x, zr_dtype x_dt,
+                           int64_t ld_x, int64_t rows, int64_t cols, const void* weight,
+                           zr_dtype param_dt, const float* mean, const float* rstd, void* dx,
+                           zr_dtype dx_dt, int64_t ld_dx, void* dweight, void* dbias,
+                           zr_dtype grad_dt, int flags, void* workspace, size_t ws_bytes,
+                           void* stream);
+
+/* Bytes of workspace of zr_ckpt_wgrad (0: none needed, or sizes out of
+ * range). Host only. */
+size_t zr_ckpt_wgrad_workspace_bytes(int64_t rows, int64_t out_cols, int64_t in_cols);
+
+/*
+ * Gradients of a linear layer y = x W^T + b from the checkpoint of its input:
+ *     dw[o, i] = sum over rows of dy[t, o] * x[t, i], dbias[o] = sum of dy[t, o]
+ * with exact products (x is held exactly in bf16; fp32 dy is taken in three
+ * bf16 terms) summed in fp32 on the matrix units, each rounded once to grad_dt.
+ *
+ *  dy         rows x out_cols, dy_dt ZR_BF16 or ZR_FP32, row stride ld_dy
+ *  ckpt       checkpoint of the rows x in_cols input
+ *  dw         out_cols x in_cols, grad_dt ZR_FP32 or ZR_BF16, row stride ld_dw
+ *  dbias      out_cols elements of grad_dt, or NULL
+ *  flags      ZR_ACCUMULATE: dw and dbias are added to (old + new in fp32)
+ *  workspace  4-byte aligned, zr_ckpt_wgrad_workspace_bytes bytes (NULL where
+ *             that is 0); shared as zr_layernorm_bwd's
+ * out_cols, in_cols in [1, 2^30]. rows == 0: dw and dbias become 0 (or stay).
+ */
+zr_status zr_ckpt_wgrad(const void* dy, zr_dtype dy_dt, int64_t ld_dy, const void* ckpt, zr_dtype format,
+                        int64_t rows, int64_t out_cols, int64_t in_cols, void* dw, zr_dtype grad_dt,
+                        int64_t ld_dw, void* dbias, int flags, void* workspace, size_t ws_bytes,
+                        void* stream);
 
 #ifdef __cplusplus
 }
