@@ -38,7 +38,7 @@ FLAGS = [f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-ffp-contract=
 # (its largest share), so the slowest units build in parallel.
 SOURCES = ["zr_rsf_bf16_f32.hip", "zr_rsf_bf16_bf16.hip", "zr_rsf_f32_f32.hip", "zr_rsf_f32_bf16.hip",
            "zr_rs.hip", "zr_ar.hip", "zr_rsf.hip", "zr_ag.hip", "zr_flatten.hip", "zr_wgrad.hip",
-           "zr_norm.hip", "zr_ckpt.hip", "zr_abi.cpp", "zr_sched.cpp",
+           "zr_norm_bwd.hip", "zr_norm_fwd.hip", "zr_ckpt.hip", "zr_abi.cpp", "zr_sched.cpp",
            "zr_prefetch.cpp", "zr_cost.cpp"]
 
 

@@ -32,6 +32,8 @@ __host__ __device__ __forceinline__ int64_t ckpt_pitch(int64_t cols) {
 }
 
 typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 // The same vectors at element alignment: rows of any stride and base are read
 // and written with wide accesses (gfx950 allows them at any alignment).
 typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
@@ -92,20 +94,33 @@ __device__ __forceinline__ u32x2 ckpt_encode8(const float f[8], uint32_t s, bool
     return q;
 }
 
-// Values of 8 codes of a block with scale 2^e.
+// 8 codes as the values they have at scale 1.
 template <int FMT>
-__device__ __forceinline__ void ckpt_decode8(const u32x2& q, float scale, float f[8]) {
+__device__ __forceinline__ void ckpt_codes8(const u32x2& q, float f[8]) {
     if constexpr (FMT == kE4m3) {
         const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(q.x, false), b = __builtin_amdgcn_cvt_pk_f32_fp8(q.x, true);
         const f32x2 c = __builtin_amdgcn_cvt_pk_f32_fp8(q.y, false), d = __builtin_amdgcn_cvt_pk_f32_fp8(q.y, true);
-        const float t[8] = {a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = t[e] * scale;
+        f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y;
+        f[4] = c.x; f[5] = c.y; f[6] = d.x; f[7] = d.y;
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            f[e] = (float)(int)(int8_t)((e < 4 ? q.x : q.y) >> (8 * (e & 3))) * scale;
+        for (int e = 0; e < 8; ++e) f[e] = (float)(int)(int8_t)((e < 4 ? q.x : q.y) >> (8 * (e & 3)));
     }
+}
+
+// Values of 8 codes of a block with scale 2^e.
+template <int FMT>
+__device__ __forceinline__ void ckpt_decode8(const u32x2& q, float scale, float f[8]) {
+    ckpt_codes8<FMT>(q, f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] *= scale;
+}
+
+// Two values rounded to bf16 (nearest even; a NaN stays one), the first in the
+// low half: one v_cvt_pk_bf16_f32.
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+    const bf16x2 r = {(__bf16)a, (__bf16)b};
+    return __builtin_bit_cast(uint32_t, r);
 }
 
 // ------------------------------------------------------------ row vectors
@@ -221,7 +236,7 @@ __device__ __forceinline__ void store8(char* row, int dt, int c, int n, const fl
         uint16_t* p = (uint16_t*)row + c;
         uint32_t w[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = bf16_round(f[2 * e]) | (bf16_round(f[2 * e + 1]) << 16);
+        for (int e = 0; e < 4; ++e) w[e] = bf16_pair(f[2 * e], f[2 * e + 1]);
         if (n == 8) {
             *(u32x4_a2*)p = u32x4{w[0], w[1], w[2], w[3]};
         } else {
