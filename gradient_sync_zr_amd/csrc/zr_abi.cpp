@@ -1146,7 +1146,9 @@ size_t zr_ckpt_wgrad_workspace_bytes(int64_t rows, int64_t out_cols, int64_t in_
     if (out_cols < 1 || out_cols > kMaxCols || in_cols < 1 || in_cols > kMaxCols || !size_valid(rows, out_cols) ||
         !size_valid(rows, in_cols) || !size_valid(out_cols, in_cols))
         return 0;
-    const int splits = wgrad_cut(rows, out_cols, in_cols).splits;
+    // either form may be taken: by dy's type and alignment, which this call does not know
+    int splits = wgrad_cut(rows, out_cols, in_cols, false).splits;
+    if (wgrad_big(rows, out_cols, in_cols)) splits = std::max(splits, wgrad_cut(rows, out_cols, in_cols, true).splits);
     return splits > 1 ? (size_t)splits * (size_t)(out_cols * in_cols + out_cols) * sizeof(float) : 0;
 }
 

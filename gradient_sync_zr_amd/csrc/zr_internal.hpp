@@ -210,15 +210,19 @@ ZR_KERNELS hipError_t launch_ckpt_unpack(const void* ckpt, zr_dtype fmt, int64_t
 
 // How a weight gradient is cut: tiles of dW, one per block, and parts that the
 // sum over rows is split into (each of `span` rows) where the tiles alone do
-// not fill the chip's 512 places (two blocks per CU).
-constexpr int kWgradTile = 128;
+// not fill the chip's places (two blocks per CU, or one of the large form).
+constexpr int kWgradTile = 128, kWgradBig = 256;
+inline bool wgrad_big(int64_t rows, int64_t out, int64_t in) {
+    return rows >= 512 && out > kWgradTile && in > kWgradTile && out * in >= (int64_t)1 << 21;
+}
 struct WgradCut {
     int splits;
     int64_t span;
 };
-inline WgradCut wgrad_cut(int64_t rows, int64_t out, int64_t in) {
-    const int64_t tiles = ((out + kWgradTile - 1) / kWgradTile) * ((in + kWgradTile - 1) / kWgradTile);
-    int64_t splits = 512 / tiles;
+inline WgradCut wgrad_cut(int64_t rows, int64_t out, int64_t in, bool big) {
+    const int64_t tile = big ? kWgradBig : kWgradTile;
+    const int64_t tiles = ((out + tile - 1) / tile) * ((in + tile - 1) / tile);
+    int64_t splits = (big ? 256 : 512) / tiles;
     const int64_t most = rows / 128;  // a part is two slabs of rows at least
     if (splits > most) splits = most;
     if (splits > 64) splits = 64;

@@ -293,6 +293,202 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void wgrad_kernel(Wgrad
     }
 }
 
+// The large form, for bf16 dY in rows of whole, aligned 16-byte chunks: tiles
+// of 256 x 256, eight waves of 128 x 64. A slab of 64 rows costs a CU 2,061
+// cycles of matrix units and reads 192 KB from LDS (1,536 cycles at 128 bytes
+// a cycle) where four tiles of 128 x 128 would read 256 KB. Each wave's 128
+// fp32 accumulators leave 128 registers for operands and the next slab.
+constexpr int kBigThreads = 512, kBigBK = 64;
+
+template <int FMT>
+__global__ __launch_bounds__(kBigThreads) void wgrad_big_kernel(WgradArgs a) {
+    constexpr int BM = kWgradBig, BN = kWgradBig, WM = 128, WN = 64, BK = kBigBK, T = kBigThreads;
+    constexpr int PA = BM * 2, PB = BN * 2;
+    constexpr int MT = WM / 32, NT = WN / 32;
+    constexpr int SA = BK * PA, SB = BK * PB, STAGE = SA + SB;
+    constexpr int RA = T / (BM / 8), RB = T / (BN / 16);  // rows that one round of loads covers
+    constexpr int NA = BK / RA, NB = BK / RB;
+    __shared__ __attribute__((aligned(1024))) char lds[2 * STAGE];
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int wm = wave / (BN / WN), wn = wave % (BN / WN);
+    const int64_t total = (int64_t)a.tiles_m * a.tiles_n * a.splits;
+    const int r4 = (lane >> 2) & 3, rbase = (lane >> 5) * 8 + r4;
+    const int low = rbase * PA + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;  // PA == PB
+    int offA[MT], offB[NT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) offA[m] = low + (((wm * WM + m * 32) * 2) ^ (r4 << 6));
+#pragma unroll
+    for (int n = 0; n < NT; ++n) offB[n] = SA + low + (((wn * WN + n * 32) * 2) ^ (r4 << 6));
+    // where this thread's chunks go; rows of a round are a multiple of 4 apart
+    const int ta = tid / (BM / 8), ca = tid % (BM / 8), tb = tid / (BN / 16), cb = tid % (BN / 16);
+    const int putA = ta * PA + ((ca * 16) ^ ((ta & 3) << 6));
+    const int putB = SA + tb * PB + ((cb * 32) ^ ((tb & 3) << 6)), putB2 = SA + tb * PB + ((cb * 32 + 16) ^ ((tb & 3) << 6));
+    const int64_t sp = a.pitch / kCkptBlock;
+
+    for (int64_t item = blockIdx.x; item < total; item += gridDim.x) {
+        int tm, tn, part;
+        item_place(a, item, total, &tm, &tn, &part);
+        const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
+        const int64_t kb = part * a.span, ke = kb + a.span < a.rows ? kb + a.span : a.rows;
+        const bool bias = a.db && tn == 0;
+        // columns behind the last are read from the last chunk and not stored
+        const int64_t col_a = m0 + ca * 8 < a.out ? m0 + ca * 8 : a.out - 8;
+        const int64_t col_b = n0 + cb * 16 < a.pitch ? n0 + cb * 16 : a.pitch - 16;
+        const uint32_t va = (uint32_t)((ta * a.ld_dy + col_a - m0) * 2);
+        const uint32_t vb = (uint32_t)(tb * a.pitch + col_b - n0);
+        const uint32_t vs = (uint32_t)(tb * sp + (col_b - n0) / kCkptBlock);
+        const char* pa = (const char*)a.dy + (kb * a.ld_dy + m0) * 2;
+        const char* pb = a.codes + kb * a.pitch + n0;
+        const uint8_t* ps = a.scales + kb * sp + n0 / kCkptBlock;
+
+        f32x16 acc[MT][NT];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) acc[m][n][e] = 0.0f;
+        float sums[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        u32x4 ra[NA], rb[NB];
+        uint32_t rs[NB];
+        auto fetch = [&](int left) {  // the slab at pa, pb, ps, of which `left` rows exist
+            if (left >= BK) {
+#pragma unroll
+                for (int j = 0; j < NA; ++j) ra[j] = *(const u32x4*)(pa + (int64_t)(j * RA) * a.ld_dy * 2 + va);
+#pragma unroll
+                for (int j = 0; j < NB; ++j) {
+                    rb[j] = *(const u32x4*)(pb + (int64_t)(j * RB) * a.pitch + vb);
+                    rs[j] = *(ps + (int64_t)(j * RB) * sp + vs);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < NA; ++j) {
+                    ra[j] = u32x4{0, 0, 0, 0};
+                    if (ta + j * RA < left) ra[j] = *(const u32x4*)(pa + (int64_t)(j * RA) * a.ld_dy * 2 + va);
+                }
+#pragma unroll
+                for (int j = 0; j < NB; ++j) {
+                    rb[j] = u32x4{0, 0, 0, 0};
+                    rs[j] = 127;
+                    if (tb + j * RB < left) {
+                        rb[j] = *(const u32x4*)(pb + (int64_t)(j * RB) * a.pitch + vb);
+                        rs[j] = *(ps + (int64_t)(j * RB) * sp + vs);
+                    }
+                }
+            }
+            pa += (int64_t)BK * a.ld_dy * 2;
+            pb += (int64_t)BK * a.pitch;
+            ps += (int64_t)BK * sp;
+        };
+        auto stage = [&](char* buf) {
+#pragma unroll
+            for (int j = 0; j < NA; ++j) {
+                *(u32x4*)(buf + putA + j * RA * PA) = ra[j];
+                if (bias) {
+                    float f[8];
+                    widen8(Raw8<kBf16>{ra[j]}, f);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) sums[e] += f[e];
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+                uint32_t w[8];
+                decode16<FMT>(rb[j], rs[j], w);
+                *(u32x4*)(buf + putB + j * RB * PB) = u32x4{w[0], w[1], w[2], w[3]};
+                *(u32x4*)(buf + putB2 + j * RB * PB) = u32x4{w[4], w[5], w[6], w[7]};
+            }
+        };
+        auto operand = [&](const char* at) {
+            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)at);
+            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(at + 4 * PA));
+            return __builtin_bit_cast(bf16x8, (s16x8)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        };
+        auto multiply = [&](const char* buf, int k) {  // 16 rows of a slab
+            bf16x8 fa[MT], fb[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) fb[n] = operand(buf + offB[n] + k * PB);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) fa[m] = operand(buf + offA[m] + k * PA);
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[m], fb[n], acc[m][n], 0, 0, 0);
+        };
+
+        if (kb < ke) {
+            int left = (int)(ke - kb < (1 << 30) ? ke - kb : 1 << 30);
+            fetch(left);
+            stage(lds);
+            __syncthreads();
+            int cur = 0;
+            for (int64_t k = kb; k < ke; k += BK) {
+                const int64_t rest = ke - k - BK;
+                const char* buf = lds + cur * STAGE;
+                if (rest > 0) fetch((int)(rest < (1 << 30) ? rest : 1 << 30));
+                multiply(buf, 0);
+                multiply(buf, 16);
+                multiply(buf, 32);
+                if (rest > 0) stage(lds + (cur ^ 1) * STAGE);
+                multiply(buf, 48);
+                __syncthreads();
+                cur ^= 1;
+            }
+        }
+
+        // D's layout: lane & 31 is the column, element e the row
+        // (e / 4) * 8 + (lane / 32) * 4 + e % 4.
+        float* const mine = a.splits > 1 ? a.part + (int64_t)part * (a.out * a.in + a.out) : nullptr;
+        const int es = !mine && a.grad_dt == kBf16 ? 2 : 4;
+        const int64_t ld = mine ? a.in : a.ld_dw;
+        char* const base = (mine ? (char*)mine : (char*)a.dw) + ((m0 + wm * WM) * ld + n0 + wn * WN) * es;
+        const int64_t o0 = a.out - m0 - wm * WM - (lane >> 5) * 4, i0 = a.in - n0 - wn * WN - (lane & 31);
+        const int64_t vo = ((lane >> 5) * 4 * ld + (lane & 31)) * es;
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int o = m * 32 + (e >> 2) * 8 + (e & 3);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    if (o >= o0 || n * 32 >= i0) continue;
+                    char* const p = base + (o * ld + n * 32) * es + vo;
+                    const float v = acc[m][n][e];
+                    if (es == 2)
+                        store_elem((uint16_t*)p, a.accumulate ? load_elem((uint16_t*)p) + v : v);
+                    else
+                        store_elem((float*)p, a.accumulate && !mine ? load_elem((float*)p) + v : v);
+                }
+            }
+        if (bias) {  // the threads that hold the same 8 columns
+            float* s = (float*)lds;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[ta * BM + ca * 8 + e] = sums[e];
+            __syncthreads();
+            if (tid < BM) {
+                float v = 0.0f;
+#pragma unroll
+                for (int r = 0; r < RA; ++r) v += s[r * BM + tid];
+                const int64_t o = m0 + tid;
+                if (o < a.out) {
+                    if (mine) {
+                        mine[a.out * a.in + o] = v;
+                    } else if (a.grad_dt == kBf16) {
+                        uint16_t* p = (uint16_t*)a.db + o;
+                        store_elem(p, a.accumulate ? load_elem(p) + v : v);
+                    } else {
+                        float* p = (float*)a.db + o;
+                        store_elem(p, a.accumulate ? load_elem(p) + v : v);
+                    }
+                }
+            }
+            __syncthreads();
+        }
+    }
+}
+
 // Sums the parts, in order. Items are runs of 1024 columns of a row of dW,
 // and after them runs of db.
 __global__ __launch_bounds__(kThreads) void wgrad_join_kernel(WgradArgs a) {
@@ -319,17 +515,23 @@ __global__ __launch_bounds__(kThreads) void wgrad_join_kernel(WgradArgs a) {
 }
 
 template <int DD, int FMT>
-hipError_t run(const WgradArgs& a, hipStream_t stream) {
+hipError_t run(const WgradArgs& a, bool big, hipStream_t stream) {
     const int64_t total = (int64_t)a.tiles_m * a.tiles_n * a.splits;
     const int grid = grid_for(total);
-    wgrad_kernel<DD, FMT, kWgradTile, kWgradTile, 64, 64, DD == kBf16 ? 64 : 32><<<grid, 256, 0, stream>>>(a);
+    if (DD == kBf16 && big)
+        wgrad_big_kernel<FMT><<<grid, kBigThreads, 0, stream>>>(a);
+    else
+        wgrad_kernel<DD, FMT, kWgradTile, kWgradTile, 64, 64, DD == kBf16 ? 64 : 32><<<grid, 256, 0, stream>>>(a);
     return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_ckpt_wgrad(const Wgrad& w, hipStream_t stream) {
-    const WgradCut cut = wgrad_cut(w.rows, w.out, w.in);
+    const bool big = wgrad_big(w.rows, w.out, w.in) && w.dy_dt == ZR_BF16 && w.out % 8 == 0 && w.ld_dy % 8 == 0 &&
+                     ((uintptr_t)w.dy & 15) == 0 && w.ld_dy <= (1 << 26) && w.in <= (1 << 26);
+    const int tile = big ? kWgradBig : kWgradTile;
+    const WgradCut cut = wgrad_cut(w.rows, w.out, w.in, big);
     WgradArgs a{};
     a.dy = w.dy;
     a.pitch = ckpt_pitch(w.in);
@@ -341,15 +543,15 @@ hipError_t launch_ckpt_wgrad(const Wgrad& w, hipStream_t stream) {
     a.rows = w.rows; a.out = w.out; a.in = w.in; a.ld_dy = w.ld_dy; a.ld_dw = w.ld_dw;
     a.span = cut.span;
     a.grad_dt = w.grad_dt; a.accumulate = w.accumulate;
-    a.tiles_m = (int)((w.out + kWgradTile - 1) / kWgradTile);
-    a.tiles_n = (int)((w.in + kWgradTile - 1) / kWgradTile);
+    a.tiles_m = (int)((w.out + tile - 1) / tile);
+    a.tiles_n = (int)((w.in + tile - 1) / tile);
     a.splits = cut.splits;
     hipError_t e;
     const bool e4m3 = w.format == ZR_CKPT_E4M3;
     if (w.dy_dt == ZR_BF16)
-        e = e4m3 ? run<kBf16, kE4m3>(a, stream) : run<kBf16, kInt8>(a, stream);
+        e = e4m3 ? run<kBf16, kE4m3>(a, big, stream) : run<kBf16, kInt8>(a, big, stream);
     else
-        e = e4m3 ? run<kFp32, kE4m3>(a, stream) : run<kFp32, kInt8>(a, stream);
+        e = e4m3 ? run<kFp32, kE4m3>(a, false, stream) : run<kFp32, kInt8>(a, false, stream);
     if (e != hipSuccess || a.splits == 1) return e;
     const int64_t items = w.out * ((w.in + 1023) / 1024) + (a.db ? (w.out + 1023) / 1024 : 0);
     wgrad_join_kernel<<<grid_for(items), kThreads, 0, stream>>>(a);

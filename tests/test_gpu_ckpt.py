@@ -196,6 +196,25 @@ def test_wgrad_exact_on_integers(rows, out, inn, dy_dt, fmt):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("rows,out,inn", [(512, 1448, 1450), (577, 136, 16384), (2111, 8200, 264), (4160, 2056, 1090)])
+def test_wgrad_exact_on_integers_large(rows, out, inn, fmt):
+    """The large form (rows of whole 16-byte chunks), with ragged last tiles, slabs and parts; and the same
+    sizes with rows that are not, which take the small one."""
+    rng = np.random.default_rng(rows)
+    dy = rng.integers(-4, 5, (rows, out)).astype(np.float32)
+    x = rng.integers(-8, 9, (rows, inn)).astype(np.float32)
+    want = dy.astype(np.float64).T @ x.astype(np.float64)
+    old = rng.integers(-50, 50, (out, inn)).astype(np.float32)
+    for gaps, grad_dt, add in (((0, 0), "fp32", False), ((8, 3), "fp32", True), ((1, 0), "fp32", True), ((0, 5), "bf16", True)):
+        w, b = run_wgrad(dy, x, fmt, "bf16", grad_dt, True, old if add else None, old[:, 0].copy() if add else None, gaps)
+        exp_w, exp_b = want + (old if add else 0), dy.astype(np.float64).sum(0) + (old[:, 0] if add else 0)
+        if grad_dt == "bf16":
+            assert (np.abs(w - exp_w) <= 2.0 ** -8 * np.abs(exp_w)).all() and (np.abs(b - exp_b) <= 2.0 ** -8 * np.abs(exp_b)).all()
+        else:
+            assert np.array_equal(w, exp_w) and np.array_equal(b, exp_b)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("dy_dt,grad_dt", [("bf16", "fp32"), ("bf16", "bf16"), ("fp32", "fp32"), ("fp32", "bf16")])
 @pytest.mark.parametrize("rows,out,inn", [(37, 70, 100), (600, 264, 300), (1100, 130, 33)])
 def test_wgrad_values(rows, out, inn, dy_dt, grad_dt, fmt):
