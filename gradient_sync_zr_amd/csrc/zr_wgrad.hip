@@ -300,6 +300,30 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void wgrad_kernel(Wgrad
 // fp32 accumulators leave 128 registers for operands and the next slab.
 constexpr int kBigThreads = 512, kBigBK = 64;
 
+// A wave's accumulators to dW (or the workspace), all of them inside it; `at`
+// is this lane's first element.
+template <typename E, int MT, int NT>
+__device__ __forceinline__ void put_tile(const f32x16 (&acc)[MT][NT], E* at, int64_t ld, bool add) {
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            float old[16];
+            if (add) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) old[e] = load_elem(at + (m * 32 + (e >> 2) * 8 + (e & 3)) * ld + n * 32);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) old[e] = 0.0f;
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                store_elem(at + (m * 32 + (e >> 2) * 8 + (e & 3)) * ld + n * 32, acc[m][n][e] + old[e]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+}
+
 template <int FMT>
 __global__ __launch_bounds__(kBigThreads) void wgrad_big_kernel(WgradArgs a) {
     constexpr int BM = kWgradBig, BN = kWgradBig, WM = 128, WN = 64, BK = kBigBK, T = kBigThreads;
@@ -310,7 +334,7 @@ __global__ __launch_bounds__(kBigThreads) void wgrad_big_kernel(WgradArgs a) {
     constexpr int NA = BK / RA, NB = BK / RB;
     __shared__ __attribute__((aligned(1024))) char lds[2 * STAGE];
 
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / (BN / WN), wn = wave % (BN / WN);
     const int64_t total = (int64_t)a.tiles_m * a.tiles_n * a.splits;
     const int r4 = (lane >> 2) & 3, rbase = (lane >> 5) * 8 + r4;
@@ -335,9 +359,8 @@ __global__ __launch_bounds__(kBigThreads) void wgrad_big_kernel(WgradArgs a) {
         // columns behind the last are read from the last chunk and not stored
         const int64_t col_a = m0 + ca * 8 < a.out ? m0 + ca * 8 : a.out - 8;
         const int64_t col_b = n0 + cb * 16 < a.pitch ? n0 + cb * 16 : a.pitch - 16;
-        const uint32_t va = (uint32_t)((ta * a.ld_dy + col_a - m0) * 2);
-        const uint32_t vb = (uint32_t)(tb * a.pitch + col_b - n0);
-        const uint32_t vs = (uint32_t)(tb * sp + (col_b - n0) / kCkptBlock);
+        const uint32_t va = (uint32_t)(col_a - m0) * 2, vb = (uint32_t)(col_b - n0), vs = vb / kCkptBlock;
+        const uint32_t la = (uint32_t)a.ld_dy * 2, lb = (uint32_t)a.pitch, ls = (uint32_t)sp;
         const char* pa = (const char*)a.dy + (kb * a.ld_dy + m0) * 2;
         const char* pb = a.codes + kb * a.pitch + n0;
         const uint8_t* ps = a.scales + kb * sp + n0 / kCkptBlock;
@@ -349,93 +372,104 @@ __global__ __launch_bounds__(kBigThreads) void wgrad_big_kernel(WgradArgs a) {
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) acc[m][n][e] = 0.0f;
-        float sums[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        float sum0 = 0.0f, sum1 = 0.0f;  // bias: two columns over a quarter of a slab's rows
         u32x4 ra[NA], rb[NB];
         uint32_t rs[NB];
-        auto fetch = [&](int left) {  // the slab at pa, pb, ps, of which `left` rows exist
-            if (left >= BK) {
+        // Rows behind the last are read from it, and staged as zeros.
+        int64_t left = ke - kb;  // rows from the next slab on
+        int have = 0;            // rows of the slab in the registers
+        auto fetch = [&] {
+            have = left < BK ? (int)left : BK;
 #pragma unroll
-                for (int j = 0; j < NA; ++j) ra[j] = *(const u32x4*)(pa + (int64_t)(j * RA) * a.ld_dy * 2 + va);
+            for (int j = 0; j < NA; ++j) {
+                const int t = ta + j * RA < have ? ta + j * RA : have - 1;
+                ra[j] = *(const u32x4*)(pa + ((uint32_t)t * la + va));
+            }
 #pragma unroll
-                for (int j = 0; j < NB; ++j) {
-                    rb[j] = *(const u32x4*)(pb + (int64_t)(j * RB) * a.pitch + vb);
-                    rs[j] = *(ps + (int64_t)(j * RB) * sp + vs);
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < NA; ++j) {
-                    ra[j] = u32x4{0, 0, 0, 0};
-                    if (ta + j * RA < left) ra[j] = *(const u32x4*)(pa + (int64_t)(j * RA) * a.ld_dy * 2 + va);
-                }
-#pragma unroll
-                for (int j = 0; j < NB; ++j) {
-                    rb[j] = u32x4{0, 0, 0, 0};
-                    rs[j] = 127;
-                    if (tb + j * RB < left) {
-                        rb[j] = *(const u32x4*)(pb + (int64_t)(j * RB) * a.pitch + vb);
-                        rs[j] = *(ps + (int64_t)(j * RB) * sp + vs);
-                    }
-                }
+            for (int j = 0; j < NB; ++j) {
+                const int t = tb + j * RB < have ? tb + j * RB : have - 1;
+                rb[j] = *(const u32x4*)(pb + ((uint32_t)t * lb + vb));
+                rs[j] = *(ps + ((uint32_t)t * ls + vs));
             }
             pa += (int64_t)BK * a.ld_dy * 2;
             pb += (int64_t)BK * a.pitch;
             ps += (int64_t)BK * sp;
+            left -= BK;
         };
-        auto stage = [&](char* buf) {
-#pragma unroll
-            for (int j = 0; j < NA; ++j) {
-                *(u32x4*)(buf + putA + j * RA * PA) = ra[j];
-                if (bias) {
-                    float f[8];
-                    widen8(Raw8<kBf16>{ra[j]}, f);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) sums[e] += f[e];
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < NB; ++j) {
-                uint32_t w[8];
-                decode16<FMT>(rb[j], rs[j], w);
-                *(u32x4*)(buf + putB + j * RB * PB) = u32x4{w[0], w[1], w[2], w[3]};
-                *(u32x4*)(buf + putB2 + j * RB * PB) = u32x4{w[4], w[5], w[6], w[7]};
-            }
+        auto put_a = [&](char* buf, int j) {
+            *(u32x4*)(buf + putA + j * RA * PA) = ta + j * RA < have ? ra[j] : u32x4{0, 0, 0, 0};
+        };
+        auto put_b = [&](char* buf, int j) {
+            uint32_t w[8];
+            const bool here = tb + j * RB < have;
+            decode16<FMT>(here ? rb[j] : u32x4{0, 0, 0, 0}, here ? rs[j] : 127u, w);
+            *(u32x4*)(buf + putB + j * RB * PB) = u32x4{w[0], w[1], w[2], w[3]};
+            *(u32x4*)(buf + putB2 + j * RB * PB) = u32x4{w[4], w[5], w[6], w[7]};
         };
         auto operand = [&](const char* at) {
             const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)at);
             const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(at + 4 * PA));
             return __builtin_bit_cast(bf16x8, (s16x8)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
         };
-        auto multiply = [&](const char* buf, int k) {  // 16 rows of a slab
-            bf16x8 fa[MT], fb[NT];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) fb[n] = operand(buf + offB[n] + k * PB);
-#pragma unroll
-            for (int m = 0; m < MT; ++m) fa[m] = operand(buf + offA[m] + k * PA);
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-                    acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[m], fb[n], acc[m][n], 0, 0, 0);
-        };
-
         if (kb < ke) {
-            int left = (int)(ke - kb < (1 << 30) ? ke - kb : 1 << 30);
-            fetch(left);
-            stage(lds);
+            const int slabs = (int)((ke - kb + BK - 1) / BK);
+            fetch();
+#pragma unroll
+            for (int j = 0; j < NA; ++j) put_a(lds, j);
+#pragma unroll
+            for (int j = 0; j < NB; ++j) put_b(lds, j);
+            if (slabs > 1) fetch();
             __syncthreads();
+            // A slab is 16 steps: 16 rows at a time, 32 of the wave's 128 columns
+            // of dY in each. The operands of a step are read two steps before it
+            // (X's up to four), so that matrix instructions do not wait for LDS;
+            // the next slab goes from registers to the other buffer in steps 1 to
+            // 6, the loads of the one after it are issued in step 8, and the
+            // barrier that publishes the other buffer stands before step 14, whose
+            // reads are the first from it. Behind the last slab the other buffer
+            // holds nothing of use: it is written and read, and not multiplied.
+            bf16x8 fa[4], fb[2][NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) fb[0][n] = operand(lds + offB[n]);
+            fa[0] = operand(lds + offA[0]);
+            fa[1] = operand(lds + offA[1]);
             int cur = 0;
-            for (int64_t k = kb; k < ke; k += BK) {
-                const int64_t rest = ke - k - BK;
+#pragma unroll 1
+            for (int k = 0; k < slabs; ++k) {
                 const char* buf = lds + cur * STAGE;
-                if (rest > 0) fetch((int)(rest < (1 << 30) ? rest : 1 << 30));
-                multiply(buf, 0);
-                multiply(buf, 16);
-                multiply(buf, 32);
-                if (rest > 0) stage(lds + (cur ^ 1) * STAGE);
-                multiply(buf, 48);
-                __syncthreads();
+                char* other = lds + (cur ^ 1) * STAGE;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    if (i == 12 && bias) {
+#pragma unroll 4
+                        for (int r = 0; r < BK / 4; ++r) {
+                            const int t = (tid >> 7) * (BK / 4) + r;
+                            const uint32_t w = *(const uint32_t*)(buf + t * PA + (((tid & 127) * 4) ^ ((t & 3) << 6)));
+                            sum0 += __uint_as_float(w << 16);
+                            sum1 += __uint_as_float(w & 0xFFFF0000u);
+                        }
+                    }
+                    if (i == 14) __syncthreads();
+                    const int ahead = (i + 2) & 15;
+                    fa[ahead & 3] = operand((i < 14 ? buf : other) + offA[ahead & 3] + (ahead >> 2) * 16 * PA);
+                    if ((i & 3) == 2) {
+                        const int ks = ((i >> 2) + 1) & 3;
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            fb[ks & 1][n] = operand((i < 14 ? buf : other) + offB[n] + ks * 16 * PB);
+                    }
+                    if (i >= 1 && i < 1 + NA) put_a(other, i - 1);
+                    if (i >= 1 + NA && i < 1 + NA + NB) put_b(other, i - 1 - NA);
+                    if (i == 8 && k + 2 < slabs) fetch();
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        acc[i & 3][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i & 3], fb[(i >> 2) & 1][n],
+                                                                               acc[i & 3][n], 0, 0, 0);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
                 cur ^= 1;
             }
+            __syncthreads();
         }
 
         // D's layout: lane & 31 is the column, element e the row
@@ -446,31 +480,40 @@ __global__ __launch_bounds__(kBigThreads) void wgrad_big_kernel(WgradArgs a) {
         char* const base = (mine ? (char*)mine : (char*)a.dw) + ((m0 + wm * WM) * ld + n0 + wn * WN) * es;
         const int64_t o0 = a.out - m0 - wm * WM - (lane >> 5) * 4, i0 = a.in - n0 - wn * WN - (lane & 31);
         const int64_t vo = ((lane >> 5) * 4 * ld + (lane & 31)) * es;
+        const bool add = a.accumulate && !mine;
+        if (m0 + BM <= a.out && n0 + BN <= a.in) {  // whole tiles: old values 16 at a time
+            char* const at = base + vo;
+            if (es == 4)
+                put_tile<float>(acc, (float*)at, ld, add);
+            else
+                put_tile<uint16_t>(acc, (uint16_t*)at, ld, add);
+        } else {
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+            for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const int o = m * 32 + (e >> 2) * 8 + (e & 3);
+                for (int e = 0; e < 16; ++e) {
+                    const int o = m * 32 + (e >> 2) * 8 + (e & 3);
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    if (o >= o0 || n * 32 >= i0) continue;
-                    char* const p = base + (o * ld + n * 32) * es + vo;
-                    const float v = acc[m][n][e];
-                    if (es == 2)
-                        store_elem((uint16_t*)p, a.accumulate ? load_elem((uint16_t*)p) + v : v);
-                    else
-                        store_elem((float*)p, a.accumulate && !mine ? load_elem((float*)p) + v : v);
+                    for (int n = 0; n < NT; ++n) {
+                        if (o >= o0 || n * 32 >= i0) continue;
+                        char* const p = base + (o * ld + n * 32) * es + vo;
+                        const float v = acc[m][n][e];
+                        if (es == 2)
+                            store_elem((uint16_t*)p, add ? load_elem((uint16_t*)p) + v : v);
+                        else
+                            store_elem((float*)p, add ? load_elem((float*)p) + v : v);
+                    }
                 }
-            }
-        if (bias) {  // the threads that hold the same 8 columns
+        }
+        if (bias) {  // the four quarters of the rows
             float* s = (float*)lds;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s[ta * BM + ca * 8 + e] = sums[e];
+            s[(tid >> 7) * BM + (tid & 127) * 2] = sum0;
+            s[(tid >> 7) * BM + (tid & 127) * 2 + 1] = sum1;
             __syncthreads();
             if (tid < BM) {
                 float v = 0.0f;
 #pragma unroll
-                for (int r = 0; r < RA; ++r) v += s[r * BM + tid];
+                for (int r = 0; r < 4; ++r) v += s[r * BM + tid];
                 const int64_t o = m0 + tid;
                 if (o < a.out) {
                     if (mine) {
@@ -529,7 +572,7 @@ hipError_t run(const WgradArgs& a, bool big, hipStream_t stream) {
 
 hipError_t launch_ckpt_wgrad(const Wgrad& w, hipStream_t stream) {
     const bool big = wgrad_big(w.rows, w.out, w.in) && w.dy_dt == ZR_BF16 && w.out % 8 == 0 && w.ld_dy % 8 == 0 &&
-                     ((uintptr_t)w.dy & 15) == 0 && w.ld_dy <= (1 << 26) && w.in <= (1 << 26);
+                     ((uintptr_t)w.dy & 15) == 0 && w.ld_dy <= (1 << 24) && w.in <= (1 << 24);
     const int tile = big ? kWgradBig : kWgradTile;
     const WgradCut cut = wgrad_cut(w.rows, w.out, w.in, big);
     WgradArgs a{};
