@@ -300,6 +300,12 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void wgrad_kernel(Wgrad
 // fp32 accumulators leave 128 registers for operands and the next slab.
 constexpr int kBigThreads = 512, kBigBK = 64;
 
+// v plus the two bf16 values of a word.
+__device__ __forceinline__ float sum2(uint32_t w, float v) {
+    const bf16x2 one = {(__bf16)1.0f, (__bf16)1.0f};
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, w), one, v, false);
+}
+
 // A wave's accumulators to dW (or the workspace), all of them inside it; `at`
 // is this lane's first element.
 template <typename E, int MT, int NT>
@@ -355,7 +361,7 @@ __global__ __launch_bounds__(kBigThreads) void wgrad_big_kernel(WgradArgs a) {
         item_place(a, item, total, &tm, &tn, &part);
         const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
         const int64_t kb = part * a.span, ke = kb + a.span < a.rows ? kb + a.span : a.rows;
-        const bool bias = a.db && tn == 0;
+        const bool bias = a.db && tn == 0 && wn == 0;
         // columns behind the last are read from the last chunk and not stored
         const int64_t col_a = m0 + ca * 8 < a.out ? m0 + ca * 8 : a.out - 8;
         const int64_t col_b = n0 + cb * 16 < a.pitch ? n0 + cb * 16 : a.pitch - 16;
@@ -372,7 +378,7 @@ __global__ __launch_bounds__(kBigThreads) void wgrad_big_kernel(WgradArgs a) {
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) acc[m][n][e] = 0.0f;
-        float sum0 = 0.0f, sum1 = 0.0f;  // bias: two columns over a quarter of a slab's rows
+        float sums[MT] = {0, 0, 0, 0};  // bias: this lane's columns of dY over half of the rows
         u32x4 ra[NA], rb[NB];
         uint32_t rs[NB];
         // Rows behind the last are read from it, and staged as zeros.
@@ -440,15 +446,6 @@ __global__ __launch_bounds__(kBigThreads) void wgrad_big_kernel(WgradArgs a) {
                 char* other = lds + (cur ^ 1) * STAGE;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    if (i == 12 && bias) {
-#pragma unroll 4
-                        for (int r = 0; r < BK / 4; ++r) {
-                            const int t = (tid >> 7) * (BK / 4) + r;
-                            const uint32_t w = *(const uint32_t*)(buf + t * PA + (((tid & 127) * 4) ^ ((t & 3) << 6)));
-                            sum0 += __uint_as_float(w << 16);
-                            sum1 += __uint_as_float(w & 0xFFFF0000u);
-                        }
-                    }
                     if (i == 14) __syncthreads();
                     const int ahead = (i + 2) & 15;
                     fa[ahead & 3] = operand((i < 14 ? buf : other) + offA[ahead & 3] + (ahead >> 2) * 16 * PA);
@@ -461,6 +458,10 @@ __global__ __launch_bounds__(kBigThreads) void wgrad_big_kernel(WgradArgs a) {
                     if (i >= 1 && i < 1 + NA) put_a(other, i - 1);
                     if (i >= 1 + NA && i < 1 + NA + NB) put_b(other, i - 1 - NA);
                     if (i == 8 && k + 2 < slabs) fetch();
+                    if (bias) {
+                        const u32x4 w = __builtin_bit_cast(u32x4, fa[i & 3]);
+                        sums[i & 3] = sum2(w.x, sum2(w.y, sum2(w.z, sum2(w.w, sums[i & 3]))));
+                    }
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
                         acc[i & 3][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i & 3], fb[(i >> 2) & 1][n],
@@ -505,29 +506,22 @@ __global__ __launch_bounds__(kBigThreads) void wgrad_big_kernel(WgradArgs a) {
                     }
                 }
         }
-        if (bias) {  // the four quarters of the rows
-            float* s = (float*)lds;
-            s[(tid >> 7) * BM + (tid & 127) * 2] = sum0;
-            s[(tid >> 7) * BM + (tid & 127) * 2 + 1] = sum1;
-            __syncthreads();
-            if (tid < BM) {
-                float v = 0.0f;
+        if (bias) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) v += s[r * BM + tid];
-                const int64_t o = m0 + tid;
-                if (o < a.out) {
-                    if (mine) {
-                        mine[a.out * a.in + o] = v;
-                    } else if (a.grad_dt == kBf16) {
-                        uint16_t* p = (uint16_t*)a.db + o;
-                        store_elem(p, a.accumulate ? load_elem(p) + v : v);
-                    } else {
-                        float* p = (float*)a.db + o;
-                        store_elem(p, a.accumulate ? load_elem(p) + v : v);
-                    }
+            for (int m = 0; m < MT; ++m) {
+                const float v = sums[m] + __shfl_xor(sums[m], 32, 64);
+                const int64_t o = m0 + wm * WM + m * 32 + (lane & 31);
+                if (lane >= 32 || o >= a.out) continue;
+                if (mine) {
+                    mine[a.out * a.in + o] = v;
+                } else if (a.grad_dt == kBf16) {
+                    uint16_t* p = (uint16_t*)a.db + o;
+                    store_elem(p, a.accumulate ? load_elem(p) + v : v);
+                } else {
+                    float* p = (float*)a.db + o;
+                    store_elem(p, a.accumulate ? load_elem(p) + v : v);
                 }
             }
-            __syncthreads();
         }
     }
 }
