@@ -699,80 +699,109 @@ class Prefetcher:
 
 
 # ------------------------------------------- layer norm and 8-bit checkpoints
+_dtypes: dict = {}  # torch dtype -> zr_dtype of the real ones
+
+
+def _real(dt) -> int:
+    """zr_dtype of a torch dtype."""
+    if not _dtypes:
+        import torch
+        _dtypes.update({torch.bfloat16: ZR_BF16, torch.float32: ZR_FP32})
+    code = _dtypes.get(dt)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dt}: bfloat16 or float32")
+    return code
+
+
 def _matrix(x, rows: int, cols: int, dtype, ld, name: str):
     """(address, dtype, row stride) of a rows x cols matrix: a torch tensor of
     that shape whose rows are contiguous, or an address with its dtype (and
     row stride, if not cols)."""
     if x is None:
         return 0, ZR_BF16, cols
-    if isinstance(x, int):
+    if x.__class__ is int:
         if dtype is None:
             raise ValueError(f"{name} is an address: its dtype is needed")
         return x, _dtype(dtype), cols if ld is None else ld
-    if dtype is not None and _dtype(dtype) != _dtype(x):
+    code = _real(x.dtype)
+    if dtype is not None and _dtype(dtype) != code:
         raise ValueError(f"{name} is {x.dtype}, not what its dtype argument says")
-    if tuple(x.shape) != (rows, cols):
-        if x.dim() == 2 or x.numel() != rows * cols or not x.is_contiguous():
-            raise ValueError(f"{name} is not {rows} x {cols}")
-        stride = cols
-    elif cols > 1 and x.stride(1) != 1:
-        raise ValueError(f"{name} has rows that are not contiguous")
+    shape = x.shape
+    if len(shape) == 2 and shape[0] == rows and shape[1] == cols:
+        stride, inner = x.stride()
+        if inner != 1 and cols > 1:
+            raise ValueError(f"{name} has rows that are not contiguous")
+        if rows < 2 and stride < cols:
+            stride = cols
+    elif len(shape) == 2 or x.numel() != rows * cols or not x.is_contiguous():
+        raise ValueError(f"{name} is not {rows} x {cols}")
     else:
-        stride = x.stride(0) if rows > 1 else max(cols, x.stride(0))
+        stride = cols
     if ld is not None and ld != stride and rows > 1:
         raise ValueError(f"{name} has a row stride of {stride}, not {ld}")
-    return x.data_ptr(), _dtype(x), stride
+    return x.data_ptr(), code, stride
 
 
 def _vector(x, n: int, dtype, name: str):
     """(address, dtype) of n contiguous elements; (0, None) of None."""
     if x is None:
         return 0, None
-    if isinstance(x, int):
-        return x, _dtype(dtype) if dtype is not None else None
-    if dtype is not None and _dtype(dtype) != _dtype(x):
+    if x.__class__ is int:
+        return x, None if dtype is None else _dtype(dtype)
+    code = _real(x.dtype)
+    if dtype is not None and dtype != code and _dtype(dtype) != code:
         raise ValueError(f"{name} is {x.dtype}, not what its dtype argument says")
     if x.numel() != n or not x.is_contiguous():
         raise ValueError(f"{name} is not {n} contiguous elements")
-    return x.data_ptr(), _dtype(x)
+    return x.data_ptr(), code
 
 
-def _one_dtype(pairs, default: int, what: str) -> int:
-    found = {dt for _, dt in pairs if dt is not None}
-    if len(found) > 1:
-        raise ValueError(f"{what} are of different dtypes")
-    return found.pop() if found else default
+def _one_dtype(a, b, default: int, what: str) -> int:
+    """The dtype of two vectors of which one may be missing."""
+    if a is None or b is None or a == b:
+        return b if a is None and b is not None else (default if a is None else a)
+    raise ValueError(f"{what} are of different dtypes")
 
 
 def _ckpt(x, rows: int, cols: int, name: str) -> int:
     """Address of a checkpoint: a contiguous tensor of one-byte elements, of
     zr_ckpt_bytes(rows, cols) of them at least, or an address."""
-    if x is None or isinstance(x, int):
+    if x is None or x.__class__ is int:
         return x or 0
     if x.element_size() != 1 or not x.is_contiguous() or x.numel() < zr_ckpt_bytes(rows, cols):
         raise ValueError(f"{name} is not a contiguous buffer of zr_ckpt_bytes({rows}, {cols}) bytes")
     return x.data_ptr()
 
 
+_raw_stream = None  # torch's current stream of a GPU as a handle
+
+
 def _run_on(stream, *xs) -> int:
     """The stream's handle, for a call on these buffers: tensors must be on the
-    GPU that the stream is on (torch's current stream: on the current GPU)."""
-    import torch
-    here = None
+    GPU that is current (and the stream, if given, is on)."""
+    global _raw_stream
+    here = -2
     for x in xs:
-        x = x[0] if isinstance(x, tuple) else x
-        if x is None or isinstance(x, int):
+        if x is None or x.__class__ is int or x.__class__ is tuple:
             continue
-        if not x.is_cuda:
-            raise ValueError("a tensor is not on the GPU")
-        if here is None:
-            here = x.device
-        if x.device != here:
-            raise ValueError(f"tensors on {here} and {x.device}")
-    if here is not None:
+        d = x.get_device()
+        if d != here:
+            if d < 0:
+                raise ValueError("a tensor is not on the GPU")
+            if here >= 0:
+                raise ValueError(f"tensors on GPUs {here} and {d}")
+            here = d
+    if here >= 0 or stream is None:
+        import torch
         on = torch.cuda.current_device()
-        if here.index != on or (stream is not None and not isinstance(stream, int) and stream.device != here):
-            raise ValueError(f"the tensors are on {here}, the current GPU is {on}: make theirs current, and its stream")
+        if here >= 0 and (here != on or getattr(getattr(stream, "device", None), "index", here) != here):
+            raise ValueError(f"the tensors are on GPU {here}, the current one is {on}: make theirs current, "
+                             "and its stream")
+        if stream is None:
+            if _raw_stream is None:
+                _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+                    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+            return _raw_stream(on)
     return _stream(stream)
 
 
@@ -825,7 +854,7 @@ def zr_layernorm_fwd(x, rows: int, cols: int, y=None, weight=None, bias=None, ep
     else:
         py, yd, ldy = _matrix(y, rows, cols, y_dtype, ld_y, "y")
     w, b = _vector(weight, cols, param_dtype, "weight"), _vector(bias, cols, param_dtype, "bias")
-    _check(lib().zr_layernorm_fwd(px, xd, rows, cols, ldx, w[0], b[0], _one_dtype((w, b), ZR_FP32, "weight and bias"),
+    _check(lib().zr_layernorm_fwd(px, xd, rows, cols, ldx, w[0], b[0], _one_dtype(w[1], b[1], ZR_FP32, "weight and bias"),
                                   eps, py, yd, ldy, _vector(mean, rows, ZR_FP32, "mean")[0],
                                   _vector(rstd, rows, ZR_FP32, "rstd")[0], _ckpt(ckpt_x, rows, cols, "ckpt_x"),
                                   _ckpt(ckpt_y, rows, cols, "ckpt_y"), ckpt_format,
@@ -845,9 +874,9 @@ def zr_layernorm_bwd(dy, x, rows: int, cols: int, mean, rstd, weight=None, dx=No
     w = _vector(weight, cols, param_dtype, "weight")
     gw, gb = _vector(dweight, cols, grad_dtype, "dweight"), _vector(dbias, cols, grad_dtype, "dbias")
     ws, wsb = _workspace(workspace)
-    _check(lib().zr_layernorm_bwd(pdy, dyd, lddy, px, xd, ldx, rows, cols, w[0], _one_dtype((w,), ZR_FP32, "weight"),
+    _check(lib().zr_layernorm_bwd(pdy, dyd, lddy, px, xd, ldx, rows, cols, w[0], ZR_FP32 if w[1] is None else w[1],
                                   _vector(mean, rows, ZR_FP32, "mean")[0], _vector(rstd, rows, ZR_FP32, "rstd")[0],
-                                  pdx, dxd, lddx, gw[0], gb[0], _one_dtype((gw, gb), ZR_FP32, "dweight and dbias"),
+                                  pdx, dxd, lddx, gw[0], gb[0], _one_dtype(gw[1], gb[1], ZR_FP32, "dweight and dbias"),
                                   (ZR_ACCUMULATE if accumulate else 0) | (ZR_ADD_DX if add_dx else 0), ws, wsb,
                                   _run_on(stream, dy, x, mean, rstd, weight, dx, dweight, dbias, workspace)))
 
@@ -862,6 +891,6 @@ def zr_ckpt_wgrad(dy, ckpt, rows: int, out_cols: int, in_cols: int, dw, dbias=No
     gb = _vector(dbias, out_cols, grad_dtype if isinstance(dbias, int) else None, "dbias")
     ws, wsb = _workspace(workspace)
     _check(lib().zr_ckpt_wgrad(pdy, dyd, lddy, _ckpt(ckpt, rows, in_cols, "ckpt"), format, rows, out_cols, in_cols,
-                               pdw, _one_dtype(((pdw, gd), gb), gd, "dw and dbias"), lddw, gb[0],
+                               pdw, _one_dtype(gd, gb[1], gd, "dw and dbias"), lddw, gb[0],
                                ZR_ACCUMULATE if accumulate else 0, ws, wsb,
                                _run_on(stream, dy, ckpt, dw, dbias, workspace)))
