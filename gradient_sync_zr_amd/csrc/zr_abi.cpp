@@ -1147,8 +1147,8 @@ size_t zr_ckpt_wgrad_workspace_bytes(int64_t rows, int64_t out_cols, int64_t in_
         !size_valid(rows, in_cols) || !size_valid(out_cols, in_cols))
         return 0;
     // either form may be taken: by dy's type and alignment, which this call does not know
-    int splits = wgrad_cut(rows, out_cols, in_cols, false).splits;
-    if (wgrad_big(rows, out_cols, in_cols)) splits = std::max(splits, wgrad_cut(rows, out_cols, in_cols, true).splits);
+    const int splits = std::max(wgrad_cut(rows, out_cols, in_cols, false).splits,
+                                wgrad_cut(rows, out_cols, in_cols, true).splits);
     return splits > 1 ? (size_t)splits * (size_t)(out_cols * in_cols + out_cols) * sizeof(float) : 0;
 }
 

@@ -208,31 +208,38 @@ ZR_KERNELS hipError_t launch_ckpt_pack(const void* x, zr_dtype dt, int64_t rows,
 ZR_KERNELS hipError_t launch_ckpt_unpack(const void* ckpt, zr_dtype fmt, int64_t rows, int64_t cols, void* x,
                                          zr_dtype dt, int64_t ld, hipStream_t stream);
 
-// How a weight gradient is cut: tiles of dW, one per block, and parts that the
-// sum over rows is split into (each of `span` rows) where the tiles alone do
-// not fill the chip's places (two blocks per CU, or one of the large form).
+// How a weight gradient is cut: tiles of dW, one per block, in the large or the
+// small form, and parts that the sum over rows is split into (each of `span`
+// rows). More parts fill the chip where there are few tiles, but each writes
+// and reads dW once more in fp32. The number of parts, and the form, is the one
+// of least time by this model, fitted to sweeps of both over 11 shapes (rows 128
+// to 65,536, dW 128 x 128 to 4096 x 4096; within 10% of the best measured):
+//  - a slab of 64 rows takes a small block 0.95 us alone, 1.05 with one block
+//    on every CU and 1.4 with two; a large block 1.46 alone, 1.9 with all;
+//  - joining costs 5 us and 0.35 us per MB of parts.
 constexpr int kWgradTile = 128, kWgradBig = 256;
-inline bool wgrad_big(int64_t rows, int64_t out, int64_t in) {
-    return rows >= 512 && out > kWgradTile && in > kWgradTile && out * in >= (int64_t)1 << 21;
-}
 struct WgradCut {
     int splits;
     int64_t span;
+    float us;
 };
 inline WgradCut wgrad_cut(int64_t rows, int64_t out, int64_t in, bool big) {
-    const int64_t tile = big ? kWgradBig : kWgradTile;
-    const int64_t tiles = ((out + tile - 1) / tile) * ((in + tile - 1) / tile);
-    int64_t splits = (big ? 256 : 512) / tiles;
-    const int64_t most = rows / 128;  // a part is two slabs of rows at least
-    if (splits > most) splits = most;
-    if (splits > 64) splits = 64;
-    if (splits < 1) splits = 1;
-    WgradCut c;
-    c.span = ((rows + splits - 1) / splits + 63) / 64 * 64;
-    if (c.span < 64) c.span = 64;
-    c.splits = (int)((rows + c.span - 1) / c.span);
-    if (c.splits < 1) c.splits = 1;
-    return c;
+    const int64_t tile = big ? kWgradBig : kWgradTile, places = big ? 256 : 512;
+    const int64_t tiles = ((out + tile - 1) / tile) * ((in + tile - 1) / tile), slabs = (rows + 63) / 64;
+    auto slab_us = [&](int64_t blocks) {  // one slab of each of up to `places` blocks
+        const float load = (float)(blocks < 256 ? blocks : 256) / 256.0f;
+        return big ? 1.46f + 0.44f * load : (blocks > 256 ? 1.4f : 0.95f + 0.1f * load);
+    };
+    WgradCut best{1, (slabs > 0 ? slabs : 1) * 64, 0.0f};
+    for (int64_t n = 1; n <= 64 && (n == 1 || n <= slabs); ++n) {
+        const int64_t per = (slabs + n - 1) / n;
+        if (n > 1 && (slabs + per - 1) / per != n) continue;  // the same parts as a smaller n
+        const int64_t blocks = tiles * n, rounds = blocks / places, rest = blocks % places;
+        float us = (float)per * ((float)rounds * slab_us(places) + (rest ? slab_us(rest) : 0.0f));
+        if (n > 1) us += 5.0f + 0.35e-6f * 4.0f * (float)n * (float)out * (float)in;
+        if (n == 1 || us < best.us) best = WgradCut{(int)n, (per > 0 ? per : 1) * 64, us};
+    }
+    return best;
 }
 
 struct Wgrad {

@@ -526,26 +526,54 @@ __global__ __launch_bounds__(kBigThreads) void wgrad_big_kernel(WgradArgs a) {
     }
 }
 
-// Sums the parts, in order. Items are runs of 1024 columns of a row of dW,
-// and after them runs of db.
+// Sums the parts, in order. A thread takes V neighbouring elements and has the
+// loads of 8 / V parts in flight: one element where there are few outputs (of
+// many parts), four where there are many. Items are runs of 256 V columns of a
+// row of dW, and after them runs of db.
+template <int V>
 __global__ __launch_bounds__(kThreads) void wgrad_join_kernel(WgradArgs a) {
-    const int64_t segs = (a.in + 1023) / 1024, bsegs = a.db ? (a.out + 1023) / 1024 : 0;
+    constexpr int N = 8 / V;
+    const int64_t run = kThreads * V, segs = (a.in + run - 1) / run, bsegs = a.db ? (a.out + run - 1) / run : 0;
     const int64_t stride = a.out * a.in + a.out;
     for (int64_t item = blockIdx.x; item < a.out * segs + bsegs; item += gridDim.x) {
         const bool bias = item >= a.out * segs;
         const int64_t o = bias ? a.out : item / segs;
-        const int64_t c0 = (bias ? item - a.out * segs : item % segs) * 1024, end = bias ? a.out : a.in;
-        const float* src = a.part + o * a.in;
-        char* dst = bias ? (char*)a.db : (char*)a.dw + o * a.ld_dw * (a.grad_dt == kBf16 ? 2 : 4);
-        for (int64_t c = c0 + threadIdx.x; c < end && c < c0 + 1024; c += kThreads) {
-            float v = 0.0f;
-            for (int s = 0; s < a.splits; ++s) v += src[s * stride + c];
+        const int64_t c = (bias ? item - a.out * segs : item % segs) * run + threadIdx.x * V;
+        const int64_t left = (bias ? a.out : a.in) - c;
+        if (left <= 0) continue;
+        const float* src = a.part + o * a.in + c;
+        float v[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[e] = 0.0f;
+        for (int s = 0; s < a.splits; s += N) {
+            float t[N][V];
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                const float* q = src + (s + k) * stride;
+                if (V == 4 && left >= 4 && s + k < a.splits) {
+                    const f32x4 w = *(const f32x4_a4*)q;
+                    t[k][0] = w.x; t[k][1 % V] = w.y; t[k][2 % V] = w.z; t[k][3 % V] = w.w;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < V; ++e) t[k][e] = e < left && s + k < a.splits ? q[e] : 0.0f;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+#pragma unroll
+                for (int e = 0; e < V; ++e) v[e] += t[k][e];
+        }
+        const int64_t at = bias ? c : o * a.ld_dw + c;
+        void* const out = bias ? a.db : a.dw;
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            if (e >= left) continue;
             if (a.grad_dt == kBf16) {
-                uint16_t* p = (uint16_t*)dst + c;
-                store_elem(p, a.accumulate ? load_elem(p) + v : v);
+                uint16_t* p = (uint16_t*)out + at + e;
+                store_elem(p, a.accumulate ? load_elem(p) + v[e] : v[e]);
             } else {
-                float* p = (float*)dst + c;
-                store_elem(p, a.accumulate ? load_elem(p) + v : v);
+                float* p = (float*)out + at + e;
+                store_elem(p, a.accumulate ? load_elem(p) + v[e] : v[e]);
             }
         }
     }
@@ -565,10 +593,12 @@ hipError_t run(const WgradArgs& a, bool big, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_ckpt_wgrad(const Wgrad& w, hipStream_t stream) {
-    const bool big = wgrad_big(w.rows, w.out, w.in) && w.dy_dt == ZR_BF16 && w.out % 8 == 0 && w.ld_dy % 8 == 0 &&
-                     ((uintptr_t)w.dy & 15) == 0 && w.ld_dy <= (1 << 24) && w.in <= (1 << 24);
+    const bool whole = w.dy_dt == ZR_BF16 && w.out % 8 == 0 && w.ld_dy % 8 == 0 && ((uintptr_t)w.dy & 15) == 0 &&
+                       w.ld_dy <= (1 << 24) && w.in <= (1 << 24);
+    const WgradCut small = wgrad_cut(w.rows, w.out, w.in, false), large = wgrad_cut(w.rows, w.out, w.in, true);
+    const bool big = whole && large.us < small.us;
+    const WgradCut cut = big ? large : small;
     const int tile = big ? kWgradBig : kWgradTile;
-    const WgradCut cut = wgrad_cut(w.rows, w.out, w.in, big);
     WgradArgs a{};
     a.dy = w.dy;
     a.pitch = ckpt_pitch(w.in);
@@ -590,8 +620,13 @@ hipError_t launch_ckpt_wgrad(const Wgrad& w, hipStream_t stream) {
     else
         e = e4m3 ? run<kFp32, kE4m3>(a, false, stream) : run<kFp32, kInt8>(a, false, stream);
     if (e != hipSuccess || a.splits == 1) return e;
-    const int64_t items = w.out * ((w.in + 1023) / 1024) + (a.db ? (w.out + 1023) / 1024 : 0);
-    wgrad_join_kernel<<<grid_for(items), kThreads, 0, stream>>>(a);
+    const int v = w.out * w.in >= (int64_t)1 << 20 ? 4 : 1;
+    const int64_t run_of = kThreads * v;
+    const int64_t items = w.out * ((w.in + run_of - 1) / run_of) + (a.db ? (w.out + run_of - 1) / run_of : 0);
+    if (v == 4)
+        wgrad_join_kernel<4><<<grid_for(items), kThreads, 0, stream>>>(a);
+    else
+        wgrad_join_kernel<1><<<grid_for(items), kThreads, 0, stream>>>(a);
     return hipGetLastError();
 }
 
