@@ -199,7 +199,7 @@ ZR_KERNELS hipError_t launch_layernorm_bwd(const NormBwd& f, hipStream_t stream)
 // are steps of rows (a block takes 16, 4 or 1 rows at once).
 inline int layernorm_strips(int64_t rows, int64_t cols) {
     const int64_t per = cols <= 128 ? 16 : (cols <= 1024 ? 4 : 1), n = (rows + per - 1) / per;
-    const int64_t most = tuning().max_grid < 512 ? tuning().max_grid : 512;
+    const int64_t places = cols <= 4096 ? 512 : 256, most = tuning().max_grid < places ? tuning().max_grid : places;
     return (int)(n < most ? n : most);
 }
 

@@ -19,6 +19,16 @@ __device__ __forceinline__ int existing(int64_t cols, int64_t c) {
 // Threads of a block whose rows have TPR lanes.
 constexpr int norm_block(int tpr) { return tpr > kThreads ? tpr : kThreads; }
 
+// Which of the block's rows a thread has: the same for a whole wave where a row
+// takes one or more, and then kept in scalar registers, as are the addresses
+// that follow from it.
+template <int TPR>
+__device__ __forceinline__ int row_group() {
+    if constexpr (norm_block(TPR) == TPR) return 0;
+    const int g = threadIdx.x / TPR;
+    return TPR >= 64 ? __builtin_amdgcn_readfirstlane(g) : g;
+}
+
 // Sums of N values each over the TPR lanes of a row. red: N floats per wave of
 // the block, free again once every wave has passed a later barrier.
 template <int TPR, int N>

@@ -52,7 +52,7 @@ __global__ __launch_bounds__(norm_block(TPR)) void bwd_kernel(BwdArgs a) {
     constexpr int C = TPR * NV * 8;  // columns that a row's lanes cover
     __shared__ float red[2][B / 64][2];
     __shared__ float join[G > 1 ? G : 1][G > 1 ? C : 1];
-    const int lane = threadIdx.x % TPR, group = threadIdx.x / TPR;
+    const int lane = threadIdx.x % TPR, group = row_group<TPR>();
     const float inv_n = 1.0f / (float)a.cols;
     float w[NV][8], dw[NV][8], db[NV][8];
 #pragma unroll
@@ -65,6 +65,7 @@ __global__ __launch_bounds__(norm_block(TPR)) void bwd_kernel(BwdArgs a) {
     Raw8<XD> rx[NV];
     Raw8<DD> rd[NV];
     float mean_next = 0.0f, rstd_next = 0.0f;
+    const int dx_es = a.dx_dt == kBf16 ? 2 : 4;
     auto fetch = [&](int64_t row) {
         const RowPtr px = row_at<XD>(a.x, a.ld_x, a.rows, a.cols, row), pd = row_at<DD>(a.dy, a.ld_dy, a.rows, a.cols, row);
 #pragma unroll
@@ -81,6 +82,18 @@ __global__ __launch_bounds__(norm_block(TPR)) void bwd_kernel(BwdArgs a) {
     if (first < a.rows) fetch(first);
     for (int64_t row = first; row < a.rows; row += step) {
         const float mean = mean_next, rstd = rstd_next;
+        char* out = a.dx + row * a.ld_dx * dx_es;
+        Raw8<kFp32> old[NV];  // dx before; bf16 in the first half
+        if (a.add_dx) {  // in flight during the sums, and waited for before the next row's loads
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                const int c = (v * TPR + lane) * 8, n = existing(a.cols, c);
+                if (a.dx_dt == kBf16)
+                    old[v].a = __builtin_bit_cast(f32x4, load8<kBf16>({out, nullptr}, c, n).v);
+                else
+                    old[v] = load8<kFp32>({out, nullptr}, c, n);
+            }
+        }
         float xh[NV][8], g[NV][8];
         float s[2] = {0.0f, 0.0f};
 #pragma unroll
@@ -106,7 +119,6 @@ __global__ __launch_bounds__(norm_block(TPR)) void bwd_kernel(BwdArgs a) {
         row_sums<TPR>(s, red[parity]);
         parity ^= 1;
         const float k1 = -(s[0] * inv_n) * rstd, k2 = -(s[1] * inv_n) * rstd;
-        char* out = a.dx + row * a.ld_dx * (a.dx_dt == kBf16 ? 2 : 4);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int c = (v * TPR + lane) * 8, n = existing(a.cols, c);
@@ -114,10 +126,13 @@ __global__ __launch_bounds__(norm_block(TPR)) void bwd_kernel(BwdArgs a) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) g[v][e] = __builtin_fmaf(g[v][e], rstd, __builtin_fmaf(xh[v][e], k1, k2));
             if (a.add_dx) {
-                float old[8];
-                load_param8(out, a.dx_dt, c, n, 0.0f, old);
+                float o[8];
+                if (a.dx_dt == kBf16)
+                    widen8(Raw8<kBf16>{__builtin_bit_cast(u32x4, old[v].a)}, o);
+                else
+                    widen8(old[v], o);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) g[v][e] += old[e];
+                for (int e = 0; e < 8; ++e) g[v][e] += o[e];
             }
             store8(out, a.dx_dt, c, n, g[v]);
         }
@@ -240,8 +255,14 @@ __global__ __launch_bounds__(1024) void bwd_join_kernel(const float* part, int s
     for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
         const int64_t at = t * 64 + lane;
         float s = 0.0f;
-        if (at < 2 * cols)
-            for (int k = group; k < strips; k += 16) s += part[(int64_t)k * 2 * cols + at];
+        for (int k = group; k < strips; k += 128) {  // eight loads in flight
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v[e] = at < 2 * cols && k + 16 * e < strips ? part[(int64_t)(k + 16 * e) * 2 * cols + at] : 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s += v[e];
+        }
         __syncthreads();
         sum[group][lane] = s;
         __syncthreads();
@@ -276,8 +297,8 @@ hipError_t bwd_pick(const BwdArgs& a, int strips, hipStream_t stream) {
     if (n <= 512) return bwd_run<XD, DD, 64, 1>(a, strips, stream);
     if (n <= 1024) return bwd_run<XD, DD, 64, 2>(a, strips, stream);
     if (n <= 2048) return bwd_run<XD, DD, 256, 1>(a, strips, stream);
-    if (n <= 4096) return bwd_run<XD, DD, 256, 2>(a, strips, stream);
-    if (n <= 8192) return bwd_run<XD, DD, 256, 4>(a, strips, stream);
+    if (n <= 4096) return bwd_run<XD, DD, 512, 1>(a, strips, stream);
+    if (n <= 8192) return bwd_run<XD, DD, 512, 2>(a, strips, stream);
     if (n <= 12288) return bwd_run<XD, DD, 512, 3>(a, strips, stream);
     if (a.part) {  // before dx, which may take dy's or x's place
         const int64_t tiles = (n + kThreads * 8 - 1) / (kThreads * 8);
