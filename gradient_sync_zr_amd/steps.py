@@ -11,6 +11,11 @@ reducer does with the C ABI, one step at a time.
 * :class:`Zero3Gather` - full parameters gathered from 1/K shards in greedy
   prefetch buckets ("DeepSpeed ZeRO-3 源码解析", 2.1 fetch/prefetch and 2.2
   the prefetch size cap), one all-gather launch set per bucket.
+* :class:`CkptNormLinear` - one rank's norm and the linear layer behind it,
+  whose activations are kept as 8-bit checkpoints and whose backward pass
+  writes the weight gradients into the rank's flat gradient, where
+  :class:`Zero2GradSync` takes them (its ``produce`` hook is the place to call
+  the backward pass from).
 
 All tensors are torch CUDA tensors used only as device memory; every
 computation happens in libzr's kernels.
@@ -19,8 +24,9 @@ from __future__ import annotations
 
 from typing import Callable, List, Optional, Sequence
 
-from . import (ZR_BF16, ZR_FP32, ZR_ORDER_RING, Sched, zr_all_gather, zr_plan_buckets,
-               _dtype)
+from . import (ZR_BF16, ZR_CKPT_E4M3, ZR_FP32, ZR_ORDER_RING, Sched, zr_all_gather, zr_ckpt_bytes,
+               zr_ckpt_wgrad, zr_ckpt_wgrad_workspace_bytes, zr_layernorm_bwd, zr_layernorm_fwd,
+               zr_layernorm_workspace_bytes, zr_plan_buckets, _dtype)
 
 
 def ceil_div(a: int, b: int) -> int:
@@ -139,3 +145,93 @@ class Zero3Gather:
         for segs in self.buckets:
             zr_all_gather(self._sp, self._fp, segs, chunk_shift=self.shift, dtype=self.dt,
                           stream=stream)
+
+
+class CkptNormLinear:
+    """Layer norm of a rank's activations (rows x cols) and the linear layer
+    that reads it (out_cols x cols), with 8-bit checkpoints.
+
+    flat_grad : the rank's flat gradient; the layer's part of it starts at
+                element `offset` and holds, in order, the norm's weight and
+                bias (cols each), the linear layer's weight (out_cols x cols)
+                and, with `bias`, its bias (out_cols): `numel` elements
+    recompute : keep the checkpoint of the norm's input alone, and recompute the
+                linear layer's input from it in the backward pass; otherwise
+                both checkpoints are kept
+    scratch   : a uint8 tensor of `scratch_bytes` elements, the backward pass's
+                workspace (and with `recompute` its checkpoint of the linear
+                layer's input); layers whose backward passes run one after
+                another on a stream may share it, others must not
+
+    The matrix products y W^T of the forward pass and dz W of the backward pass
+    are the caller's; they come between the methods:
+        forward(x, w, b, y);  z = y W^T
+        backward_linear(dz);  dy = dz W;  backward_norm(dy, w, dx)
+    """
+
+    def __init__(self, flat_grad, offset: int, rows: int, cols: int, out_cols: int, scratch=None,
+                 format: int = ZR_CKPT_E4M3, eps: float = 1e-5, bias: bool = True, recompute: bool = True):
+        import torch
+        self.rows, self.cols, self.out_cols = rows, cols, out_cols
+        self.format, self.eps, self.recompute = format, eps, recompute
+        sizes = [cols, cols, out_cols * cols] + ([out_cols] if bias else [])
+        self.numel = sum(sizes)
+        if offset < 0 or offset + self.numel > flat_grad.numel():
+            raise ValueError(f"the flat gradient holds {flat_grad.numel()} elements, the layer needs {self.numel} "
+                             f"at {offset}")
+        parts = flat_grad[offset:offset + self.numel].split(sizes)
+        self.dw_norm, self.db_norm = parts[0], parts[1]
+        self.dw = parts[2].view(out_cols, cols)
+        self.db = parts[3] if bias else None
+        self._ws_bytes = max(zr_layernorm_workspace_bytes(rows, cols),
+                             zr_ckpt_wgrad_workspace_bytes(rows, out_cols, cols))
+        nbytes = zr_ckpt_bytes(rows, cols)
+        self._y_at = ceil_div(self._ws_bytes, 256) * 256
+        self.scratch_bytes = self._y_at + (nbytes if recompute else 0)
+        dev = flat_grad.device
+        if scratch is None:
+            scratch = torch.empty(self.scratch_bytes, dtype=torch.uint8, device=dev)
+        if scratch.numel() < self.scratch_bytes:
+            raise ValueError(f"scratch holds {scratch.numel()} bytes, needs {self.scratch_bytes}")
+        self.scratch = scratch
+        self.ckpt_x = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        self.ckpt_y = scratch[self._y_at:self._y_at + nbytes] if recompute else \
+            torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        self.mean = torch.empty(rows, dtype=torch.float32, device=dev)
+        self.rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+        self._params = None
+
+    def forward(self, x, weight, bias, y, stream=None) -> None:
+        """The norm of x into y; x itself is not needed afterwards."""
+        zr_layernorm_fwd(x, self.rows, self.cols, y, weight, bias, eps=self.eps, mean=self.mean, rstd=self.rstd,
+                         ckpt_x=self.ckpt_x, ckpt_y=None if self.recompute else self.ckpt_y,
+                         ckpt_format=self.format, stream=stream)
+        self._params = (weight, bias, y.dtype)
+
+    def backward_linear(self, dz, accumulate: bool = False, stream=None) -> None:
+        """The linear layer's gradients from its output's, dz (rows x
+        out_cols), into the flat gradient (added to with accumulate: a later
+        micro-step)."""
+        if self._params is None:
+            raise ValueError("backward before forward")
+        if self.recompute:
+            weight, bias, y_dtype = self._params
+            zr_layernorm_fwd(self.ckpt_x, self.rows, self.cols, None, weight, bias, eps=self.eps,
+                             ckpt_y=self.ckpt_y, ckpt_format=self.format, x_dtype=self.format, y_dtype=y_dtype,
+                             stream=stream)
+        zr_ckpt_wgrad(dz, self.ckpt_y, self.rows, self.out_cols, self.cols, self.dw, dbias=self.db,
+                      format=self.format, accumulate=accumulate, workspace=self._workspace(), stream=stream)
+
+    def backward_norm(self, dy, weight, dx=None, accumulate: bool = False, add_dx: bool = False,
+                      stream=None) -> None:
+        """The norm's gradients from its output's, dy: the weight's and the
+        bias's into the flat gradient, the input's into dx (added to with
+        add_dx: the residual stream's gradient)."""
+        if self._params is None:
+            raise ValueError("backward before forward")
+        zr_layernorm_bwd(dy, self.ckpt_x, self.rows, self.cols, self.mean, self.rstd, weight, dx=dx,
+                         dweight=self.dw_norm, dbias=self.db_norm, accumulate=accumulate, add_dx=add_dx,
+                         workspace=self._workspace(), x_dtype=self.format, stream=stream)
+
+    def _workspace(self):
+        return self.scratch[:self._ws_bytes]
