@@ -142,7 +142,7 @@ def test_backward_refusals():
 
 
 def wgrad(**kw):
-    a = dict(dy=A, ckpt=B, rows=256, out_cols=100, in_cols=70, dw=C, dbias=D, workspace=(E, 1 << 30), dy_dtype=BF,
+    a = dict(dy=A, ckpt=B, rows=8192, out_cols=100, in_cols=70, dw=C, dbias=D, workspace=(E, 1 << 30), dy_dtype=BF,
              grad_dtype=FP, stream=0)
     a.update(kw)
     zr.zr_ckpt_wgrad(**a)
@@ -161,7 +161,7 @@ def test_wgrad_refusals():
     expect(zr.ZR_ERR_UNSUPPORTED, wgrad, dy_dtype=zr.ZR_CKPT_E4M3)
     expect(zr.ZR_ERR_UNSUPPORTED, wgrad, grad_dtype=zr.ZR_CKPT_E4M3, dbias=None)
     expect(zr.ZR_ERR_UNSUPPORTED, wgrad, format=BF)
-    need = zr.zr_ckpt_wgrad_workspace_bytes(256, 100, 70)
+    need = zr.zr_ckpt_wgrad_workspace_bytes(8192, 100, 70)
     assert need > 0
     expect(zr.ZR_ERR_WORKSPACE, wgrad, workspace=None)
     expect(zr.ZR_ERR_WORKSPACE, wgrad, workspace=(E, need - 1))
