@@ -293,12 +293,25 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void wgrad_kernel(Wgrad
     }
 }
 
-// The large form, for bf16 dY in rows of whole, aligned 16-byte chunks: tiles
-// of 256 x 256, eight waves of 128 x 64. A slab of 64 rows costs a CU 2,061
-// cycles of matrix units and reads 192 KB from LDS (1,536 cycles at 128 bytes
-// a cycle) where four tiles of 128 x 128 would read 256 KB. Each wave's 128
-// fp32 accumulators leave 128 registers for operands and the next slab.
+// The large form, for bf16 dY: tiles of 256 x 256, eight waves of 128 x 64. A
+// slab of 64 rows costs a CU 2,061 cycles of matrix units and reads 192 KB from
+// LDS (1,536 cycles at 128 bytes a cycle) where four tiles of 128 x 128 would
+// read 256 KB. Each wave's 128 fp32 accumulators leave 128 registers for
+// operands and the next slab.
 constexpr int kBigThreads = 512, kBigBK = 64;
+
+// The 128 bits behind the first `bits` of v (zeros after them); 128 and more: none.
+__device__ __forceinline__ u32x4 behind(const u32x4& v, int bits) {
+    uint64_t lo = ((uint64_t)v.y << 32) | v.x, hi = ((uint64_t)v.w << 32) | v.z;
+    if (bits >= 64) {
+        lo = hi;
+        hi = 0;
+    }
+    const int by = bits & 63;
+    if (by) lo = (lo >> by) | (hi << (64 - by));
+    hi >>= by;
+    return bits >= 128 ? u32x4{0, 0, 0, 0} : u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+}
 
 // v plus the two bf16 values of a word.
 __device__ __forceinline__ float sum2(uint32_t w, float v) {
@@ -363,11 +376,16 @@ __global__ __launch_bounds__(kBigThreads) void wgrad_big_kernel(WgradArgs a) {
         const int64_t kb = part * a.span, ke = kb + a.span < a.rows ? kb + a.span : a.rows;
         const bool bias = a.db && tn == 0 && wn == 0;
         // columns behind the last are read from the last chunk and not stored
-        const int64_t col_a = m0 + ca * 8 < a.out ? m0 + ca * 8 : a.out - 8;
+        const int64_t col_a = m0 + ca * 8 <= a.out - 8 ? m0 + ca * 8 : a.out - 8;
         const int64_t col_b = n0 + cb * 16 < a.pitch ? n0 + cb * 16 : a.pitch - 16;
-        const uint32_t va = (uint32_t)(col_a - m0) * 2, vb = (uint32_t)(col_b - n0), vs = vb / kCkptBlock;
+        // in the last tile of an `out` that is not whole chunks, the last chunk
+        // that exists in part is read from `out - 8` and moved into place
+        const bool ragged = m0 + BM > a.out && a.out % 8 != 0;
+        const int late = (int)(m0 + ca * 8 - col_a) * 16;  // bits, 0 in other chunks
+        const int64_t from = m0 <= a.out - 8 ? m0 : a.out - 8;  // no chunk starts before it
+        const uint32_t va = (uint32_t)(col_a - from) * 2, vb = (uint32_t)(col_b - n0), vs = vb / kCkptBlock;
         const uint32_t la = (uint32_t)a.ld_dy * 2, lb = (uint32_t)a.pitch, ls = (uint32_t)sp;
-        const char* pa = (const char*)a.dy + (kb * a.ld_dy + m0) * 2;
+        const char* pa = (const char*)a.dy + (kb * a.ld_dy + from) * 2;
         const char* pb = a.codes + kb * a.pitch + n0;
         const uint8_t* ps = a.scales + kb * sp + n0 / kCkptBlock;
 
@@ -389,7 +407,7 @@ __global__ __launch_bounds__(kBigThreads) void wgrad_big_kernel(WgradArgs a) {
 #pragma unroll
             for (int j = 0; j < NA; ++j) {
                 const int t = ta + j * RA < have ? ta + j * RA : have - 1;
-                ra[j] = *(const u32x4*)(pa + ((uint32_t)t * la + va));
+                ra[j] = *(const u32x4_a2*)(pa + ((uint32_t)t * la + va));
             }
 #pragma unroll
             for (int j = 0; j < NB; ++j) {
@@ -403,7 +421,9 @@ __global__ __launch_bounds__(kBigThreads) void wgrad_big_kernel(WgradArgs a) {
             left -= BK;
         };
         auto put_a = [&](char* buf, int j) {
-            *(u32x4*)(buf + putA + j * RA * PA) = ta + j * RA < have ? ra[j] : u32x4{0, 0, 0, 0};
+            u32x4 v = ta + j * RA < have ? ra[j] : u32x4{0, 0, 0, 0};
+            if (ragged) v = behind(v, late);
+            *(u32x4*)(buf + putA + j * RA * PA) = v;
         };
         auto put_b = [&](char* buf, int j) {
             uint32_t w[8];
@@ -593,10 +613,9 @@ hipError_t run(const WgradArgs& a, bool big, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_ckpt_wgrad(const Wgrad& w, hipStream_t stream) {
-    const bool whole = w.dy_dt == ZR_BF16 && w.out % 8 == 0 && w.ld_dy % 8 == 0 && ((uintptr_t)w.dy & 15) == 0 &&
-                       w.ld_dy <= (1 << 24) && w.in <= (1 << 24);
+    const bool can = w.dy_dt == ZR_BF16 && w.out >= 8 && w.ld_dy <= (1 << 24) && w.in <= (1 << 24);
     const WgradCut small = wgrad_cut(w.rows, w.out, w.in, false), large = wgrad_cut(w.rows, w.out, w.in, true);
-    const bool big = whole && large.us < small.us;
+    const bool big = can && large.us < small.us;
     const WgradCut cut = big ? large : small;
     const int tile = big ? kWgradBig : kWgradTile;
     WgradArgs a{};

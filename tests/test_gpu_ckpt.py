@@ -196,10 +196,10 @@ def test_wgrad_exact_on_integers(rows, out, inn, dy_dt, fmt):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
-@pytest.mark.parametrize("rows,out,inn", [(577, 136, 16384), (4160, 2056, 1090), (700, 4104, 4100), (65, 4104, 4100)])
+@pytest.mark.parametrize("rows,out,inn", [(577, 136, 16384), (4160, 2056, 1090), (700, 4104, 4100), (65, 4104, 4100),
+                                          (700, 4097, 4100), (65, 4103, 4100), (130, 4351, 4100)])
 def test_wgrad_exact_on_integers_large(rows, out, inn, fmt):
-    """The large form (rows of whole 16-byte chunks), with ragged last tiles, slabs and parts; and the same
-    sizes with rows that are not, which take the small one."""
+    """The large form, with ragged last tiles, slabs and parts, and rows that do not start or end on 16 bytes."""
     rng = np.random.default_rng(rows)
     dy = rng.integers(-4, 5, (rows, out)).astype(np.float32)
     x = rng.integers(-8, 9, (rows, inn)).astype(np.float32)
