@@ -1146,10 +1146,7 @@ size_t zr_ckpt_wgrad_workspace_bytes(int64_t rows, int64_t out_cols, int64_t in_
     if (out_cols < 1 || out_cols > kMaxCols || in_cols < 1 || in_cols > kMaxCols || !size_valid(rows, out_cols) ||
         !size_valid(rows, in_cols) || !size_valid(out_cols, in_cols))
         return 0;
-    // either form may be taken: by dy's type and alignment, which this call does not know
-    const int splits = std::max(wgrad_cut(rows, out_cols, in_cols, false).splits,
-                                wgrad_cut(rows, out_cols, in_cols, true).splits);
-    return splits > 1 ? (size_t)splits * (size_t)(out_cols * in_cols + out_cols) * sizeof(float) : 0;
+    return (size_t)wgrad_workspace(rows, out_cols, in_cols) * sizeof(float);
 }
 
 zr_status zr_ckpt_wgrad(const void* dy, zr_dtype dy_dt, int64_t ld_dy, const void* ckpt, zr_dtype format, int64_t rows,

@@ -208,27 +208,28 @@ ZR_KERNELS hipError_t launch_ckpt_pack(const void* x, zr_dtype dt, int64_t rows,
 ZR_KERNELS hipError_t launch_ckpt_unpack(const void* ckpt, zr_dtype fmt, int64_t rows, int64_t cols, void* x,
                                          zr_dtype dt, int64_t ld, hipStream_t stream);
 
-// How a weight gradient is cut: tiles of dW, one per block, in the large or the
-// small form, and parts that the sum over rows is split into (each of `span`
-// rows). More parts fill the chip where there are few tiles, but each writes
-// and reads dW once more in fp32. The number of parts, and the form, is the one
-// of least time by this model, fitted to sweeps of both over 11 shapes (rows 128
-// to 65,536, dW 128 x 128 to 4096 x 4096; within 10% of the best measured):
+// How a weight gradient is cut. Both forms' times come from a model fitted to
+// sweeps over 11 shapes (rows 128 to 65,536, dW 128 x 128 to 4096 x 4096; its
+// choices are within 10% of the best measured), and the smaller one is taken:
 //  - a slab of 64 rows takes a small block 0.95 us alone, 1.05 with one block
 //    on every CU and 1.4 with two; a large block 1.46 alone, 1.9 with all;
 //  - joining costs 5 us and 0.35 us per MB of parts.
+//
+// Small form: tiles of 128 x 128, the sum over rows in `splits` parts of `span`
+// rows. More parts fill the chip where there are few tiles, but each writes
+// and reads dW once more in fp32.
 constexpr int kWgradTile = 128, kWgradBig = 256;
+constexpr float kWgradJoinUs = 5.0f, kWgradMbUs = 0.35f;
 struct WgradCut {
     int splits;
     int64_t span;
     float us;
 };
-inline WgradCut wgrad_cut(int64_t rows, int64_t out, int64_t in, bool big) {
-    const int64_t tile = big ? kWgradBig : kWgradTile, places = big ? 256 : 512;
-    const int64_t tiles = ((out + tile - 1) / tile) * ((in + tile - 1) / tile), slabs = (rows + 63) / 64;
-    auto slab_us = [&](int64_t blocks) {  // one slab of each of up to `places` blocks
-        const float load = (float)(blocks < 256 ? blocks : 256) / 256.0f;
-        return big ? 1.46f + 0.44f * load : (blocks > 256 ? 1.4f : 0.95f + 0.1f * load);
+inline WgradCut wgrad_cut(int64_t rows, int64_t out, int64_t in) {
+    const int64_t tiles = ((out + kWgradTile - 1) / kWgradTile) * ((in + kWgradTile - 1) / kWgradTile);
+    const int64_t slabs = (rows + 63) / 64, places = 512;
+    auto slab_us = [](int64_t blocks) {  // one slab of each of up to `places` blocks
+        return blocks > 256 ? 1.4f : 0.95f + 0.1f * (float)blocks / 256.0f;
     };
     WgradCut best{1, (slabs > 0 ? slabs : 1) * 64, 0.0f};
     for (int64_t n = 1; n <= 64 && (n == 1 || n <= slabs); ++n) {
@@ -236,10 +237,46 @@ inline WgradCut wgrad_cut(int64_t rows, int64_t out, int64_t in, bool big) {
         if (n > 1 && (slabs + per - 1) / per != n) continue;  // the same parts as a smaller n
         const int64_t blocks = tiles * n, rounds = blocks / places, rest = blocks % places;
         float us = (float)per * ((float)rounds * slab_us(places) + (rest ? slab_us(rest) : 0.0f));
-        if (n > 1) us += 5.0f + 0.35e-6f * 4.0f * (float)n * (float)out * (float)in;
+        if (n > 1) us += kWgradJoinUs + kWgradMbUs * 4e-6f * (float)n * (float)out * (float)in;
         if (n == 1 || us < best.us) best = WgradCut{(int)n, (per > 0 ? per : 1) * 64, us};
     }
     return best;
+}
+
+// Large form: tiles of 256 x 256, of which whole rounds of 256 take one block
+// each; the slabs of the `rest` tiles are split into `parts` of `share` slabs,
+// joined from the workspace, where part p of rest tile t has slot p * rest + t.
+// (Sharing the rest's slabs out evenly, a block's share beginning anywhere in a
+// tile, would fill the last round too, but blocks at different rows have no
+// slabs in common in their L2: 16384x11008x4096, 176 rest tiles, took 1,446 us
+// against 1,428 unsplit.)
+struct WgradShare {
+    int64_t slabs, full, rest, parts, share;
+    float us;
+};
+constexpr int64_t kWgradSlot = kWgradBig * kWgradBig + kWgradBig;  // floats: a tile and its bias
+inline WgradShare wgrad_share(int64_t rows, int64_t out, int64_t in) {
+    const int64_t tiles = ((out + kWgradBig - 1) / kWgradBig) * ((in + kWgradBig - 1) / kWgradBig);
+    auto slab_us = [](int64_t blocks) { return 1.46f + 0.44f * (float)blocks / 256.0f; };
+    WgradShare w;
+    w.slabs = rows > 0 ? (rows + 63) / 64 : 1;
+    w.full = tiles / 256 * 256;
+    w.rest = tiles - w.full;
+    w.parts = 1;
+    w.share = w.slabs;
+    float best = (float)w.slabs * slab_us(w.rest);
+    for (int64_t n = 2; n * w.rest <= 256 && n <= w.slabs && w.rest > 0; ++n) {
+        const int64_t share = (w.slabs + n - 1) / n;
+        if ((w.slabs + share - 1) / share != n) continue;  // the same shares as a smaller n
+        const float us = (float)share * slab_us(n * w.rest) + kWgradJoinUs + kWgradMbUs * 4e-6f * (float)(n * w.rest * kWgradSlot);
+        if (us < best) {
+            best = us;
+            w.parts = n;
+            w.share = share;
+        }
+    }
+    w.us = (float)(w.full / 256) * (float)w.slabs * slab_us(256) + (w.rest > 0 ? best : 0.0f);
+    return w;
 }
 
 struct Wgrad {
@@ -248,8 +285,22 @@ struct Wgrad {
     int64_t rows, out, in, ld_dy, ld_dw;
     void *dw, *dbias;
     int accumulate;
-    void* workspace;  // splits > 1: splits * (out * in + out) floats
+    void* workspace;  // of wgrad_workspace() floats
 };
+// The large form needs dY in bf16, at least a chunk of it per row, and 32-bit
+// offsets within a slab.
+inline bool wgrad_can_be_large(const Wgrad& w) {
+    return w.dy_dt == ZR_BF16 && w.out >= 8 && w.ld_dy <= (1 << 24) && w.in <= (1 << 24);
+}
+// Floats of workspace that either form needs.
+inline int64_t wgrad_workspace(int64_t rows, int64_t out, int64_t in) {
+    const WgradCut c = wgrad_cut(rows, out, in);
+    const WgradShare s = wgrad_share(rows, out, in);
+    const int64_t a = c.splits > 1 ? c.splits * (out * in + out) : 0;
+    const int64_t b = s.parts > 1 ? s.parts * s.rest * kWgradSlot : 0;
+    // the large form is taken only where it is the faster one
+    return s.us < c.us && b > a ? b : a;
+}
 ZR_KERNELS hipError_t launch_ckpt_wgrad(const Wgrad& w, hipStream_t stream);
 
 }  // namespace zr

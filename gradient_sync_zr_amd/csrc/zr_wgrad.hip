@@ -43,6 +43,7 @@ struct WgradArgs {
     void *dw, *db;
     int64_t rows, out, in, ld_dy, ld_dw, pitch, span;
     int grad_dt, accumulate, tiles_m, tiles_n, splits;
+    int64_t slabs, full, rest, parts, share;  // the large form's (WgradShare)
 };
 
 // 16 codes of one block as 16 bf16 values (8 words).
@@ -79,22 +80,37 @@ __device__ __forceinline__ void split3(float v, uint32_t t[3]) {
     t[2] = __float_as_uint(r2) & 0xFFFF0000u;
 }
 
-// Which tile and part a block's item is: consecutive items of one XCD (blocks
-// are dealt to the 8 XCDs in turn) take neighbouring tiles, so that their
-// slabs meet in that XCD's L2.
-__device__ __forceinline__ void item_place(const WgradArgs& a, int64_t item, int64_t total, int* tm, int* tn, int* part) {
-    const int64_t x = item % 8, i = item / 8, q = total / 8, r = total % 8;
-    const int64_t at = (x < r ? x * (q + 1) : r * (q + 1) + (x - r) * q) + i;
-    const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
-    *part = (int)(at / tiles);
-    const int64_t t = at % tiles;
-    constexpr int GM = 8;
-    const int64_t per = (int64_t)GM * a.tiles_n;
-    const int64_t group = t / per, in_group = t % per;
-    const int first = (int)(group * GM);
-    const int gm = a.tiles_m - first < GM ? a.tiles_m - first : GM;
-    *tm = first + (int)(in_group % gm);
-    *tn = (int)(in_group / gm);
+// The same value in every lane, kept in scalar registers (a division's result
+// comes in vector ones).
+__device__ __forceinline__ int uniform(uint32_t v) { return __builtin_amdgcn_readfirstlane((int)v); }
+
+// Blocks are dealt to the 8 XCDs in turn: neighbours among `total` items for
+// the blocks of one XCD, so that their slabs meet in that XCD's L2.
+__device__ __forceinline__ uint32_t by_xcd(uint32_t item, uint32_t total) {
+    const uint32_t x = item % 8, i = item / 8, q = total / 8, r = total % 8;
+    return (x < r ? x * (q + 1) : r * (q + 1) + (x - r) * q) + i;
+}
+
+// Row and column of tile t, in groups of 8 rows of tiles.
+__device__ __forceinline__ void tile_place(const WgradArgs& a, uint32_t t, int* tm, int* tn) {
+    constexpr uint32_t GM = 8;
+    const uint32_t per = GM * (uint32_t)a.tiles_n;
+    const uint32_t group = t / per, in_group = t - group * per, first = group * GM;
+    const uint32_t gm = (uint32_t)a.tiles_m - first < GM ? (uint32_t)a.tiles_m - first : GM;
+    const uint32_t n = in_group / gm;
+    *tm = uniform(first + in_group - n * gm);
+    *tn = uniform(n);
+}
+
+// A sum to an element of a gradient.
+__device__ __forceinline__ void put_grad(void* p, int64_t at, float v, int grad_dt, bool add) {
+    if (grad_dt == kBf16) {
+        uint16_t* q = (uint16_t*)p + at;
+        store_elem(q, add ? load_elem(q) + v : v);
+    } else {
+        float* q = (float*)p + at;
+        store_elem(q, add ? load_elem(q) + v : v);
+    }
 }
 
 template <int DD, int FMT, int BM, int BN, int WM, int WN, int BK>
@@ -125,8 +141,10 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void wgrad_kernel(Wgrad
         offB[n] = P * SA + rbase * PB + (((wn * WN + n * 32) * 2) ^ (r4 << 6)) + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
 
     for (int64_t item = blockIdx.x; item < total; item += gridDim.x) {
-        int tm, tn, part;
-        item_place(a, item, total, &tm, &tn, &part);
+        int tm, tn;
+        const uint32_t at = by_xcd((uint32_t)item, (uint32_t)total), tiles = (uint32_t)(a.tiles_m * a.tiles_n);
+        const int part = uniform(at / tiles);
+        tile_place(a, at % tiles, &tm, &tn);
         const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
         const int64_t kb = part * a.span, ke = kb + a.span < a.rows ? kb + a.span : a.rows;
         const bool bias = a.db && tn == 0;
@@ -256,15 +274,10 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void wgrad_kernel(Wgrad
                     const int64_t i = n0 + wn * WN + n * 32 + (lane & 31);
                     if (o >= a.out || i >= a.in) continue;
                     const float v = acc[m][n][e];
-                    if (mine) {
+                    if (mine)
                         mine[o * a.in + i] = v;
-                    } else if (a.grad_dt == kBf16) {
-                        uint16_t* p = (uint16_t*)a.dw + o * a.ld_dw + i;
-                        store_elem(p, a.accumulate ? load_elem(p) + v : v);
-                    } else {
-                        float* p = (float*)a.dw + o * a.ld_dw + i;
-                        store_elem(p, a.accumulate ? load_elem(p) + v : v);
-                    }
+                    else
+                        put_grad(a.dw, o * a.ld_dw + i, v, a.grad_dt, a.accumulate);
                 }
         if (bias) {  // the threads that hold the same 8 columns
             float* s = (float*)lds;
@@ -276,17 +289,11 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void wgrad_kernel(Wgrad
 #pragma unroll
                 for (int r = 0; r < T / CA; ++r) v += s[r * BM + c];
                 const int64_t o = m0 + c;
-                if (o < a.out) {
-                    if (mine) {
-                        mine[a.out * a.in + o] = v;
-                    } else if (a.grad_dt == kBf16) {
-                        uint16_t* p = (uint16_t*)a.db + o;
-                        store_elem(p, a.accumulate ? load_elem(p) + v : v);
-                    } else {
-                        float* p = (float*)a.db + o;
-                        store_elem(p, a.accumulate ? load_elem(p) + v : v);
-                    }
-                }
+                if (o >= a.out) continue;
+                if (mine)
+                    mine[a.out * a.in + o] = v;
+                else
+                    put_grad(a.db, o, v, a.grad_dt, a.accumulate);
             }
             __syncthreads();
         }
@@ -355,7 +362,6 @@ __global__ __launch_bounds__(kBigThreads) void wgrad_big_kernel(WgradArgs a) {
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / (BN / WN), wn = wave % (BN / WN);
-    const int64_t total = (int64_t)a.tiles_m * a.tiles_n * a.splits;
     const int r4 = (lane >> 2) & 3, rbase = (lane >> 5) * 8 + r4;
     const int low = rbase * PA + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;  // PA == PB
     int offA[MT], offB[NT];
@@ -369,11 +375,25 @@ __global__ __launch_bounds__(kBigThreads) void wgrad_big_kernel(WgradArgs a) {
     const int putB = SA + tb * PB + ((cb * 32) ^ ((tb & 3) << 6)), putB2 = SA + tb * PB + ((cb * 32 + 16) ^ ((tb & 3) << 6));
     const int64_t sp = a.pitch / kCkptBlock;
 
-    for (int64_t item = blockIdx.x; item < total; item += gridDim.x) {
-        int tm, tn, part;
-        item_place(a, item, total, &tm, &tn, &part);
+    const uint32_t full = (uint32_t)a.full, rest = (uint32_t)a.rest, total = full + rest * (uint32_t)a.parts;
+    for (uint32_t item = blockIdx.x; item < total; item += gridDim.x) {
+        // the parts of one share of the rows lie together, tile by tile
+        uint32_t tile;
+        int64_t k0 = 0, k1 = a.slabs;
+        float* mine = nullptr;  // a part of a tile goes to its slot of the workspace
+        if (item < full) {
+            tile = by_xcd(item, full);
+        } else {
+            const uint32_t p = by_xcd(item - full, rest * (uint32_t)a.parts), part = uniform(p / rest);
+            tile = full + p - part * rest;
+            k0 = part * a.share;
+            k1 = k0 + a.share < k1 ? k0 + a.share : k1;
+            if (a.parts > 1) mine = a.part + p * kWgradSlot;
+        }
+        int tm, tn;
+        tile_place(a, tile, &tm, &tn);
         const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
-        const int64_t kb = part * a.span, ke = kb + a.span < a.rows ? kb + a.span : a.rows;
+        const int64_t kb = k0 * BK, ke = k1 * BK < a.rows ? k1 * BK : a.rows;
         const bool bias = a.db && tn == 0 && wn == 0;
         // columns behind the last are read from the last chunk and not stored
         const int64_t col_a = m0 + ca * 8 <= a.out - 8 ? m0 + ca * 8 : a.out - 8;
@@ -495,19 +515,18 @@ __global__ __launch_bounds__(kBigThreads) void wgrad_big_kernel(WgradArgs a) {
 
         // D's layout: lane & 31 is the column, element e the row
         // (e / 4) * 8 + (lane / 32) * 4 + e % 4.
-        float* const mine = a.splits > 1 ? a.part + (int64_t)part * (a.out * a.in + a.out) : nullptr;
         const int es = !mine && a.grad_dt == kBf16 ? 2 : 4;
-        const int64_t ld = mine ? a.in : a.ld_dw;
-        char* const base = (mine ? (char*)mine : (char*)a.dw) + ((m0 + wm * WM) * ld + n0 + wn * WN) * es;
+        const int64_t ld = mine ? BN : a.ld_dw;
+        char* const base = mine ? (char*)(mine + wm * WM * BN + wn * WN)
+                                : (char*)a.dw + ((m0 + wm * WM) * ld + n0 + wn * WN) * es;
         const int64_t o0 = a.out - m0 - wm * WM - (lane >> 5) * 4, i0 = a.in - n0 - wn * WN - (lane & 31);
         const int64_t vo = ((lane >> 5) * 4 * ld + (lane & 31)) * es;
         const bool add = a.accumulate && !mine;
-        if (m0 + BM <= a.out && n0 + BN <= a.in) {  // whole tiles: old values 16 at a time
-            char* const at = base + vo;
+        if (mine || (m0 + BM <= a.out && n0 + BN <= a.in)) {  // whole tiles: old values 16 at a time
             if (es == 4)
-                put_tile<float>(acc, (float*)at, ld, add);
+                put_tile<float>(acc, (float*)(base + vo), ld, add);
             else
-                put_tile<uint16_t>(acc, (uint16_t*)at, ld, add);
+                put_tile<uint16_t>(acc, (uint16_t*)(base + vo), ld, add);
         } else {
 #pragma unroll
             for (int m = 0; m < MT; ++m)
@@ -530,19 +549,50 @@ __global__ __launch_bounds__(kBigThreads) void wgrad_big_kernel(WgradArgs a) {
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
                 const float v = sums[m] + __shfl_xor(sums[m], 32, 64);
-                const int64_t o = m0 + wm * WM + m * 32 + (lane & 31);
-                if (lane >= 32 || o >= a.out) continue;
-                if (mine) {
-                    mine[a.out * a.in + o] = v;
-                } else if (a.grad_dt == kBf16) {
-                    uint16_t* p = (uint16_t*)a.db + o;
-                    store_elem(p, a.accumulate ? load_elem(p) + v : v);
-                } else {
-                    float* p = (float*)a.db + o;
-                    store_elem(p, a.accumulate ? load_elem(p) + v : v);
-                }
+                const int c = wm * WM + m * 32 + (lane & 31);
+                if (lane >= 32) continue;
+                if (mine)
+                    mine[BM * BN + c] = v;
+                else if (m0 + c < a.out)
+                    put_grad(a.db, m0 + c, v, a.grad_dt, a.accumulate);
             }
         }
+    }
+}
+
+// Sums the parts of the large form's rest tiles, in order: an item is four
+// rows of a tile, or (the last of its 65) the tile's part of the bias.
+__global__ __launch_bounds__(kThreads) void wgrad_big_join_kernel(WgradArgs a) {
+    constexpr int BM = kWgradBig, BN = kWgradBig;
+    for (int64_t item = blockIdx.x; item < a.rest * 65; item += gridDim.x) {
+        const int64_t t = item / 65;
+        const int q = (int)(item % 65);
+        int tm, tn;
+        tile_place(a, (uint32_t)(a.full + t), &tm, &tn);
+        const float* src = a.part + t * kWgradSlot + q * 4 * BN + threadIdx.x * (q < 64 ? 4 : 1);
+        const int64_t next = a.rest * kWgradSlot;
+        if (q == 64) {
+            if (!a.db || tn != 0) continue;
+            float v = 0.0f;
+            for (int64_t p = 0; p < a.parts; ++p) v += src[p * next];
+            const int64_t o = (int64_t)tm * BM + threadIdx.x;
+            if (o < a.out) put_grad(a.db, o, v, a.grad_dt, a.accumulate);
+            continue;
+        }
+        f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int64_t p = 0; p < a.parts; p += 4) {  // four parts' loads in flight
+            f32x4 w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                w[e] = p + e < a.parts ? (f32x4)*(const f32x4_a4*)(src + (p + e) * next) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v += w[e];
+        }
+        const int64_t o = (int64_t)tm * BM + q * 4 + threadIdx.x / 64, i = (int64_t)tn * BN + (threadIdx.x & 63) * 4;
+        if (o >= a.out) continue;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (i + e < a.in) put_grad(a.dw, o * a.ld_dw + i + e, v[e], a.grad_dt, a.accumulate);
     }
 }
 
@@ -587,37 +637,43 @@ __global__ __launch_bounds__(kThreads) void wgrad_join_kernel(WgradArgs a) {
         void* const out = bias ? a.db : a.dw;
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-            if (e >= left) continue;
-            if (a.grad_dt == kBf16) {
-                uint16_t* p = (uint16_t*)out + at + e;
-                store_elem(p, a.accumulate ? load_elem(p) + v[e] : v[e]);
-            } else {
-                float* p = (float*)out + at + e;
-                store_elem(p, a.accumulate ? load_elem(p) + v[e] : v[e]);
-            }
+            if (e < left) put_grad(out, at + e, v[e], a.grad_dt, a.accumulate);
         }
     }
 }
 
+template <int FMT>
+hipError_t run_large(const WgradArgs& a, hipStream_t stream) {
+    wgrad_big_kernel<FMT><<<grid_for(a.full + a.rest * a.parts), kBigThreads, 0, stream>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.parts == 1) return e;
+    wgrad_big_join_kernel<<<grid_for(a.rest * 65), kThreads, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
 template <int DD, int FMT>
-hipError_t run(const WgradArgs& a, bool big, hipStream_t stream) {
+hipError_t run_small(const WgradArgs& a, hipStream_t stream) {
     const int64_t total = (int64_t)a.tiles_m * a.tiles_n * a.splits;
-    const int grid = grid_for(total);
-    if (DD == kBf16 && big)
-        wgrad_big_kernel<FMT><<<grid, kBigThreads, 0, stream>>>(a);
+    wgrad_kernel<DD, FMT, kWgradTile, kWgradTile, 64, 64, DD == kBf16 ? 64 : 32><<<grid_for(total), 256, 0, stream>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.splits == 1) return e;
+    const int v = a.out * a.in >= (int64_t)1 << 20 ? 4 : 1;
+    const int64_t n = kThreads * v;
+    const int64_t items = a.out * ((a.in + n - 1) / n) + (a.db ? (a.out + n - 1) / n : 0);
+    if (v == 4)
+        wgrad_join_kernel<4><<<grid_for(items), kThreads, 0, stream>>>(a);
     else
-        wgrad_kernel<DD, FMT, kWgradTile, kWgradTile, 64, 64, DD == kBf16 ? 64 : 32><<<grid, 256, 0, stream>>>(a);
+        wgrad_join_kernel<1><<<grid_for(items), kThreads, 0, stream>>>(a);
     return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_ckpt_wgrad(const Wgrad& w, hipStream_t stream) {
-    const bool can = w.dy_dt == ZR_BF16 && w.out >= 8 && w.ld_dy <= (1 << 24) && w.in <= (1 << 24);
-    const WgradCut small = wgrad_cut(w.rows, w.out, w.in, false), large = wgrad_cut(w.rows, w.out, w.in, true);
-    const bool big = can && large.us < small.us;
-    const WgradCut cut = big ? large : small;
-    const int tile = big ? kWgradBig : kWgradTile;
+    const WgradCut cut = wgrad_cut(w.rows, w.out, w.in);
+    const WgradShare share = wgrad_share(w.rows, w.out, w.in);
+    const bool large = wgrad_can_be_large(w) && share.us < cut.us, e4m3 = w.format == ZR_CKPT_E4M3;
+    const int tile = large ? kWgradBig : kWgradTile;
     WgradArgs a{};
     a.dy = w.dy;
     a.pitch = ckpt_pitch(w.in);
@@ -632,21 +688,10 @@ hipError_t launch_ckpt_wgrad(const Wgrad& w, hipStream_t stream) {
     a.tiles_m = (int)((w.out + tile - 1) / tile);
     a.tiles_n = (int)((w.in + tile - 1) / tile);
     a.splits = cut.splits;
-    hipError_t e;
-    const bool e4m3 = w.format == ZR_CKPT_E4M3;
-    if (w.dy_dt == ZR_BF16)
-        e = e4m3 ? run<kBf16, kE4m3>(a, big, stream) : run<kBf16, kInt8>(a, big, stream);
-    else
-        e = e4m3 ? run<kFp32, kE4m3>(a, false, stream) : run<kFp32, kInt8>(a, false, stream);
-    if (e != hipSuccess || a.splits == 1) return e;
-    const int v = w.out * w.in >= (int64_t)1 << 20 ? 4 : 1;
-    const int64_t run_of = kThreads * v;
-    const int64_t items = w.out * ((w.in + run_of - 1) / run_of) + (a.db ? (w.out + run_of - 1) / run_of : 0);
-    if (v == 4)
-        wgrad_join_kernel<4><<<grid_for(items), kThreads, 0, stream>>>(a);
-    else
-        wgrad_join_kernel<1><<<grid_for(items), kThreads, 0, stream>>>(a);
-    return hipGetLastError();
+    a.slabs = share.slabs; a.full = share.full; a.rest = share.rest; a.parts = share.parts; a.share = share.share;
+    if (large) return e4m3 ? run_large<kE4m3>(a, stream) : run_large<kInt8>(a, stream);
+    if (w.dy_dt == ZR_BF16) return e4m3 ? run_small<kBf16, kE4m3>(a, stream) : run_small<kBf16, kInt8>(a, stream);
+    return e4m3 ? run_small<kFp32, kE4m3>(a, stream) : run_small<kFp32, kInt8>(a, stream);
 }
 
 }  // namespace zr

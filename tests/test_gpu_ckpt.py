@@ -197,13 +197,16 @@ def test_wgrad_exact_on_integers(rows, out, inn, dy_dt, fmt):
 
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("rows,out,inn", [(577, 136, 16384), (4160, 2056, 1090), (700, 4104, 4100), (65, 4104, 4100),
-                                          (700, 4097, 4100), (65, 4103, 4100), (130, 4351, 4100)])
+                                          (700, 4097, 4100), (65, 4103, 4100), (130, 4351, 4100),
+                                          (9000, 2056, 1090), (4000, 4300, 4100)])
 def test_wgrad_exact_on_integers_large(rows, out, inn, fmt):
-    """The large form, with ragged last tiles, slabs and parts, and rows that do not start or end on 16 bytes."""
+    """The large form, with ragged last tiles and slabs, tiles split by rows (the last two sizes), and rows
+    that do not start or end on 16 bytes."""
     rng = np.random.default_rng(rows)
     dy = rng.integers(-4, 5, (rows, out)).astype(np.float32)
     x = rng.integers(-8, 9, (rows, inn)).astype(np.float32)
-    want = dy.astype(np.float64).T @ x.astype(np.float64)
+    import torch
+    want = (torch.from_numpy(dy).cuda().double().t() @ torch.from_numpy(x).cuda().double()).cpu().numpy()
     old = rng.integers(-50, 50, (out, inn)).astype(np.float32)
     for gaps, grad_dt, add in (((0, 0), "fp32", False), ((8, 3), "fp32", True), ((1, 0), "fp32", True), ((0, 5), "bf16", True)):
         w, b = run_wgrad(dy, x, fmt, "bf16", grad_dt, True, old if add else None, old[:, 0].copy() if add else None, gaps)
