@@ -113,8 +113,62 @@ __device__ __forceinline__ void put_grad(void* p, int64_t at, float v, int grad_
     }
 }
 
+// A wave's accumulators to dW or the workspace; `at` is this lane's first
+// element, of which `rows` rows and `cols` columns from it exist (ALL: all of
+// the tile's). D's layout: lane & 31 is the column, element e the row
+// (e / 4) * 8 + (lane / 32) * 4 + e % 4. Old values are read 16 at a time, so
+// that they do not wait for each other.
+template <typename E, bool ALL, int MT, int NT>
+__device__ __forceinline__ void put_tile(const f32x16 (&acc)[MT][NT], E* at, int64_t ld, int64_t rows, int64_t cols,
+                                         bool add) {
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            float old[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) old[e] = 0.0f;
+            if (add) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int r = m * 32 + (e >> 2) * 8 + (e & 3);
+                    if (ALL || (r < rows && n * 32 < cols)) old[e] = load_elem(at + r * ld + n * 32);
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int r = m * 32 + (e >> 2) * 8 + (e & 3);
+                if (ALL || (r < rows && n * 32 < cols)) store_elem(at + r * ld + n * 32, acc[m][n][e] + old[e]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+}
+
+// The same for a wave's part of a tile that begins at element (o, i) of dW.
+template <int MT, int NT>
+__device__ __forceinline__ void put_dw(const f32x16 (&acc)[MT][NT], const WgradArgs& a, int64_t o, int64_t i, int lane) {
+    const bool all = o + MT * 32 <= a.out && i + NT * 32 <= a.in;
+    o += (lane >> 5) * 4;
+    i += lane & 31;
+    const int64_t at = o * a.ld_dw + i, rows = a.out - o, cols = a.in - i;
+    if (a.grad_dt == kBf16) {
+        uint16_t* p = (uint16_t*)a.dw + at;
+        if (all)
+            put_tile<uint16_t, true>(acc, p, a.ld_dw, rows, cols, a.accumulate);
+        else
+            put_tile<uint16_t, false>(acc, p, a.ld_dw, rows, cols, a.accumulate);
+    } else {
+        float* p = (float*)a.dw + at;
+        if (all)
+            put_tile<float, true>(acc, p, a.ld_dw, rows, cols, a.accumulate);
+        else
+            put_tile<float, false>(acc, p, a.ld_dw, rows, cols, a.accumulate);
+    }
+}
+
 template <int DD, int FMT, int BM, int BN, int WM, int WN, int BK>
-__global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void wgrad_kernel(WgradArgs a) {
+__global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wgrad_kernel(WgradArgs a) {
     constexpr int T = (BM / WM) * (BN / WN) * 64;  // threads
     constexpr int P = DD == kFp32 ? 3 : 1;         // bf16 terms of dY
     constexpr int PA = BM * 2, PB = BN * 2;        // LDS row bytes
@@ -261,24 +315,14 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void wgrad_kernel(Wgrad
             }
         }
 
-        // D's layout: lane & 31 is the column, element e the row
-        // (e / 4) * 8 + (lane / 32) * 4 + e % 4.
         float* const mine = a.splits > 1 ? a.part + (int64_t)part * (a.out * a.in + a.out) : nullptr;
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int64_t o = m0 + wm * WM + m * 32 + (e >> 2) * 8 + (lane >> 5) * 4 + (e & 3);
-                    const int64_t i = n0 + wn * WN + n * 32 + (lane & 31);
-                    if (o >= a.out || i >= a.in) continue;
-                    const float v = acc[m][n][e];
-                    if (mine)
-                        mine[o * a.in + i] = v;
-                    else
-                        put_grad(a.dw, o * a.ld_dw + i, v, a.grad_dt, a.accumulate);
-                }
+        const int64_t o0 = m0 + wm * WM, i0 = n0 + wn * WN;
+        if (mine) {
+            const int64_t o = o0 + (lane >> 5) * 4, i = i0 + (lane & 31);
+            put_tile<float, false>(acc, mine + o * a.in + i, a.in, a.out - o, a.in - i, false);
+        } else {
+            put_dw(acc, a, o0, i0, lane);
+        }
         if (bias) {  // the threads that hold the same 8 columns
             float* s = (float*)lds;
 #pragma unroll
@@ -326,30 +370,6 @@ __device__ __forceinline__ float sum2(uint32_t w, float v) {
     return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, w), one, v, false);
 }
 
-// A wave's accumulators to dW (or the workspace), all of them inside it; `at`
-// is this lane's first element.
-template <typename E, int MT, int NT>
-__device__ __forceinline__ void put_tile(const f32x16 (&acc)[MT][NT], E* at, int64_t ld, bool add) {
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            float old[16];
-            if (add) {
-#pragma unroll
-                for (int e = 0; e < 16; ++e) old[e] = load_elem(at + (m * 32 + (e >> 2) * 8 + (e & 3)) * ld + n * 32);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 16; ++e) old[e] = 0.0f;
-            }
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-                store_elem(at + (m * 32 + (e >> 2) * 8 + (e & 3)) * ld + n * 32, acc[m][n][e] + old[e]);
-            __builtin_amdgcn_sched_barrier(0);
-        }
-}
-
 template <int FMT>
 __global__ __launch_bounds__(kBigThreads) void wgrad_big_kernel(WgradArgs a) {
     constexpr int BM = kWgradBig, BN = kWgradBig, WM = 128, WN = 64, BK = kBigBK, T = kBigThreads;
@@ -364,15 +384,15 @@ __global__ __launch_bounds__(kBigThreads) void wgrad_big_kernel(WgradArgs a) {
     const int wm = wave / (BN / WN), wn = wave % (BN / WN);
     const int r4 = (lane >> 2) & 3, rbase = (lane >> 5) * 8 + r4;
     const int low = rbase * PA + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;  // PA == PB
-    int offA[MT], offB[NT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) offA[m] = low + (((wm * WM + m * 32) * 2) ^ (r4 << 6));
-#pragma unroll
-    for (int n = 0; n < NT; ++n) offB[n] = SA + low + (((wn * WN + n * 32) * 2) ^ (r4 << 6));
+    // operand m of dY lies at offA ^ (m << 6), n of X at offB ^ (n << 6): the
+    // windows' exchange has bits 6 and 7 to itself (wn's bit 7 is in offB's)
+    const int offA = (low | (r4 << 6)) + wm * WM * 2;
+    const int offB = SA + ((low | (r4 << 6)) ^ ((wn & 1) << 7)) + (wn >> 1) * 256;
+    static_assert(WM * 2 % 256 == 0 && WN == 64, "operand offsets");
     // where this thread's chunks go; rows of a round are a multiple of 4 apart
     const int ta = tid / (BM / 8), ca = tid % (BM / 8), tb = tid / (BN / 16), cb = tid % (BN / 16);
     const int putA = ta * PA + ((ca * 16) ^ ((ta & 3) << 6));
-    const int putB = SA + tb * PB + ((cb * 32) ^ ((tb & 3) << 6)), putB2 = SA + tb * PB + ((cb * 32 + 16) ^ ((tb & 3) << 6));
+    const int putB = SA + tb * PB + ((cb * 32) ^ ((tb & 3) << 6));
     const int64_t sp = a.pitch / kCkptBlock;
 
     const uint32_t full = (uint32_t)a.full, rest = (uint32_t)a.rest, total = full + rest * (uint32_t)a.parts;
@@ -403,8 +423,10 @@ __global__ __launch_bounds__(kBigThreads) void wgrad_big_kernel(WgradArgs a) {
         const bool ragged = m0 + BM > a.out && a.out % 8 != 0;
         const int late = (int)(m0 + ca * 8 - col_a) * 16;  // bits, 0 in other chunks
         const int64_t from = m0 <= a.out - 8 ? m0 : a.out - 8;  // no chunk starts before it
-        const uint32_t va = (uint32_t)(col_a - from) * 2, vb = (uint32_t)(col_b - n0), vs = vb / kCkptBlock;
-        const uint32_t la = (uint32_t)a.ld_dy * 2, lb = (uint32_t)a.pitch, ls = (uint32_t)sp;
+        const uint32_t va = (uint32_t)(col_a - from) * 2, vb = (uint32_t)(col_b - n0);
+        // byte offsets of rows within a slab, in 32 bits (a slab is below 2^31 bytes)
+        const uint32_t la = (uint32_t)a.ld_dy * 2, lb = (uint32_t)a.pitch;
+        const uint32_t ta_la = (uint32_t)ta * la, tb_lb = (uint32_t)tb * lb;
         const char* pa = (const char*)a.dy + (kb * a.ld_dy + from) * 2;
         const char* pb = a.codes + kb * a.pitch + n0;
         const uint8_t* ps = a.scales + kb * sp + n0 / kCkptBlock;
@@ -424,16 +446,21 @@ __global__ __launch_bounds__(kBigThreads) void wgrad_big_kernel(WgradArgs a) {
         int have = 0;            // rows of the slab in the registers
         auto fetch = [&] {
             have = left < BK ? (int)left : BK;
+            const uint32_t last_a = (uint32_t)(have - 1) * la, last_b = (uint32_t)(have - 1) * lb;
+            // opaque, so that the six rows' offsets are computed here and do not
+            // occupy registers through the loop
+            uint32_t row_a = ta_la, row_b = tb_lb;
+            asm volatile("" : "+v"(row_a), "+v"(row_b));
 #pragma unroll
             for (int j = 0; j < NA; ++j) {
-                const int t = ta + j * RA < have ? ta + j * RA : have - 1;
-                ra[j] = *(const u32x4_a2*)(pa + ((uint32_t)t * la + va));
+                const uint32_t row = row_a + (uint32_t)(j * RA) * la;
+                ra[j] = *(const u32x4_a2*)(pa + ((row < last_a ? row : last_a) + va));
             }
 #pragma unroll
             for (int j = 0; j < NB; ++j) {
-                const int t = tb + j * RB < have ? tb + j * RB : have - 1;
-                rb[j] = *(const u32x4*)(pb + ((uint32_t)t * lb + vb));
-                rs[j] = *(ps + ((uint32_t)t * ls + vs));
+                const uint32_t row = row_b + (uint32_t)(j * RB) * lb, at = (row < last_b ? row : last_b) + vb;
+                rb[j] = *(const u32x4*)(pb + at);
+                rs[j] = *(ps + at / kCkptBlock);  // a row of exponents is a 32nd of one of codes
             }
             pa += (int64_t)BK * a.ld_dy * 2;
             pb += (int64_t)BK * a.pitch;
@@ -450,7 +477,7 @@ __global__ __launch_bounds__(kBigThreads) void wgrad_big_kernel(WgradArgs a) {
             const bool here = tb + j * RB < have;
             decode16<FMT>(here ? rb[j] : u32x4{0, 0, 0, 0}, here ? rs[j] : 127u, w);
             *(u32x4*)(buf + putB + j * RB * PB) = u32x4{w[0], w[1], w[2], w[3]};
-            *(u32x4*)(buf + putB2 + j * RB * PB) = u32x4{w[4], w[5], w[6], w[7]};
+            *(u32x4*)(buf + putB + 16 + j * RB * PB) = u32x4{w[4], w[5], w[6], w[7]};
         };
         auto operand = [&](const char* at) {
             const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)at);
@@ -476,9 +503,9 @@ __global__ __launch_bounds__(kBigThreads) void wgrad_big_kernel(WgradArgs a) {
             // holds nothing of use: it is written and read, and not multiplied.
             bf16x8 fa[4], fb[2][NT];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) fb[0][n] = operand(lds + offB[n]);
-            fa[0] = operand(lds + offA[0]);
-            fa[1] = operand(lds + offA[1]);
+            for (int n = 0; n < NT; ++n) fb[0][n] = operand(lds + (offB ^ (n << 6)));
+            fa[0] = operand(lds + offA);
+            fa[1] = operand(lds + (offA ^ (1 << 6)));
             int cur = 0;
 #pragma unroll 1
             for (int k = 0; k < slabs; ++k) {
@@ -488,12 +515,12 @@ __global__ __launch_bounds__(kBigThreads) void wgrad_big_kernel(WgradArgs a) {
                 for (int i = 0; i < 16; ++i) {
                     if (i == 14) __syncthreads();
                     const int ahead = (i + 2) & 15;
-                    fa[ahead & 3] = operand((i < 14 ? buf : other) + offA[ahead & 3] + (ahead >> 2) * 16 * PA);
+                    fa[ahead & 3] = operand((i < 14 ? buf : other) + (offA ^ ((ahead & 3) << 6)) + (ahead >> 2) * 16 * PA);
                     if ((i & 3) == 2) {
                         const int ks = ((i >> 2) + 1) & 3;
 #pragma unroll
                         for (int n = 0; n < NT; ++n)
-                            fb[ks & 1][n] = operand((i < 14 ? buf : other) + offB[n] + ks * 16 * PB);
+                            fb[ks & 1][n] = operand((i < 14 ? buf : other) + (offB ^ (n << 6)) + ks * 16 * PB);
                     }
                     if (i >= 1 && i < 1 + NA) put_a(other, i - 1);
                     if (i >= 1 + NA && i < 1 + NA + NB) put_b(other, i - 1 - NA);
@@ -513,38 +540,10 @@ __global__ __launch_bounds__(kBigThreads) void wgrad_big_kernel(WgradArgs a) {
             __syncthreads();
         }
 
-        // D's layout: lane & 31 is the column, element e the row
-        // (e / 4) * 8 + (lane / 32) * 4 + e % 4.
-        const int es = !mine && a.grad_dt == kBf16 ? 2 : 4;
-        const int64_t ld = mine ? BN : a.ld_dw;
-        char* const base = mine ? (char*)(mine + wm * WM * BN + wn * WN)
-                                : (char*)a.dw + ((m0 + wm * WM) * ld + n0 + wn * WN) * es;
-        const int64_t o0 = a.out - m0 - wm * WM - (lane >> 5) * 4, i0 = a.in - n0 - wn * WN - (lane & 31);
-        const int64_t vo = ((lane >> 5) * 4 * ld + (lane & 31)) * es;
-        const bool add = a.accumulate && !mine;
-        if (mine || (m0 + BM <= a.out && n0 + BN <= a.in)) {  // whole tiles: old values 16 at a time
-            if (es == 4)
-                put_tile<float>(acc, (float*)(base + vo), ld, add);
-            else
-                put_tile<uint16_t>(acc, (uint16_t*)(base + vo), ld, add);
-        } else {
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int o = m * 32 + (e >> 2) * 8 + (e & 3);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        if (o >= o0 || n * 32 >= i0) continue;
-                        char* const p = base + (o * ld + n * 32) * es + vo;
-                        const float v = acc[m][n][e];
-                        if (es == 2)
-                            store_elem((uint16_t*)p, add ? load_elem((uint16_t*)p) + v : v);
-                        else
-                            store_elem((float*)p, add ? load_elem((float*)p) + v : v);
-                    }
-                }
-        }
+        if (mine)
+            put_tile<float, true>(acc, mine + (wm * WM + (lane >> 5) * 4) * BN + wn * WN + (lane & 31), BN, BM, BN, false);
+        else
+            put_dw(acc, a, m0 + wm * WM, n0 + wn * WN, lane);
         if (bias) {
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
@@ -590,6 +589,11 @@ __global__ __launch_bounds__(kThreads) void wgrad_big_join_kernel(WgradArgs a) {
         }
         const int64_t o = (int64_t)tm * BM + q * 4 + threadIdx.x / 64, i = (int64_t)tn * BN + (threadIdx.x & 63) * 4;
         if (o >= a.out) continue;
+        if (i + 4 <= a.in && a.grad_dt == kFp32) {
+            f32x4_a4* p = (f32x4_a4*)((float*)a.dw + o * a.ld_dw + i);
+            *p = a.accumulate ? (f32x4)*p + v : v;
+            continue;
+        }
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             if (i + e < a.in) put_grad(a.dw, o * a.ld_dw + i + e, v[e], a.grad_dt, a.accumulate);
