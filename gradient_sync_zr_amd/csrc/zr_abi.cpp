@@ -1096,7 +1096,7 @@ zr_status zr_layernorm_fwd(const void* x, zr_dtype x_dt, int64_t rows, int64_t c
 
 size_t zr_layernorm_workspace_bytes(int64_t rows, int64_t cols) {
     if (cols < 1 || cols > kMaxCols || !size_valid(rows, cols)) return 0;
-    return (size_t)layernorm_strips(rows, cols) * 2 * (size_t)cols * sizeof(float);
+    return (size_t)layernorm_workspace(rows, cols) * sizeof(float);
 }
 
 zr_status zr_layernorm_bwd(const void* dy, zr_dtype dy_dt, int64_t ld_dy, const void* x, zr_dtype x_dt, int64_t ld_x,

@@ -270,6 +270,17 @@ __device__ __forceinline__ void load_param8(const void* p, int dt, int c, int n,
     }
 }
 
+// A sum to an element of a gradient.
+__device__ __forceinline__ void put_grad(void* p, int64_t at, float v, int grad_dt, bool add) {
+    if (grad_dt == kBf16) {
+        uint16_t* q = (uint16_t*)p + at;
+        store_elem(q, add ? load_elem(q) + v : v);
+    } else {
+        float* q = (float*)p + at;
+        store_elem(q, add ? load_elem(q) + v : v);
+    }
+}
+
 // ------------------------------------------------------------- reductions
 // Sums over the lanes of a row within a wave: DPP steps inside 16 lanes, then
 // two exchanges across the wave.

@@ -191,16 +191,25 @@ struct NormBwd {
     int64_t rows, cols, ld_dy, ld_x, ld_dx;
     void *dx, *dweight, *dbias;
     int accumulate, add_dx;
-    void* workspace;  // layernorm_strips(rows, cols) * 2 * cols floats
+    void* workspace;  // of layernorm_workspace() floats
 };
 ZR_KERNELS hipError_t launch_layernorm_bwd(const NormBwd& f, hipStream_t stream);
 // Strips of rows that a backward pass leaves partial parameter gradients of:
 // one block each, as many as the chip holds at once, and no more than there
-// are steps of rows (a block takes 16, 4 or 1 rows at once).
+// are steps of rows (a block takes 16, 4 or 1 rows at once). Below kNormOne
+// elements one block walks over all rows and writes the gradients itself: it
+// takes longer than several would, but saves the joining launch.
+constexpr int64_t kNormOne = 16384;
 inline int layernorm_strips(int64_t rows, int64_t cols) {
+    if (rows > 0 && rows * cols <= kNormOne) return 1;
     const int64_t per = cols <= 128 ? 16 : (cols <= 1024 ? 4 : 1), n = (rows + per - 1) / per;
     const int64_t places = cols <= 4096 ? 512 : 256, most = tuning().max_grid < places ? tuning().max_grid : places;
     return (int)(n < most ? n : most);
+}
+// Floats of workspace for them.
+inline int64_t layernorm_workspace(int64_t rows, int64_t cols) {
+    const int64_t strips = layernorm_strips(rows, cols);
+    return strips > 1 || cols > 12288 ? strips * 2 * cols : 0;
 }
 
 ZR_KERNELS hipError_t launch_ckpt_pack(const void* x, zr_dtype dt, int64_t rows, int64_t cols, int64_t ld, zr_dtype fmt,

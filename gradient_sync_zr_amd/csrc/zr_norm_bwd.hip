@@ -2,7 +2,7 @@
 // checkpoints. With xh = (x - mean) * rstd and g = dy * w, per row of n columns:
 //     dx = rstd * (g - sum(g) / n - xh * sum(g * xh) / n)
 //     dw = sum over rows of dy * xh,  db = sum over rows of dy
-// all in fp32. Rows too wide for registers (over 16384 columns) are read again
+// all in fp32. Rows too wide for registers (over 12288 columns) are read again
 // from memory in each pass.
 //
 // The weight's and the bias's gradient are column sums over all rows. A block
@@ -26,7 +26,9 @@ struct BwdArgs {
     const void *dy, *x, *w;
     const float *mean, *rstd;
     char* dx;
-    float* part;  // [strips][2][cols], or null: no parameter gradients
+    float* part;  // [strips][2][cols], or null: no parameter gradients or those below
+    void *dw, *db;  // written by the only block, or null
+    int grad_dt, accumulate;
     int64_t rows, cols, ld_dy, ld_x, ld_dx;
     int param_dt, dx_dt, add_dx;
 };
@@ -137,10 +139,12 @@ __global__ __launch_bounds__(norm_block(TPR)) void bwd_kernel(BwdArgs a) {
             store8(out, a.dx_dt, c, n, g[v]);
         }
     }
-    if (!a.part) return;
-    float* out = a.part + (int64_t)blockIdx.x * 2 * a.cols;
+    // the block's sums: to the workspace, or as the gradients
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
+        void* const grad = which ? a.db : a.dw;
+        if (!a.part && !grad) continue;
+        float* const out = a.part ? a.part + ((int64_t)blockIdx.x * 2 + which) * a.cols : nullptr;
         if constexpr (G > 1) {
             __syncthreads();
 #pragma unroll
@@ -152,13 +156,25 @@ __global__ __launch_bounds__(norm_block(TPR)) void bwd_kernel(BwdArgs a) {
                 float t = 0.0f;
 #pragma unroll
                 for (int r = 0; r < G; ++r) t += join[r][c];
-                out[which * a.cols + c] = t;
+                if (out)
+                    out[c] = t;
+                else
+                    put_grad(grad, c, t, a.grad_dt, a.accumulate);
             }
         } else {
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
                 const int c = (v * TPR + lane) * 8, n = existing(a.cols, c);
-                if (n > 0) store8((char*)(out + which * a.cols), kFp32, c, n, which ? db[v] : dw[v]);
+                if (n == 0) continue;
+                if (out) {
+                    store8((char*)out, kFp32, c, n, which ? db[v] : dw[v]);
+                } else {
+                    float old[8];
+                    load_param8(a.accumulate ? grad : nullptr, a.grad_dt, c, n, 0.0f, old);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) old[e] += which ? db[v][e] : dw[v][e];
+                    store8((char*)grad, a.grad_dt, c, n, old);
+                }
             }
         }
     }
@@ -271,14 +287,7 @@ __global__ __launch_bounds__(1024) void bwd_join_kernel(const float* part, int s
 #pragma unroll
             for (int g = 0; g < 16; ++g) s += sum[g][lane];
             void* out = at < cols ? dw : db;
-            const int64_t o = at < cols ? at : at - cols;
-            if (out && grad_dt == kBf16) {
-                uint16_t* q = (uint16_t*)out + o;
-                store_elem(q, accumulate ? load_elem(q) + s : s);
-            } else if (out) {
-                float* q = (float*)out + o;
-                store_elem(q, accumulate ? load_elem(q) + s : s);
-            }
+            if (out) put_grad(out, at < cols ? at : at - cols, s, grad_dt, accumulate);
         }
     }
 }
@@ -324,8 +333,13 @@ hipError_t launch_layernorm_bwd(const NormBwd& f, hipStream_t stream) {
     a.rows = f.rows; a.cols = f.cols; a.ld_dy = f.ld_dy; a.ld_x = f.ld_x; a.ld_dx = f.ld_dx;
     a.param_dt = f.param_dt; a.dx_dt = f.dx_dt; a.add_dx = f.add_dx;
     const bool grads = f.dweight || f.dbias;
-    a.part = grads ? (float*)f.workspace : nullptr;
     const int strips = layernorm_strips(f.rows, f.cols);
+    const bool joined = layernorm_workspace(f.rows, f.cols) > 0 || strips == 0;
+    a.part = grads && joined ? (float*)f.workspace : nullptr;
+    if (!joined) {
+        a.dw = f.dweight; a.db = f.dbias;
+        a.grad_dt = f.grad_dt; a.accumulate = f.accumulate;
+    }
     hipError_t e = hipSuccess;
     if (strips > 0) {
         switch (f.x_dt) {
@@ -336,7 +350,7 @@ hipError_t launch_layernorm_bwd(const NormBwd& f, hipStream_t stream) {
         }
         if (e != hipSuccess) return e;
     }
-    if (!grads) return e;
+    if (!grads || !joined) return e;
     const int64_t tiles = (2 * f.cols + 63) / 64;
     bwd_join_kernel<<<grid_for(tiles), 1024, 0, stream>>>((const float*)f.workspace, strips, f.cols, f.dweight, f.dbias,
                                                           f.grad_dt, f.accumulate);

@@ -102,17 +102,6 @@ __device__ __forceinline__ void tile_place(const WgradArgs& a, uint32_t t, int* 
     *tn = uniform(n);
 }
 
-// A sum to an element of a gradient.
-__device__ __forceinline__ void put_grad(void* p, int64_t at, float v, int grad_dt, bool add) {
-    if (grad_dt == kBf16) {
-        uint16_t* q = (uint16_t*)p + at;
-        store_elem(q, add ? load_elem(q) + v : v);
-    } else {
-        float* q = (float*)p + at;
-        store_elem(q, add ? load_elem(q) + v : v);
-    }
-}
-
 // A wave's accumulators to dW or the workspace; `at` is this lane's first
 // element, of which `rows` rows and `cols` columns from it exist (ALL: all of
 // the tile's). D's layout: lane & 31 is the column, element e the row

@@ -101,7 +101,7 @@ def test_forward_refusals():
 
 
 def bwd(**kw):
-    a = dict(dy=A, x=B, rows=10, cols=100, mean=C, rstd=C + 4096, weight=D, dx=E, dweight=F, dbias=F + 4096,
+    a = dict(dy=A, x=B, rows=300, cols=100, mean=C, rstd=C + 4096, weight=D, dx=E, dweight=F, dbias=F + 4096,
              workspace=(G, 1 << 30), dy_dtype=BF, x_dtype=BF, dx_dtype=BF, param_dtype=BF, grad_dtype=FP, stream=0)
     a.update(kw)
     zr.zr_layernorm_bwd(**a)
@@ -118,7 +118,7 @@ def test_backward_refusals():
     for n in ("dy_dtype", "param_dtype", "dx_dtype", "grad_dtype"):
         expect(zr.ZR_ERR_UNSUPPORTED, bwd, **{n: zr.ZR_CKPT_E4M3})
     expect(zr.ZR_ERR_UNSUPPORTED, bwd, x_dtype=11)
-    need = zr.zr_layernorm_workspace_bytes(10, 100)
+    need = zr.zr_layernorm_workspace_bytes(300, 100)
     assert need > 0
     expect(zr.ZR_ERR_WORKSPACE, bwd, workspace=None)
     expect(zr.ZR_ERR_WORKSPACE, bwd, workspace=(G, need - 1))
