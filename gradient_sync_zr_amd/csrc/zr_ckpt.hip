@@ -44,12 +44,13 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(const void* x, int64_t l
             row[k] = row0 + dr;
             const int64_t left = cols - c[k];
             n[k] = row[k] < rows ? (left >= 8 ? 8 : (left > 0 ? (int)left : 0)) : -1;
-            if (n[k] >= 0) raw[k] = load8<DT>(row_at<DT>(x, ld, rows, cols, row[k]), c[k], n[k]);
+            if (n[k] >= 0) raw[k] = fetch8<DT>(row_at<DT>(x, ld, rows, cols, row[k]), c[k], n[k]);
         }
 #pragma unroll
         for (int k = 0; k < kCkptVecs; ++k) {
             if (n[k] < 0) continue;  // rows end with whole blocks, so a block's lanes leave together
             float f[8];
+            settle8(raw[k], c[k], n[k]);
             widen8(raw[k], f);
             ckpt_store8(ckpt + row[k] * pitch, (uint8_t*)ckpt + rows * pitch + row[k] * (pitch / kCkptBlock), c[k], f,
                         e4m3 != 0);
@@ -76,7 +77,7 @@ __global__ __launch_bounds__(kThreads) void unpack_kernel(const char* ckpt, int6
             row[k] = row0 + dr;
             const int64_t left = cols - c[k];
             n[k] = row[k] < rows ? (left >= 8 ? 8 : (left > 0 ? (int)left : 0)) : 0;
-            if (n[k] > 0) raw[k] = load8<FMT>(row_at<FMT>(ckpt, 0, rows, cols, row[k]), c[k], n[k]);
+            if (n[k] > 0) raw[k] = fetch8<FMT>(row_at<FMT>(ckpt, 0, rows, cols, row[k]), c[k], n[k]);
         }
 #pragma unroll
         for (int k = 0; k < kCkptVecs; ++k) {

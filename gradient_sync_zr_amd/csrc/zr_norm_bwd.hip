@@ -52,6 +52,8 @@ template <int XD, int DD, int TPR, int NV>
 __global__ __launch_bounds__(norm_block(TPR)) void bwd_kernel(BwdArgs a) {
     constexpr int B = norm_block(TPR), G = B / TPR;
     constexpr int C = TPR * NV * 8;  // columns that a row's lanes cover
+    // three vectors with one source in fp32 leave no registers for old dx
+    constexpr bool LATE = NV == 3 && (XD == kFp32 || DD == kFp32);
     __shared__ float red[2][B / 64][2];
     __shared__ float join[G > 1 ? G : 1][G > 1 ? C : 1];
     const int lane = threadIdx.x % TPR, group = row_group<TPR>();
@@ -73,8 +75,8 @@ __global__ __launch_bounds__(norm_block(TPR)) void bwd_kernel(BwdArgs a) {
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int c = (v * TPR + lane) * 8, n = existing(a.cols, c);
-            rx[v] = load8<XD>(px, c, n);
-            rd[v] = load8<DD>(pd, c, n);
+            rx[v] = fetch8<XD>(px, c, n);
+            rd[v] = fetch8<DD>(pd, c, n);
         }
         mean_next = a.mean[row];
         rstd_next = a.rstd[row];
@@ -85,22 +87,27 @@ __global__ __launch_bounds__(norm_block(TPR)) void bwd_kernel(BwdArgs a) {
     for (int64_t row = first; row < a.rows; row += step) {
         const float mean = mean_next, rstd = rstd_next;
         char* out = a.dx + row * a.ld_dx * dx_es;
-        Raw8<kFp32> old[NV];  // dx before; bf16 in the first half
-        if (a.add_dx) {  // in flight during the sums, and waited for before the next row's loads
+        // dx before (bf16 in the first half): in flight during the sums, and waited
+        // for before the next row's loads
+        Raw8<kFp32> old[LATE ? 1 : NV];
+        auto fetch_old = [&](int v) {
+            const int c = (v * TPR + lane) * 8, n = existing(a.cols, c);
+            if (a.dx_dt == kBf16)
+                old[LATE ? 0 : v].a = __builtin_bit_cast(f32x4, fetch8<kBf16>({out, nullptr}, c, n).v);
+            else
+                old[LATE ? 0 : v] = fetch8<kFp32>({out, nullptr}, c, n);
+        };
+        if (!LATE && a.add_dx) {
 #pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                const int c = (v * TPR + lane) * 8, n = existing(a.cols, c);
-                if (a.dx_dt == kBf16)
-                    old[v].a = __builtin_bit_cast(f32x4, load8<kBf16>({out, nullptr}, c, n).v);
-                else
-                    old[v] = load8<kFp32>({out, nullptr}, c, n);
-            }
+            for (int v = 0; v < NV; ++v) fetch_old(v);
         }
         float xh[NV][8], g[NV][8];
         float s[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int c = (v * TPR + lane) * 8, n = existing(a.cols, c);
+            settle8(rx[v], c, n);
+            settle8(rd[v], c, n);
             centered8<XD>(rx[v], mean, xh[v]);
             widen8(rd[v], g[v]);
             if (n < 8) keep_first(xh[v], n);
@@ -129,10 +136,15 @@ __global__ __launch_bounds__(norm_block(TPR)) void bwd_kernel(BwdArgs a) {
             for (int e = 0; e < 8; ++e) g[v][e] = __builtin_fmaf(g[v][e], rstd, __builtin_fmaf(xh[v][e], k1, k2));
             if (a.add_dx) {
                 float o[8];
-                if (a.dx_dt == kBf16)
-                    widen8(Raw8<kBf16>{__builtin_bit_cast(u32x4, old[v].a)}, o);
-                else
-                    widen8(old[v], o);
+                if (LATE) fetch_old(v);
+                if (a.dx_dt == kBf16) {
+                    Raw8<kBf16> h{__builtin_bit_cast(u32x4, old[LATE ? 0 : v].a)};
+                    settle8(h, c, n);
+                    widen8(h, o);
+                } else {
+                    settle8(old[LATE ? 0 : v], c, n);
+                    widen8(old[LATE ? 0 : v], o);
+                }
 #pragma unroll
                 for (int e = 0; e < 8; ++e) g[v][e] += o[e];
             }

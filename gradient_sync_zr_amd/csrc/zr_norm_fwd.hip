@@ -69,7 +69,7 @@ __global__ __launch_bounds__(norm_block(TPR)) void fwd_kernel(FwdArgs a) {
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int c = (v * TPR + lane) * 8;
-            raw[v] = load8<XD>(p, c, existing(a.cols, c));
+            raw[v] = fetch8<XD>(p, c, existing(a.cols, c));
         }
     };
     const int64_t first = (int64_t)blockIdx.x * G + group, step = (int64_t)gridDim.x * G;
@@ -82,8 +82,9 @@ __global__ __launch_bounds__(norm_block(TPR)) void fwd_kernel(FwdArgs a) {
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int c = (v * TPR + lane) * 8, n = existing(a.cols, c);
+            settle8(raw[v], c, n);
             widen8(raw[v], f[v]);
-            if (n < 8) keep_first(f[v], n);
+            if (XD > kFp32 && n < 8) keep_first(f[v], n);
 #pragma unroll
             for (int e = 0; e < 8; ++e) s[0] += f[v][e];
         }

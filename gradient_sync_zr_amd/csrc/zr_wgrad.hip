@@ -201,6 +201,8 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wgrad_kernel(Wg
                 for (int e = 0; e < 16; ++e) acc[m][n][e] = 0.0f;
         float sums[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 
+        const int64_t behind_chunk = a.out - (m0 + (tid % CA) * 8);
+        const int chunk = behind_chunk >= 8 ? 8 : (behind_chunk > 0 ? (int)behind_chunk : 0);  // columns of its chunks
         Raw8<DD> ra[NA];
         u32x4 rb[NB];
         uint32_t rs[NB];
@@ -209,9 +211,8 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wgrad_kernel(Wg
             for (int j = 0; j < NA; ++j) {
                 const int id = tid + j * T;
                 const int64_t row = k + id / CA, col = m0 + (id % CA) * 8;
-                const int64_t left = row < ke ? a.out - col : 0;
-                const int n = left >= 8 ? 8 : (left > 0 ? (int)left : 0);
-                ra[j] = load8<DD>({(const char*)a.dy + row * a.ld_dy * (DD == kBf16 ? 2 : 4), nullptr}, (int)col, n);
+                const int n = row < ke ? chunk : 0;
+                ra[j] = fetch8<DD>({(const char*)a.dy + row * a.ld_dy * (DD == kBf16 ? 2 : 4), nullptr}, (int)col, n);
             }
 #pragma unroll
             for (int j = 0; j < NB; ++j) {
@@ -230,6 +231,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wgrad_kernel(Wg
             for (int j = 0; j < NA; ++j) {
                 const int id = tid + j * T, t = id / CA, c = id % CA;
                 char* at = buf + t * PA + ((c * 16) ^ ((t & 3) << 6));
+                settle8(ra[j], (int)(m0 + c * 8), chunk);
                 if constexpr (DD == kBf16) {
                     *(u32x4*)at = ra[j].v;
                 } else {
@@ -339,19 +341,6 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wgrad_kernel(Wg
 // read 256 KB. Each wave's 128 fp32 accumulators leave 128 registers for
 // operands and the next slab.
 constexpr int kBigThreads = 512, kBigBK = 64;
-
-// The 128 bits behind the first `bits` of v (zeros after them); 128 and more: none.
-__device__ __forceinline__ u32x4 behind(const u32x4& v, int bits) {
-    uint64_t lo = ((uint64_t)v.y << 32) | v.x, hi = ((uint64_t)v.w << 32) | v.z;
-    if (bits >= 64) {
-        lo = hi;
-        hi = 0;
-    }
-    const int by = bits & 63;
-    if (by) lo = (lo >> by) | (hi << (64 - by));
-    hi >>= by;
-    return bits >= 128 ? u32x4{0, 0, 0, 0} : u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
-}
 
 // v plus the two bf16 values of a word.
 __device__ __forceinline__ float sum2(uint32_t w, float v) {
