@@ -631,8 +631,9 @@ size_t zr_layernorm_workspace_bytes(int64_t rows, int64_t cols);
  *  flags      ZR_ACCUMULATE: dweight and dbias are added to (old + new in
  *             fp32); ZR_ADD_DX: dx is added to, as where a residual stream's
  *             gradient passes by the norm
- *  workspace  4-byte aligned, zr_layernorm_workspace_bytes(rows, cols) bytes,
- *             if dweight or dbias is given (ZR_ERR_WORKSPACE). Calls on one
+ *  workspace  4-byte aligned, zr_layernorm_workspace_bytes(rows, cols) bytes
+ *             (NULL where that is 0), if dweight or dbias is given
+ *             (ZR_ERR_WORKSPACE). Calls on one
  *             stream may share it; calls, or captured graphs, that may run at
  *             the same time must not
  * rows == 0: dx is untouched, dweight and dbias become 0 (or stay).

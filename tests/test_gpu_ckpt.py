@@ -261,3 +261,25 @@ def test_wgrad_without_rows_and_values_that_are_not_finite(fmt):
         w, b = run_wgrad(d2, x2, fmt, dt, "fp32", True)
         assert (w[7] == np.inf).all() and np.isfinite(np.delete(w, 7, 0)).all()
         assert b[7] == np.inf and np.isfinite(np.delete(b, 7)).all()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_wgrad_offsets_past_32_bits(dt):
+    """dy of more than 2^32 elements. Integers, and sums that wander far below 2^24, so exact in fp32."""
+    import torch
+    rows, out, inn = 1100000, 4096, 40
+    dy = torch.empty(rows, out, dtype=torch.bfloat16 if dt == "bf16" else torch.float32, device="cuda")
+    x = torch.randint(-8, 9, (rows, inn), device="cuda").float()
+    want = torch.zeros(out, inn, dtype=torch.float64, device="cuda")
+    step = 110000
+    for r in range(0, rows, step):
+        part = torch.randint(-4, 5, (step, out), device="cuda", dtype=torch.int8).float()
+        dy[r:r + step] = part
+        want += (part.t() @ x[r:r + step]).double()     # exact in fp32: at most 32 x 110,000
+        del part
+    ck = torch.empty(zr().zr_ckpt_bytes(rows, inn), dtype=torch.uint8, device="cuda")
+    zr().zr_ckpt_pack(x, rows, inn, ck, format=ref.INT8)
+    dw = torch.empty(out, inn, device="cuda")
+    ws = torch.empty(zr().zr_ckpt_wgrad_workspace_bytes(rows, out, inn) + 1, dtype=torch.uint8, device="cuda")
+    zr().zr_ckpt_wgrad(dy, ck, rows, out, inn, dw, format=ref.INT8, workspace=ws)
+    assert torch.equal(dw.double(), want)

@@ -10,8 +10,7 @@ most 64 adds in line (a lane's own at most 32, then 6 across a wave and at most
    d <= 0.002 of the deviation, as in these inputs;
  * y: |w| rstd (66 u mean|x| + 2 u |x - mean|) + 40 u |w xh| + 2 u |y| + 2 u |w xh|,
    and half a step of y's type;
- * dx: written out below in the same way; dw, db: a strip's rows, 16 rows of a
-   block, 32 strips in line and 16 more: (rows / 512 + 70) u of the sum of
+ * dx: written out below in the same way; dw, db: column_adds() u of the sum of
    magnitudes, and half a step of their type.
 """
 import numpy as np
@@ -181,6 +180,15 @@ def backward64(dy, x, mean, rstd, w):
     return dx, (dy * xh).sum(0), dy.sum(0), bdx, (np.abs(dy * xh)).sum(0), np.abs(dy).sum(0)
 
 
+def column_adds(rows, cols):
+    """Adds in line of a column's sum: a block takes `per` rows at once, each lane group the strip's share of
+    them, then the groups' sums are added, then the strips' (16 groups of lanes, each every 16th, then those)."""
+    per = 16 if cols <= 128 else 4 if cols <= 1024 else 1
+    steps = -(-rows // per)
+    strips = 1 if rows * cols <= 16384 else min(steps, 512 if cols <= 4096 else 256)
+    return -(-steps // strips) + per + (-(-strips // 16) + 16 if strips > 1 else 0)
+
+
 @pytest.mark.parametrize("cols", COLS)
 def test_backward(cols):
     import torch
@@ -225,7 +233,8 @@ def test_backward(cols):
         assert (np.abs(got - dx) <= bdx + HALF[dd] * (np.abs(dx) + bdx)).all(), k
         for g, want, mag, o in ((gdw, dw, bw, ow), (gdb, db, bb, ob)):
             want = want + (o if acc else 0)
-            lim = (rows / 512 + 73) * U * mag + (2 * U * (mag + np.abs(o)) if acc else 0)
+            # three roundings of a term (x - mean, times rstd, times dy) and the column's adds
+            lim = (column_adds(rows, cols) + 3) * U * mag + (2 * U * (mag + np.abs(o)) if acc else 0)
             assert (np.abs(take(g, gd) - want) <= lim + HALF[gd] * (np.abs(want) + lim)).all(), k
         for g in (gdx, gdw, gdb, gdy, gm, gr):
             assert g.guards_intact()
@@ -286,3 +295,30 @@ def test_backward_in_place_apart_and_without_rows(cols):
     assert torch.equal(w2, dw)
     z.zr_layernorm_bwd(dy[:0], x[:0], 0, cols, mean[:0], rstd[:0], dweight=w2, dbias=b2, workspace=ws)
     assert not w2.any() and not b2.any()
+
+
+def test_offsets_past_32_bits():
+    """More than 2^32 elements, in registers and in the wide form: the last rows equal a call of their own."""
+    import torch
+    z = zr()
+    for rows, cols in ((530000, 8200), (66000, 65600)):
+        x = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda")
+        for r in range(0, rows, rows // 10):
+            x[r:r + rows // 10].normal_()
+        y = torch.empty_like(x)
+        ck = torch.empty(z.zr_ckpt_bytes(rows, cols), dtype=torch.uint8, device="cuda")
+        mean, rstd = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+        z.zr_layernorm_fwd(x, rows, cols, y, mean=mean, rstd=rstd, ckpt_x=ck)
+        last, ly = x[-3:].clone(), torch.empty(3, cols, dtype=torch.bfloat16, device="cuda")
+        lc = torch.empty(z.zr_ckpt_bytes(3, cols), dtype=torch.uint8, device="cuda")
+        lm, lr = torch.empty(3, device="cuda"), torch.empty(3, device="cuda")
+        z.zr_layernorm_fwd(last, 3, cols, ly, mean=lm, rstd=lr, ckpt_x=lc)
+        p = ref.pitch(cols)
+        assert torch.equal(y[-3:], ly) and torch.equal(mean[-3:], lm) and torch.equal(rstd[-3:], lr)
+        assert torch.equal(ck[(rows - 3) * p: rows * p], lc[:3 * p]) and torch.equal(ck[rows * p + (rows - 3) * (p // 32):], lc[3 * p:])
+        z.zr_layernorm_bwd(y, ck, rows, cols, mean, rstd, dx=x, x_dtype=ref.E4M3)
+        ldx = torch.empty_like(ly)
+        z.zr_layernorm_bwd(ly, lc, 3, cols, lm, lr, dx=ldx, x_dtype=ref.E4M3)
+        assert torch.equal(x[-3:], ldx)
+        del x, y, ck
+        torch.cuda.empty_cache()
