@@ -44,7 +44,7 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(const void* x, int64_t l
             row[k] = row0 + dr;
             const int64_t left = cols - c[k];
             n[k] = row[k] < rows ? (left >= 8 ? 8 : (left > 0 ? (int)left : 0)) : -1;
-            if (n[k] >= 0) raw[k] = fetch8<DT>(row_at<DT>(x, ld, rows, cols, row[k]), c[k], n[k]);
+            if (n[k] >= 0) raw[k] = fetch8<DT, true>(row_at<DT>(x, ld, rows, cols, row[k]), c[k], n[k]);
         }
 #pragma unroll
         for (int k = 0; k < kCkptVecs; ++k) {
@@ -52,8 +52,13 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(const void* x, int64_t l
             float f[8];
             settle8(raw[k], c[k], n[k]);
             widen8(raw[k], f);
+            uint32_t amax;
+            if constexpr (DT == kBf16)
+                amax = block_amax(raw[k].v);
+            else
+                amax = block_amax(f);
             ckpt_store8(ckpt + row[k] * pitch, (uint8_t*)ckpt + rows * pitch + row[k] * (pitch / kCkptBlock), c[k], f,
-                        e4m3 != 0);
+                        amax, e4m3 != 0);
         }
     }
 }
@@ -77,14 +82,14 @@ __global__ __launch_bounds__(kThreads) void unpack_kernel(const char* ckpt, int6
             row[k] = row0 + dr;
             const int64_t left = cols - c[k];
             n[k] = row[k] < rows ? (left >= 8 ? 8 : (left > 0 ? (int)left : 0)) : 0;
-            if (n[k] > 0) raw[k] = fetch8<FMT>(row_at<FMT>(ckpt, 0, rows, cols, row[k]), c[k], n[k]);
+            if (n[k] > 0) raw[k] = fetch8<FMT, true>(row_at<FMT>(ckpt, 0, rows, cols, row[k]), c[k], n[k]);
         }
 #pragma unroll
         for (int k = 0; k < kCkptVecs; ++k) {
             if (n[k] == 0) continue;
             float f[8];
             widen8(raw[k], f);
-            store8(x + row[k] * ld * es, dt, c[k], n[k], f);
+            store8<true>(x + row[k] * ld * es, dt, c[k], n[k], f);
         }
     }
 }

@@ -39,6 +39,33 @@ typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
 typedef f32x4 f32x4_a4 __attribute__((aligned(4)));
 
+// 16 bytes of bf16 or fp32 elements at the elements' alignment; NT: past the
+// caches. (A template over these types would drop their alignment.)
+template <bool NT>
+__device__ __forceinline__ u32x4 ld16(const uint16_t* p) {
+    const u32x4_a2* q = (const u32x4_a2*)p;
+    return NT ? (u32x4)__builtin_nontemporal_load(q) : (u32x4)*q;
+}
+template <bool NT>
+__device__ __forceinline__ f32x4 ld32(const float* p) {
+    const f32x4_a4* q = (const f32x4_a4*)p;
+    return NT ? (f32x4)__builtin_nontemporal_load(q) : (f32x4)*q;
+}
+template <bool NT>
+__device__ __forceinline__ void st16(uint16_t* p, u32x4 v) {
+    if constexpr (NT)
+        __builtin_nontemporal_store(v, (u32x4_a2*)p);
+    else
+        *(u32x4_a2*)p = v;
+}
+template <bool NT>
+__device__ __forceinline__ void st32(float* p, f32x4 v) {
+    if constexpr (NT)
+        __builtin_nontemporal_store(v, (f32x4_a4*)p);
+    else
+        *(f32x4_a4*)p = v;
+}
+
 // Formats and sources as the kernels' template arguments (zr_dtype values).
 constexpr int kBf16 = ZR_BF16, kFp32 = ZR_FP32, kE4m3 = ZR_CKPT_E4M3, kInt8 = ZR_CKPT_INT8;
 
@@ -72,22 +99,30 @@ __device__ __forceinline__ u32x2 ckpt_encode8(const float f[8], uint32_t s, bool
     float v[8];
     u32x2 q;
     if (e4m3) {
-        const float lim = s == 247u ? 240.0f : 448.0f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = __builtin_amdgcn_fmed3f(f[e] * inv, -lim, lim);
+        for (int e = 0; e < 8; ++e) v[e] = f[e] * inv;
+        if (s == 247u) {  // 248 and more would round to 2^128
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = __builtin_amdgcn_fmed3f(v[e], -240.0f, 240.0f);
+        }
         int a = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
         a = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], a, true);
         int b = __builtin_amdgcn_cvt_pk_fp8_f32(v[4], v[5], 0, false);
         b = __builtin_amdgcn_cvt_pk_fp8_f32(v[6], v[7], b, true);
         q = u32x2{(uint32_t)a, (uint32_t)b};
     } else {
-        const float lim = s == 249u ? 63.0f : 127.0f;
         uint32_t w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = f[e] * inv;
+        if (s == 249u) {  // 63.5 and more would round to 2^128
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = __builtin_amdgcn_fmed3f(v[e], -63.0f, 63.0f);
+        }
         // adding 1.5 * 2^23 rounds to an integer (to nearest even) whose two's
         // complement is then the low byte
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            w[e] = __float_as_uint(__fadd_rn(__builtin_amdgcn_fmed3f(f[e] * inv, -lim, lim), 12582912.0f));
+            w[e] = __float_as_uint(__fadd_rn(v[e], 12582912.0f));
         q = u32x2{low_bytes(w[0], w[1], w[2], w[3]), low_bytes(w[4], w[5], w[6], w[7])};
     }
     if (s == kCkptNan) q = u32x2{0, 0};
@@ -182,13 +217,17 @@ __device__ __forceinline__ u32x4 behind(const u32x4& v, int bits) {
 // behind a branch, would be waited for at the load (rows of 4095 columns took
 // 1.6 times as long forward and twice backward as of 4096). Only rows of less
 // than 8 columns are read by the element.
-template <int DT>
+//
+// NT: a stream, read once, past the caches (as the stores of streams are): pack
+// and unpack of 65536x4096 bf16 took 273 us with both, 300 without. Codes are read
+// through them (16384x4096 forward from e4m3: 47 us, past them 50).
+template <int DT, bool NT>
 __device__ __forceinline__ Raw8<DT> fetch8(const RowPtr& p, int c, int n) {
     Raw8<DT> r;
     if constexpr (DT == kBf16) {
         r.v = u32x4{0, 0, 0, 0};
         if (n > 0 && c + n >= 8) {
-            r.v = *(const u32x4_a2*)((const uint16_t*)p.row + c - (8 - n));
+            r.v = ld16<NT>((const uint16_t*)p.row + c - (8 - n));
         } else if (n > 0) {
             const uint16_t* s = (const uint16_t*)p.row;
             uint32_t w[4] = {0, 0, 0, 0};
@@ -201,8 +240,8 @@ __device__ __forceinline__ Raw8<DT> fetch8(const RowPtr& p, int c, int n) {
         r.a = r.b = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         if (n > 0 && c + n >= 8) {
             const float* s = (const float*)p.row + c - (8 - n);
-            r.a = *(const f32x4_a4*)s;
-            r.b = *(const f32x4_a4*)(s + 4);
+            r.a = ld32<NT>(s);
+            r.b = ld32<NT>(s + 4);
         } else if (n > 0) {
             const float* s = (const float*)p.row;
             float w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
@@ -247,7 +286,7 @@ __device__ __forceinline__ void settle8(Raw8<DT>& r, int c, int n) {
 // Both, for values that are used at once.
 template <int DT>
 __device__ __forceinline__ Raw8<DT> load8(const RowPtr& p, int c, int n) {
-    Raw8<DT> r = fetch8<DT>(p, c, n);
+    Raw8<DT> r = fetch8<DT, false>(p, c, n);
     settle8(r, c, n);
     return r;
 }
@@ -278,6 +317,7 @@ __device__ __forceinline__ void keep_first(float f[8], int n) {
 }
 
 // The first n values rounded to dt (ZR_BF16 or ZR_FP32) at column c of a row.
+template <bool NT>
 __device__ __forceinline__ void store8(char* row, int dt, int c, int n, const float f[8]) {
     if (dt == kBf16) {
         uint16_t* p = (uint16_t*)row + c;
@@ -285,7 +325,7 @@ __device__ __forceinline__ void store8(char* row, int dt, int c, int n, const fl
 #pragma unroll
         for (int e = 0; e < 4; ++e) w[e] = bf16_pair(f[2 * e], f[2 * e + 1]);
         if (n == 8) {
-            *(u32x4_a2*)p = u32x4{w[0], w[1], w[2], w[3]};
+            st16<NT>(p, u32x4{w[0], w[1], w[2], w[3]});
         } else {
 #pragma unroll
             for (int e = 0; e < 7; ++e)
@@ -294,8 +334,8 @@ __device__ __forceinline__ void store8(char* row, int dt, int c, int n, const fl
     } else {
         float* p = (float*)row + c;
         if (n == 8) {
-            *(f32x4_a4*)p = f32x4{f[0], f[1], f[2], f[3]};
-            *(f32x4_a4*)(p + 4) = f32x4{f[4], f[5], f[6], f[7]};
+            st32<NT>(p, f32x4{f[0], f[1], f[2], f[3]});
+            st32<NT>(p + 4, f32x4{f[4], f[5], f[6], f[7]});
         } else {
 #pragma unroll
             for (int e = 0; e < 7; ++e)
@@ -349,7 +389,16 @@ __device__ __forceinline__ float wave_sum(float v) {
     return v;
 }
 
-// Largest magnitude (fp32 bits) over the 4 lanes of a block.
+// The largest of m over the 4 lanes of a block.
+__device__ __forceinline__ uint32_t block_max(uint32_t m) {
+    uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xB1, 0xF, 0xF, true);
+    m = o > m ? o : m;
+    o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4E, 0xF, 0xF, true);
+    return o > m ? o : m;
+}
+
+// Largest magnitude (fp32 bits) of a block, of fp32 values or of bf16 pairs
+// (two at a time); a NaN is larger than all else.
 __device__ __forceinline__ uint32_t block_amax(const float f[8]) {
     uint32_t m = 0;
 #pragma unroll
@@ -357,17 +406,22 @@ __device__ __forceinline__ uint32_t block_amax(const float f[8]) {
         const uint32_t b = __float_as_uint(f[e]) & 0x7FFFFFFFu;
         m = b > m ? b : m;
     }
-    uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xB1, 0xF, 0xF, true);
-    m = o > m ? o : m;
-    o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4E, 0xF, 0xF, true);
-    return o > m ? o : m;
+    return block_max(m);
+}
+__device__ __forceinline__ uint32_t block_amax(const u32x4& w) {
+    auto pair = [](uint32_t a) { return __builtin_bit_cast(u16x2, a & 0x7FFF7FFFu); };
+    const u16x2 m = __builtin_elementwise_max(__builtin_elementwise_max(pair(w.x), pair(w.y)),
+                                              __builtin_elementwise_max(pair(w.z), pair(w.w)));
+    return block_max(m.x > m.y ? m.x : m.y) << 16;
 }
 
-// Encodes a lane's vector at column c (< pitch; the block's 4 lanes are all
-// here) of a checkpoint row; values behind the row's end must be zero.
-__device__ __forceinline__ void ckpt_store8(char* codes, uint8_t* scales, int c, const float f[8], bool e4m3) {
-    const uint32_t s = ckpt_byte(block_amax(f), e4m3);
-    *(u32x2*)(codes + c) = ckpt_encode8(f, s, e4m3);
+// Encodes a lane's vector, of largest magnitude amax in its block, at column c
+// (< pitch; the block's 4 lanes are all here) of a checkpoint row; values
+// behind the row's end must be zero.
+__device__ __forceinline__ void ckpt_store8(char* codes, uint8_t* scales, int c, const float f[8], uint32_t amax,
+                                            bool e4m3) {
+    const uint32_t s = ckpt_byte(amax, e4m3);
+    st<true>((u32x2*)(codes + c), ckpt_encode8(f, s, e4m3));
     if ((c & (kCkptBlock - 1)) == 0) scales[c / kCkptBlock] = (uint8_t)s;
 }
 

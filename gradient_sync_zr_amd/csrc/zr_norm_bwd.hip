@@ -75,8 +75,8 @@ __global__ __launch_bounds__(norm_block(TPR)) void bwd_kernel(BwdArgs a) {
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int c = (v * TPR + lane) * 8, n = existing(a.cols, c);
-            rx[v] = fetch8<XD>(px, c, n);
-            rd[v] = fetch8<DD>(pd, c, n);
+            rx[v] = fetch8<XD, true>(px, c, n);
+            rd[v] = fetch8<DD, true>(pd, c, n);
         }
         mean_next = a.mean[row];
         rstd_next = a.rstd[row];
@@ -93,9 +93,9 @@ __global__ __launch_bounds__(norm_block(TPR)) void bwd_kernel(BwdArgs a) {
         auto fetch_old = [&](int v) {
             const int c = (v * TPR + lane) * 8, n = existing(a.cols, c);
             if (a.dx_dt == kBf16)
-                old[LATE ? 0 : v].a = __builtin_bit_cast(f32x4, fetch8<kBf16>({out, nullptr}, c, n).v);
+                old[LATE ? 0 : v].a = __builtin_bit_cast(f32x4, fetch8<kBf16, true>({out, nullptr}, c, n).v);
             else
-                old[LATE ? 0 : v] = fetch8<kFp32>({out, nullptr}, c, n);
+                old[LATE ? 0 : v] = fetch8<kFp32, true>({out, nullptr}, c, n);
         };
         if (!LATE && a.add_dx) {
 #pragma unroll
@@ -148,7 +148,7 @@ __global__ __launch_bounds__(norm_block(TPR)) void bwd_kernel(BwdArgs a) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) g[v][e] += o[e];
             }
-            store8(out, a.dx_dt, c, n, g[v]);
+            store8<true>(out, a.dx_dt, c, n, g[v]);
         }
     }
     // the block's sums: to the workspace, or as the gradients
@@ -179,13 +179,13 @@ __global__ __launch_bounds__(norm_block(TPR)) void bwd_kernel(BwdArgs a) {
                 const int c = (v * TPR + lane) * 8, n = existing(a.cols, c);
                 if (n == 0) continue;
                 if (out) {
-                    store8((char*)out, kFp32, c, n, which ? db[v] : dw[v]);
+                    store8<false>((char*)out, kFp32, c, n, which ? db[v] : dw[v]);
                 } else {
                     float old[8];
                     load_param8(a.accumulate ? grad : nullptr, a.grad_dt, c, n, 0.0f, old);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) old[e] += which ? db[v][e] : dw[v][e];
-                    store8((char*)grad, a.grad_dt, c, n, old);
+                    store8<false>((char*)grad, a.grad_dt, c, n, old);
                 }
             }
         }
@@ -240,7 +240,7 @@ __global__ __launch_bounds__(1024) void bwd_wide_dx_kernel(BwdArgs a) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) d[e] += old[e];
             }
-            store8(out, a.dx_dt, (int)c, n, d);
+            store8<true>(out, a.dx_dt, (int)c, n, d);
         }
     }
 }
@@ -268,8 +268,8 @@ __global__ __launch_bounds__(kThreads) void bwd_wide_sums_kernel(BwdArgs a, int 
             }
         }
         float* out = a.part + (int64_t)s * 2 * a.cols;
-        store8((char*)out, kFp32, (int)c, n, dw);
-        store8((char*)(out + a.cols), kFp32, (int)c, n, db);
+        store8<false>((char*)out, kFp32, (int)c, n, dw);
+        store8<false>((char*)(out + a.cols), kFp32, (int)c, n, db);
     }
 }
 

@@ -24,8 +24,9 @@ struct FwdArgs {
 };
 
 __device__ __forceinline__ void put_ckpt(const FwdArgs& a, char* ckpt, int64_t row, int64_t pitch, int c,
-                                         const float f[8]) {
-    ckpt_store8(ckpt + row * pitch, (uint8_t*)ckpt + a.rows * pitch + row * (pitch / kCkptBlock), c, f, a.e4m3 != 0);
+                                         const float f[8], uint32_t amax) {
+    ckpt_store8(ckpt + row * pitch, (uint8_t*)ckpt + a.rows * pitch + row * (pitch / kCkptBlock), c, f, amax,
+                a.e4m3 != 0);
 }
 
 // One vector of the output at column c < pitch: y rounded to its type, then
@@ -34,18 +35,18 @@ __device__ __forceinline__ void put_y(const FwdArgs& a, int64_t row, int64_t pit
                                       const float w[8], const float b[8], float mean, float rstd) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) f[e] = __builtin_fmaf((f[e] - mean) * rstd, w[e], b[e]);
-    if (a.y && n > 0) store8(a.y + row * a.ld_y * (a.y_dt == kBf16 ? 2 : 4), a.y_dt, c, n, f);
+    if (a.y && n > 0) store8<true>(a.y + row * a.ld_y * (a.y_dt == kBf16 ? 2 : 4), a.y_dt, c, n, f);
     if (a.ckpt_y) {
-        if (a.y_dt == kBf16) {
-#pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-                const uint32_t h = bf16_pair(f[e], f[e + 1]);
-                f[e] = __uint_as_float(h << 16);
-                f[e + 1] = __uint_as_float(h & 0xFFFF0000u);
-            }
-        }
         if (n < 8) keep_first(f, n);
-        put_ckpt(a, a.ckpt_y, row, pitch, c, f);
+        uint32_t amax;
+        if (a.y_dt == kBf16) {
+            const u32x4 h = {bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7])};
+            widen8(Raw8<kBf16>{h}, f);
+            amax = block_amax(h);
+        } else {
+            amax = block_amax(f);
+        }
+        put_ckpt(a, a.ckpt_y, row, pitch, c, f, amax);
     }
 }
 
@@ -69,7 +70,7 @@ __global__ __launch_bounds__(norm_block(TPR)) void fwd_kernel(FwdArgs a) {
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int c = (v * TPR + lane) * 8;
-            raw[v] = fetch8<XD>(p, c, existing(a.cols, c));
+            raw[v] = fetch8<XD, true>(p, c, existing(a.cols, c));
         }
     };
     const int64_t first = (int64_t)blockIdx.x * G + group, step = (int64_t)gridDim.x * G;
@@ -95,7 +96,7 @@ __global__ __launch_bounds__(norm_block(TPR)) void fwd_kernel(FwdArgs a) {
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int c = (v * TPR + lane) * 8, n = existing(a.cols, c);
-            if (XD <= kFp32 && a.ckpt_x && c < pitch) put_ckpt(a, a.ckpt_x, row, pitch, c, f[v]);
+            if (XD <= kFp32 && a.ckpt_x && c < pitch) put_ckpt(a, a.ckpt_x, row, pitch, c, f[v], block_amax(f[v]));
             float d[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) d[e] = f[v][e] - mean;
@@ -130,7 +131,7 @@ __global__ __launch_bounds__(1024) void fwd_wide_kernel(FwdArgs a) {
             float f[8];
             widen8(load8<XD>(p, (int)c, n), f);
             if (n < 8) keep_first(f, n);
-            if (XD <= kFp32 && a.ckpt_x) put_ckpt(a, a.ckpt_x, row, pitch, (int)c, f);
+            if (XD <= kFp32 && a.ckpt_x) put_ckpt(a, a.ckpt_x, row, pitch, (int)c, f, block_amax(f));
             float t = 0.0f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) t += f[e];

@@ -212,7 +212,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wgrad_kernel(Wg
                 const int id = tid + j * T;
                 const int64_t row = k + id / CA, col = m0 + (id % CA) * 8;
                 const int n = row < ke ? chunk : 0;
-                ra[j] = fetch8<DD>({(const char*)a.dy + row * a.ld_dy * (DD == kBf16 ? 2 : 4), nullptr}, (int)col, n);
+                ra[j] = fetch8<DD, false>({(const char*)a.dy + row * a.ld_dy * (DD == kBf16 ? 2 : 4), nullptr}, (int)col, n);
             }
 #pragma unroll
             for (int j = 0; j < NB; ++j) {
