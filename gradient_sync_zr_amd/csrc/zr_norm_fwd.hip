@@ -7,6 +7,14 @@
 // bias in registers and the next row's loads in flight while a row is reduced
 // and written. Rows too wide for registers (over 16384 columns) are read again
 // from memory in each pass.
+//
+// Bound by memory: 16384x4096 bf16 takes 48 us (5.6 TB/s; 86 before the next
+// row's loads were in flight and the weights kept), 64 with x's checkpoint, 45
+// from an e4m3 checkpoint (4.6 TB/s, the row's two barriers); 24576x11008 201 us
+// (5.4), and 354 with the checkpoint of y too, whose arithmetic one block of 512
+// per CU does not hide. Two vectors of 8 columns a lane measured best: with one
+// (512 lanes a row) 16384x4096 takes 59 us; and so did 1024 blocks of 256, which
+// are what the chip holds at once (2048: 56).
 #include <hip/hip_runtime.h>
 
 #include "zr_norm.hpp"
