@@ -773,13 +773,23 @@ def _ckpt(x, rows: int, cols: int, name: str) -> int:
     return x.data_ptr()
 
 
-_raw_stream = None  # torch's current stream of a GPU as a handle
+# torch's current GPU and its current stream on a GPU as a handle: the lookups
+# behind torch.cuda.current_device() and current_stream().cuda_stream, without
+# the stream object that the latter builds (2.8 us a call)
+_current_gpu = _raw_stream = None
+
+
+def _find_lookups() -> None:
+    global _current_gpu, _raw_stream
+    import torch
+    _current_gpu = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+        (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _run_on(stream, *xs) -> int:
     """The stream's handle, for a call on these buffers: tensors must be on the
     GPU that is current (and the stream, if given, is on)."""
-    global _raw_stream
     here = -2
     for x in xs:
         if x is None or x.__class__ is int or x.__class__ is tuple:
@@ -791,18 +801,16 @@ def _run_on(stream, *xs) -> int:
             if here >= 0:
                 raise ValueError(f"tensors on GPUs {here} and {d}")
             here = d
-    if here >= 0 or stream is None:
-        import torch
-        on = torch.cuda.current_device()
-        if here >= 0 and (here != on or getattr(getattr(stream, "device", None), "index", here) != here):
-            raise ValueError(f"the tensors are on GPU {here}, the current one is {on}: make theirs current, "
-                             "and its stream")
-        if stream is None:
-            if _raw_stream is None:
-                _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
-                    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-            return _raw_stream(on)
-    return _stream(stream)
+    if here < 0 and stream is not None:
+        return _stream(stream)
+    if _raw_stream is None:
+        _find_lookups()
+    on = _current_gpu()
+    if here >= 0 and (here != on or (stream is not None and
+                                     getattr(getattr(stream, "device", None), "index", here) != here)):
+        raise ValueError(f"the tensors are on GPU {here}, the current one is {on}: make theirs current, "
+                         "and its stream")
+    return _raw_stream(on) if stream is None else _stream(stream)
 
 
 def zr_ckpt_bytes(rows: int, cols: int) -> int:
@@ -854,11 +862,16 @@ def zr_layernorm_fwd(x, rows: int, cols: int, y=None, weight=None, bias=None, ep
     else:
         py, yd, ldy = _matrix(y, rows, cols, y_dtype, ld_y, "y")
     w, b = _vector(weight, cols, param_dtype, "weight"), _vector(bias, cols, param_dtype, "bias")
-    _check(lib().zr_layernorm_fwd(px, xd, rows, cols, ldx, w[0], b[0], _one_dtype(w[1], b[1], ZR_FP32, "weight and bias"),
-                                  eps, py, yd, ldy, _vector(mean, rows, ZR_FP32, "mean")[0],
-                                  _vector(rstd, rows, ZR_FP32, "rstd")[0], _ckpt(ckpt_x, rows, cols, "ckpt_x"),
-                                  _ckpt(ckpt_y, rows, cols, "ckpt_y"), ckpt_format,
-                                  _run_on(stream, x, y, weight, bias, mean, rstd, ckpt_x, ckpt_y)))
+    st = lib().zr_layernorm_fwd(px, xd, rows, cols, ldx, w[0], b[0],
+                                w[1] if w[1] == b[1] and b[1] is not None else
+                                _one_dtype(w[1], b[1], ZR_FP32, "weight and bias"),
+                                eps, py, yd, ldy, _vector(mean, rows, ZR_FP32, "mean")[0],
+                                _vector(rstd, rows, ZR_FP32, "rstd")[0],
+                                0 if ckpt_x is None else _ckpt(ckpt_x, rows, cols, "ckpt_x"),
+                                0 if ckpt_y is None else _ckpt(ckpt_y, rows, cols, "ckpt_y"), ckpt_format,
+                                _run_on(stream, x, y, weight, bias, mean, rstd, ckpt_x, ckpt_y))
+    if st:
+        _check(st)
 
 
 def zr_layernorm_bwd(dy, x, rows: int, cols: int, mean, rstd, weight=None, dx=None, dweight=None, dbias=None,

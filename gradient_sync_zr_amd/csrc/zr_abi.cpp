@@ -334,7 +334,16 @@ bool mats_overlap(const Mat& a, const Mat& b) {
 // Buffers of a call: outputs must be disjoint from each other and from the
 // inputs, but for the pairs that `same` allows at equal address and shape.
 struct Buffers {
-    std::vector<Mat> in, out;
+    struct List {  // no call has more than 8 of either
+        Mat m[8];
+        int n = 0;
+        void push_back(const Mat& x) { m[n++] = x; }
+        int size() const { return n; }
+        const Mat& operator[](int i) const { return m[i]; }
+        const Mat* begin() const { return m; }
+        const Mat* end() const { return m + n; }
+    };
+    List in, out;
 
     static zr_status check(const void* p, int64_t es, const char* name) {
         if (!p) return fail(ZR_ERR_INVALID, "%s is NULL", name);
@@ -367,8 +376,8 @@ struct Buffers {
     }
     // in_place: this output may be an input of the same address, row stride and width
     zr_status disjoint(const char* in_place) const {
-        for (size_t i = 0; i < out.size(); ++i) {
-            for (size_t j = i + 1; j < out.size(); ++j)
+        for (int i = 0; i < out.size(); ++i) {
+            for (int j = i + 1; j < out.size(); ++j)
                 if (mats_overlap(out[i], out[j]))
                     return fail(ZR_ERR_ALIAS, "%s and %s overlap", out[i].name, out[j].name);
             for (const Mat& m : in) {
