@@ -196,9 +196,10 @@ struct NormBwd {
 ZR_KERNELS hipError_t launch_layernorm_bwd(const NormBwd& f, hipStream_t stream);
 // Strips of rows that a backward pass leaves partial parameter gradients of:
 // one block each, as many as the chip holds at once, and no more than there
-// are steps of rows (a block takes 16, 4 or 1 rows at once). Below kNormOne
-// elements one block walks over all rows and writes the gradients itself: it
-// takes longer than several would, but saves the joining launch.
+// are steps of rows (a block takes 16, 4 or 1 rows at once). Up to kNormOne
+// elements one block, with more rows at once, walks over all rows and writes the
+// gradients itself: it takes longer than several would, but saves the joining
+// launch.
 constexpr int64_t kNormOne = 16384;
 inline int layernorm_strips(int64_t rows, int64_t cols) {
     if (rows > 0 && rows * cols <= kNormOne) return 1;

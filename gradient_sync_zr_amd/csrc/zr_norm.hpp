@@ -22,9 +22,9 @@ constexpr int norm_block(int tpr) { return tpr > kThreads ? tpr : kThreads; }
 // Which of the block's rows a thread has: the same for a whole wave where a row
 // takes one or more, and then kept in scalar registers, as are the addresses
 // that follow from it.
-template <int TPR>
+template <int TPR, int B = norm_block(TPR)>
 __device__ __forceinline__ int row_group() {
-    if constexpr (norm_block(TPR) == TPR) return 0;
+    if constexpr (B == TPR) return 0;
     const int g = threadIdx.x / TPR;
     return TPR >= 64 ? __builtin_amdgcn_readfirstlane(g) : g;
 }

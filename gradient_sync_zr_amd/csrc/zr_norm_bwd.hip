@@ -54,15 +54,18 @@ __device__ __forceinline__ void centered8(const Raw8<XD>& r, float mean, float f
     }
 }
 
-template <int XD, int DD, int TPR, int NV>
-__global__ __launch_bounds__(norm_block(TPR)) void bwd_kernel(BwdArgs a) {
-    constexpr int B = norm_block(TPR), G = B / TPR;
+template <int XD, int DD, int TPR, int NV, int B>
+__global__ __launch_bounds__(B) void bwd_kernel(BwdArgs a) {
+    constexpr int G = B / TPR;
+    // a block's groups leave the loop at different turns, so only a block of one
+    // group may have barriers in it
+    static_assert(TPR <= 64 || B == TPR, "barriers need one row per block");
     constexpr int C = TPR * NV * 8;  // columns that a row's lanes cover
     // three vectors with one source in fp32 leave no registers for old dx
     constexpr bool LATE = NV == 3 && (XD == kFp32 || DD == kFp32);
     __shared__ float red[2][B / 64][2];
     __shared__ float join[G > 1 ? G : 1][G > 1 ? C : 1];
-    const int lane = threadIdx.x % TPR, group = row_group<TPR>();
+    const int lane = threadIdx.x % TPR, group = row_group<TPR, B>();
     const float inv_n = 1.0f / (float)a.cols;
     float w[NV][8], dw[NV][8], db[NV][8];
 #pragma unroll
@@ -310,16 +313,20 @@ __global__ __launch_bounds__(1024) void bwd_join_kernel(const float* part, int s
     }
 }
 
-template <int XD, int DD, int TPR, int NV>
+template <int XD, int DD, int TPR, int NV, int B = norm_block(TPR)>
 hipError_t bwd_run(const BwdArgs& a, int strips, hipStream_t stream) {
-    constexpr int B = norm_block(TPR);
-    bwd_kernel<XD, DD, TPR, NV><<<strips, B, 0, stream>>>(a);
+    bwd_kernel<XD, DD, TPR, NV, B><<<strips, B, 0, stream>>>(a);
     return hipGetLastError();
 }
 
 template <int XD, int DD>
 hipError_t bwd_pick(const BwdArgs& a, int strips, hipStream_t stream) {
     const int64_t n = a.cols;
+    // one block for all rows: as many of them at once as it can hold (16x768 from
+    // 8.6 us with 4 at once to 6.8 with 8)
+    if (strips == 1 && n <= 128) return bwd_run<XD, DD, 16, 1, 1024>(a, strips, stream);
+    if (strips == 1 && n <= 512) return bwd_run<XD, DD, 64, 1, 1024>(a, strips, stream);
+    if (strips == 1 && n <= 1024) return bwd_run<XD, DD, 64, 2, 512>(a, strips, stream);
     if (n <= 128) return bwd_run<XD, DD, 16, 1>(a, strips, stream);
     if (n <= 512) return bwd_run<XD, DD, 64, 1>(a, strips, stream);
     if (n <= 1024) return bwd_run<XD, DD, 64, 2>(a, strips, stream);

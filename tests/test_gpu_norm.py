@@ -182,11 +182,15 @@ def backward64(dy, x, mean, rstd, w):
 
 def column_adds(rows, cols):
     """Adds in line of a column's sum: a block takes `per` rows at once, each lane group the strip's share of
-    them, then the groups' sums are added, then the strips' (16 groups of lanes, each every 16th, then those)."""
+    them, then the groups' sums are added, then the strips' (16 groups of lanes, each every 16th, then those).
+    At most 16384 elements are one block's, with more rows at once."""
+    if rows * cols <= 16384:
+        per = 64 if cols <= 128 else 16 if cols <= 512 else 8 if cols <= 1024 else 1
+        return -(-rows // per) + min(per, rows)
     per = 16 if cols <= 128 else 4 if cols <= 1024 else 1
     steps = -(-rows // per)
-    strips = 1 if rows * cols <= 16384 else min(steps, 512 if cols <= 4096 else 256)
-    return -(-steps // strips) + per + (-(-strips // 16) + 16 if strips > 1 else 0)
+    strips = min(steps, 512 if cols <= 4096 else 256)
+    return -(-steps // strips) + per + -(-strips // 16) + 16
 
 
 @pytest.mark.parametrize("cols", COLS)
