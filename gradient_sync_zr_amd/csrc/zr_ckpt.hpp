@@ -383,8 +383,10 @@ __device__ __forceinline__ float wave_sum(float v) {
     v = dpp_add<0x141>(v);  // mirrored within 8
     v = dpp_add<0x140>(v);  // mirrored within 16
     if constexpr (LANES >= 64) {
-        v += __shfl_xor(v, 16, 64);
-        v += __shfl_xor(v, 32, 64);
+        // swaps of 16 and 32 lanes leave a lane's own and its partner's value
+        auto both = [](auto r) { return __uint_as_float(r[0]) + __uint_as_float(r[1]); };
+        v = both(__builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false));
+        v = both(__builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false));
     }
     return v;
 }

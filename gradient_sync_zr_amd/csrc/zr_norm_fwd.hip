@@ -8,13 +8,16 @@
 // and written. Rows too wide for registers (over 16384 columns) are read again
 // from memory in each pass.
 //
-// Bound by memory: 16384x4096 bf16 takes 48 us (5.6 TB/s; 86 before the next
-// row's loads were in flight and the weights kept), 64 with x's checkpoint, 45
-// from an e4m3 checkpoint (4.6 TB/s, the row's two barriers); 24576x11008 201 us
-// (5.4), and 354 with the checkpoint of y too, whose arithmetic one block of 512
-// per CU does not hide. Two vectors of 8 columns a lane measured best: with one
-// (512 lanes a row) 16384x4096 takes 59 us; and so did 1024 blocks of 256, which
-// are what the chip holds at once (2048: 56).
+// Bound by memory, and by the arithmetic of checkpoints: 16384x4096 bf16 takes 48
+// us (5.5 TB/s; 86 before the next row's loads were in flight and the weights
+// kept), 64 with x's checkpoint, 37 from an e4m3 checkpoint (5.5 TB/s; 45 while
+// every vector was masked by the element and lanes 16 and 32 apart were added
+// through LDS); 24576x11008 179 us (6.05 TB/s, 201 so), 156 (216) from e4m3, and
+// 343 with the checkpoint of y too. A wave's own mean and squares, joined with one
+// barrier a row, instead of two passes with two: 43 us where they took 40, as the
+// vector instructions count, not the barriers. Two vectors of 8 columns a lane
+// measured best: with one (512 lanes a row) 16384x4096 took 59 us for 52; and 1024
+// blocks of 256, which are what the chip holds at once (2048: 56).
 #include <hip/hip_runtime.h>
 
 #include "zr_norm.hpp"
@@ -37,15 +40,16 @@ __device__ __forceinline__ void put_ckpt(const FwdArgs& a, char* ckpt, int64_t r
                 a.e4m3 != 0);
 }
 
-// One vector of the output at column c < pitch: y rounded to its type, then
-// its checkpoint, of y as its readers have it.
+// One vector of the output at column c < pitch, of the centred row: y rounded
+// to its type, then its checkpoint, of y as its readers have it.
 __device__ __forceinline__ void put_y(const FwdArgs& a, int64_t row, int64_t pitch, int c, int n, float f[8],
-                                      const float w[8], const float b[8], float mean, float rstd) {
+                                      const float w[8], const float b[8], float rstd) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = __builtin_fmaf((f[e] - mean) * rstd, w[e], b[e]);
+    for (int e = 0; e < 8; ++e) f[e] = __builtin_fmaf(f[e] * rstd, w[e], b[e]);
     if (a.y && n > 0) store8<true>(a.y + row * a.ld_y * (a.y_dt == kBf16 ? 2 : 4), a.y_dt, c, n, f);
     if (a.ckpt_y) {
-        if (n < 8) keep_first(f, n);
+        if (a.cols & 7) keep_first(f, n);
+        if (n == 0) keep_first(f, 0);
         uint32_t amax;
         if (a.y_dt == kBf16) {
             const u32x4 h = {bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7])};
@@ -65,7 +69,10 @@ __global__ __launch_bounds__(norm_block(TPR)) void fwd_kernel(FwdArgs a) {
     const int lane = threadIdx.x % TPR, group = row_group<TPR>();
     const int64_t pitch = ckpt_pitch(a.cols);
     const float inv_n = 1.0f / (float)a.cols;
-    float w[NV][8], b[NV][8];  // read again for each row instead, 24576x11008 takes 354 us, not 217
+    // the same for all threads: masks of single elements are stepped over, not
+    // issued, where every vector is whole or absent
+    const bool ragged = (a.cols & 7) != 0;
+    float w[NV][8], b[NV][8];  // read again for each row instead, 24576x11008 took 354 us for 217
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
         const int c = (v * TPR + lane) * 8, n = existing(a.cols, c);
@@ -91,9 +98,9 @@ __global__ __launch_bounds__(norm_block(TPR)) void fwd_kernel(FwdArgs a) {
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int c = (v * TPR + lane) * 8, n = existing(a.cols, c);
-            settle8(raw[v], c, n);
+            if (ragged) settle8(raw[v], c, n);
             widen8(raw[v], f[v]);
-            if (XD > kFp32 && n < 8) keep_first(f[v], n);
+            if (XD > kFp32 && ragged) keep_first(f[v], n);
 #pragma unroll
             for (int e = 0; e < 8; ++e) s[0] += f[v][e];
         }
@@ -105,15 +112,15 @@ __global__ __launch_bounds__(norm_block(TPR)) void fwd_kernel(FwdArgs a) {
         for (int v = 0; v < NV; ++v) {
             const int c = (v * TPR + lane) * 8, n = existing(a.cols, c);
             if (XD <= kFp32 && a.ckpt_x && c < pitch) put_ckpt(a, a.ckpt_x, row, pitch, c, f[v], block_amax(f[v]));
-            float d[8];
+            const float m = n > 0 ? mean : 0.0f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) d[e] = f[v][e] - mean;
-            if (n < 8) keep_first(d, n);
+            for (int e = 0; e < 8; ++e) f[v][e] -= m;
+            if (ragged) keep_first(f[v], n);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s[0] = __builtin_fmaf(d[e], d[e], s[0]);
+            for (int e = 0; e < 8; ++e) s[0] = __builtin_fmaf(f[v][e], f[v][e], s[0]);
         }
         row_sums<TPR>(s, red[1]);
-        const float rstd = 1.0f / sqrtf(s[0] * inv_n + a.eps);
+        const float rstd = rsqrtf(s[0] * inv_n + a.eps);  // one unit in the last place, as root and division
         if (lane == 0) {
             if (a.mean) a.mean[row] = mean;
             if (a.rstd) a.rstd[row] = rstd;
@@ -121,7 +128,7 @@ __global__ __launch_bounds__(norm_block(TPR)) void fwd_kernel(FwdArgs a) {
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int c = (v * TPR + lane) * 8;
-            if (c < pitch) put_y(a, row, pitch, c, existing(a.cols, c), f[v], w[v], b[v], mean, rstd);
+            if (c < pitch) put_y(a, row, pitch, c, existing(a.cols, c), f[v], w[v], b[v], rstd);
         }
     }
 }
@@ -161,7 +168,7 @@ __global__ __launch_bounds__(1024) void fwd_wide_kernel(FwdArgs a) {
             s[0] += t;
         }
         row_sums<1024>(s, red[1]);
-        const float rstd = 1.0f / sqrtf(s[0] / (float)a.cols + a.eps);
+        const float rstd = rsqrtf(s[0] / (float)a.cols + a.eps);
         if (threadIdx.x == 0) {
             if (a.mean) a.mean[row] = mean;
             if (a.rstd) a.rstd[row] = rstd;
@@ -172,7 +179,9 @@ __global__ __launch_bounds__(1024) void fwd_wide_kernel(FwdArgs a) {
             widen8(load8<XD>(p, (int)c, n), f);
             load_param8(a.w, a.param_dt, (int)c, n, 1.0f, w);
             load_param8(a.b, a.param_dt, (int)c, n, 0.0f, b);
-            put_y(a, row, pitch, (int)c, n, f, w, b, mean, rstd);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] -= mean;
+            put_y(a, row, pitch, (int)c, n, f, w, b, rstd);
         }
     }
 }
