@@ -10,14 +10,14 @@
 //
 // Bound by memory, and by the arithmetic of checkpoints: 16384x4096 bf16 takes 48
 // us (5.5 TB/s; 86 before the next row's loads were in flight and the weights
-// kept), 64 with x's checkpoint, 37 from an e4m3 checkpoint (5.5 TB/s; 45 while
-// every vector was masked by the element and lanes 16 and 32 apart were added
-// through LDS); 24576x11008 179 us (6.05 TB/s, 201 so), 156 (216) from e4m3, and
-// 343 with the checkpoint of y too. A wave's own mean and squares, joined with one
-// barrier a row, instead of two passes with two: 43 us where they took 40, as the
-// vector instructions count, not the barriers. Two vectors of 8 columns a lane
-// measured best: with one (512 lanes a row) 16384x4096 took 59 us for 52; and 1024
-// blocks of 256, which are what the chip holds at once (2048: 56).
+// kept), 64 with x's checkpoint, 37 to 40 from an e4m3 checkpoint (5.1 to 5.5
+// TB/s; 45 while every vector was masked by the element and lanes 16 and 32 apart
+// were added through LDS); 24576x11008 179 us (6.05 TB/s, 201 so), 156 (216) from
+// e4m3, and 343 with the checkpoint of y too. A wave's own mean and squares,
+// joined with one barrier a row, instead of two passes with two: 43 us where they
+// took 40, as the vector instructions count, not the barriers. Two vectors of 8
+// columns a lane measured best: with one (512 lanes a row) 16384x4096 took 59 us
+// for 52; and 1024 blocks of 256, which are what the chip holds at once (2048: 56).
 #include <hip/hip_runtime.h>
 
 #include "zr_norm.hpp"
