@@ -1138,7 +1138,8 @@ zr_status zr_layernorm_bwd(const void* dy, zr_dtype dy_dt, int64_t ld_dy, const 
                 ((!std::strcmp(m.name, "dy") && dx_dt != dy_dt) || (!std::strcmp(m.name, "x") && dx_dt != x_dt)))
                 return fail(ZR_ERR_ALIAS, "dx is %s but of another type", m.name);
         ZR_TRY(b.disjoint("dx"));
-        if (rows == 0 && !dweight && !dbias) return ok();
+        // without rows there is nothing to add, and what is added to stays as it is
+        if (rows == 0 && ((!dweight && !dbias) || (flags & ZR_ACCUMULATE))) return ok();
         ZR_TRY(have(launch_layernorm_bwd, "layer norm backward"));
         NormBwd f{};
         f.dy = dy; f.x = x; f.weight = weight; f.mean = mean; f.rstd = rstd;
@@ -1175,6 +1176,7 @@ zr_status zr_ckpt_wgrad(const void* dy, zr_dtype dy_dt, int64_t ld_dy, const voi
         if (dbias) ZR_TRY(b.vector(true, dbias, dt_bytes(grad_dt), out_cols, "dbias"));
         ZR_TRY(need_workspace(b, workspace, ws_bytes, zr_ckpt_wgrad_workspace_bytes(rows, out_cols, in_cols)));
         ZR_TRY(b.disjoint(nullptr));
+        if (rows == 0 && (flags & ZR_ACCUMULATE)) return ok();  // what is added to stays as it is
         ZR_TRY(have(launch_ckpt_wgrad, "weight gradient"));
         Wgrad w{};
         w.dy = dy; w.ckpt = ckpt;
