@@ -743,7 +743,8 @@ def _matrix(x, rows: int, cols: int, dtype, ld, name: str):
 
 
 def _vector(x, n: int, dtype, name: str):
-    """(address, dtype) of n contiguous elements; (0, None) of None."""
+    """(address, dtype) of n contiguous elements; (0, None) of None. The dtype
+    of an address is what the dtype argument says, None without one."""
     if x is None:
         return 0, None
     if x.__class__ is int:
@@ -756,11 +757,21 @@ def _vector(x, n: int, dtype, name: str):
     return x.data_ptr(), code
 
 
-def _one_dtype(a, b, default: int, what: str) -> int:
-    """The dtype of two vectors of which one may be missing."""
-    if a is None or b is None or a == b:
-        return b if a is None and b is not None else (default if a is None else a)
-    raise ValueError(f"{what} are of different dtypes")
+def _one_dtype(a, b, names) -> int:
+    """The dtype of two vectors of which one may be missing or an address whose
+    dtype is the other's: (address, dtype) of each. Any will do if both are
+    missing."""
+    if a[1] is None or b[1] is None:
+        code = b[1] if a[1] is None else a[1]
+        if code is None:
+            for (at, _), name in zip((a, b), names):
+                if at:
+                    raise ValueError(f"{name} is an address: its dtype is needed")
+            return ZR_FP32
+        return code
+    if a[1] != b[1]:
+        raise ValueError(f"{' and '.join(names)} are of different dtypes")
+    return a[1]
 
 
 def _ckpt(x, rows: int, cols: int, name: str) -> int:
@@ -863,8 +874,7 @@ def zr_layernorm_fwd(x, rows: int, cols: int, y=None, weight=None, bias=None, ep
         py, yd, ldy = _matrix(y, rows, cols, y_dtype, ld_y, "y")
     w, b = _vector(weight, cols, param_dtype, "weight"), _vector(bias, cols, param_dtype, "bias")
     st = lib().zr_layernorm_fwd(px, xd, rows, cols, ldx, w[0], b[0],
-                                w[1] if w[1] == b[1] and b[1] is not None else
-                                _one_dtype(w[1], b[1], ZR_FP32, "weight and bias"),
+                                w[1] if w[1] == b[1] and b[1] is not None else _one_dtype(w, b, ("weight", "bias")),
                                 eps, py, yd, ldy, _vector(mean, rows, ZR_FP32, "mean")[0],
                                 _vector(rstd, rows, ZR_FP32, "rstd")[0],
                                 0 if ckpt_x is None else _ckpt(ckpt_x, rows, cols, "ckpt_x"),
@@ -887,9 +897,9 @@ def zr_layernorm_bwd(dy, x, rows: int, cols: int, mean, rstd, weight=None, dx=No
     w = _vector(weight, cols, param_dtype, "weight")
     gw, gb = _vector(dweight, cols, grad_dtype, "dweight"), _vector(dbias, cols, grad_dtype, "dbias")
     ws, wsb = _workspace(workspace)
-    _check(lib().zr_layernorm_bwd(pdy, dyd, lddy, px, xd, ldx, rows, cols, w[0], ZR_FP32 if w[1] is None else w[1],
+    _check(lib().zr_layernorm_bwd(pdy, dyd, lddy, px, xd, ldx, rows, cols, w[0], _one_dtype(w, (0, None), ("weight",)),
                                   _vector(mean, rows, ZR_FP32, "mean")[0], _vector(rstd, rows, ZR_FP32, "rstd")[0],
-                                  pdx, dxd, lddx, gw[0], gb[0], _one_dtype(gw[1], gb[1], ZR_FP32, "dweight and dbias"),
+                                  pdx, dxd, lddx, gw[0], gb[0], _one_dtype(gw, gb, ("dweight", "dbias")),
                                   (ZR_ACCUMULATE if accumulate else 0) | (ZR_ADD_DX if add_dx else 0), ws, wsb,
                                   _run_on(stream, dy, x, mean, rstd, weight, dx, dweight, dbias, workspace)))
 
@@ -904,6 +914,6 @@ def zr_ckpt_wgrad(dy, ckpt, rows: int, out_cols: int, in_cols: int, dw, dbias=No
     gb = _vector(dbias, out_cols, grad_dtype if isinstance(dbias, int) else None, "dbias")
     ws, wsb = _workspace(workspace)
     _check(lib().zr_ckpt_wgrad(pdy, dyd, lddy, _ckpt(ckpt, rows, in_cols, "ckpt"), format, rows, out_cols, in_cols,
-                               pdw, _one_dtype(gd, gb[1], gd, "dw and dbias"), lddw, gb[0],
+                               pdw, _one_dtype((pdw, gd), gb, ("dw", "dbias")), lddw, gb[0],
                                ZR_ACCUMULATE if accumulate else 0, ws, wsb,
                                _run_on(stream, dy, ckpt, dw, dbias, workspace)))
