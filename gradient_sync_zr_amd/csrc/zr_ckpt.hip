@@ -105,7 +105,7 @@ int64_t tiles_of(int64_t rows, int64_t cols) {
 hipError_t launch_ckpt_pack(const void* x, zr_dtype dt, int64_t rows, int64_t cols, int64_t ld, zr_dtype fmt,
                             void* ckpt, hipStream_t stream) {
     const int64_t tiles = tiles_of(rows, cols);
-    const dim3 grid(grid_for(tiles)), block(kThreads);
+    const dim3 grid(grid_for(tiles, kThreads)), block(kThreads);
     const int e4m3 = fmt == ZR_CKPT_E4M3;
     if (dt == ZR_BF16)
         pack_kernel<kBf16><<<grid, block, 0, stream>>>(x, ld, rows, cols, (char*)ckpt, e4m3, tiles);
@@ -117,7 +117,7 @@ hipError_t launch_ckpt_pack(const void* x, zr_dtype dt, int64_t rows, int64_t co
 hipError_t launch_ckpt_unpack(const void* ckpt, zr_dtype fmt, int64_t rows, int64_t cols, void* x, zr_dtype dt,
                               int64_t ld, hipStream_t stream) {
     const int64_t tiles = tiles_of(rows, cols);
-    const dim3 grid(grid_for(tiles)), block(kThreads);
+    const dim3 grid(grid_for(tiles, kThreads)), block(kThreads);
     if (fmt == ZR_CKPT_E4M3)
         unpack_kernel<kE4m3><<<grid, block, 0, stream>>>((const char*)ckpt, rows, cols, (char*)x, ld, dt, tiles);
     else

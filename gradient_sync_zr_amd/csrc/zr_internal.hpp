@@ -57,9 +57,11 @@ struct Tuning {
     int debug;             // ZR_DEBUG: 1 = wait for the stream after each call's launches
 };
 const Tuning& tuning();
-// Blocks for a launch of `tiles` tiles: one per tile, at most tuning().max_grid.
-inline int grid_for(int64_t tiles, int64_t cap_divisor = 1) {
-    const int64_t cap = tuning().max_grid / cap_divisor > 0 ? tuning().max_grid / cap_divisor : 1;
+// Blocks of `threads` threads for a launch of `tiles` tiles: one per tile, at
+// most tuning().max_grid, and fewer than 2^32 threads in all (HIP refuses more).
+inline int grid_for(int64_t tiles, int threads = 256) {
+    const int64_t most = (((int64_t)1 << 32) - 1) / threads;
+    const int64_t cap = tuning().max_grid < most ? tuning().max_grid : most;
     return (int)(tiles < cap ? tiles : cap);
 }
 int device_cu_count();  // CUs of the current device (cached per device)

@@ -336,11 +336,11 @@ hipError_t bwd_pick(const BwdArgs& a, int strips, hipStream_t stream) {
     if (n <= 12288) return bwd_run<XD, DD, 512, 3>(a, strips, stream);
     if (a.part) {  // before dx, which may take dy's or x's place
         const int64_t tiles = (n + kThreads * 8 - 1) / (kThreads * 8);
-        bwd_wide_sums_kernel<XD, DD><<<grid_for(tiles * strips), kThreads, 0, stream>>>(a, strips);
+        bwd_wide_sums_kernel<XD, DD><<<grid_for(tiles * strips, kThreads), kThreads, 0, stream>>>(a, strips);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    if (a.dx) bwd_wide_dx_kernel<XD, DD><<<grid_for(a.rows), 1024, 0, stream>>>(a);
+    if (a.dx) bwd_wide_dx_kernel<XD, DD><<<grid_for(a.rows, 1024), 1024, 0, stream>>>(a);
     return hipGetLastError();
 }
 
@@ -377,7 +377,7 @@ hipError_t launch_layernorm_bwd(const NormBwd& f, hipStream_t stream) {
     }
     if (!grads || !joined) return e;
     const int64_t tiles = (2 * f.cols + 63) / 64;
-    bwd_join_kernel<<<grid_for(tiles), 1024, 0, stream>>>((const float*)f.workspace, strips, f.cols, f.dweight, f.dbias,
+    bwd_join_kernel<<<grid_for(tiles, 1024), 1024, 0, stream>>>((const float*)f.workspace, strips, f.cols, f.dweight, f.dbias,
                                                           f.grad_dt, f.accumulate);
     return hipGetLastError();
 }

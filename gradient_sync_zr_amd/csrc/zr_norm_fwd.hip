@@ -191,7 +191,7 @@ hipError_t fwd_run(const FwdArgs& a, hipStream_t stream) {
     constexpr int B = norm_block(TPR), G = B / TPR;
     const int64_t groups = (a.rows + G - 1) / G;
     const int64_t most = 1024 * kThreads / B;
-    fwd_kernel<XD, TPR, NV><<<grid_for(groups < most ? groups : most), B, 0, stream>>>(a);
+    fwd_kernel<XD, TPR, NV><<<grid_for(groups < most ? groups : most, B), B, 0, stream>>>(a);
     return hipGetLastError();
 }
 
@@ -206,7 +206,7 @@ hipError_t fwd_pick(const FwdArgs& a, hipStream_t stream) {
     if (n <= 8192) return fwd_run<XD, 512, 2>(a, stream);
     if (n <= 12288) return fwd_run<XD, 512, 3>(a, stream);
     if (n <= 16384) return fwd_run<XD, 512, 4>(a, stream);
-    fwd_wide_kernel<XD><<<grid_for(a.rows), 1024, 0, stream>>>(a);
+    fwd_wide_kernel<XD><<<grid_for(a.rows, 1024), 1024, 0, stream>>>(a);
     return hipGetLastError();
 }
 

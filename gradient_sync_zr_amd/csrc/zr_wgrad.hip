@@ -652,26 +652,26 @@ __global__ __launch_bounds__(kThreads) void wgrad_join_kernel(WgradArgs a) {
 
 template <int FMT>
 hipError_t run_large(const WgradArgs& a, hipStream_t stream) {
-    wgrad_big_kernel<FMT><<<grid_for(a.full + a.rest * a.parts), kBigThreads, 0, stream>>>(a);
+    wgrad_big_kernel<FMT><<<grid_for(a.full + a.rest * a.parts, kBigThreads), kBigThreads, 0, stream>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.parts == 1) return e;
-    wgrad_big_join_kernel<<<grid_for(a.rest * 65), kThreads, 0, stream>>>(a);
+    wgrad_big_join_kernel<<<grid_for(a.rest * 65, kThreads), kThreads, 0, stream>>>(a);
     return hipGetLastError();
 }
 
 template <int DD, int FMT>
 hipError_t run_small(const WgradArgs& a, hipStream_t stream) {
     const int64_t total = (int64_t)a.tiles_m * a.tiles_n * a.splits;
-    wgrad_kernel<DD, FMT, kWgradTile, kWgradTile, 64, 64, DD == kBf16 ? 64 : 32><<<grid_for(total), 256, 0, stream>>>(a);
+    wgrad_kernel<DD, FMT, kWgradTile, kWgradTile, 64, 64, DD == kBf16 ? 64 : 32><<<grid_for(total, 256), 256, 0, stream>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.splits == 1) return e;
     const int v = a.out * a.in >= (int64_t)1 << 20 ? 4 : 1;
     const int64_t n = kThreads * v;
     const int64_t items = a.out * ((a.in + n - 1) / n) + (a.db ? (a.out + n - 1) / n : 0);
     if (v == 4)
-        wgrad_join_kernel<4><<<grid_for(items), kThreads, 0, stream>>>(a);
+        wgrad_join_kernel<4><<<grid_for(items, kThreads), kThreads, 0, stream>>>(a);
     else
-        wgrad_join_kernel<1><<<grid_for(items), kThreads, 0, stream>>>(a);
+        wgrad_join_kernel<1><<<grid_for(items, kThreads), kThreads, 0, stream>>>(a);
     return hipGetLastError();
 }
 
