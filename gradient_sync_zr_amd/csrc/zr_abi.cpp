@@ -309,8 +309,12 @@ constexpr int64_t kMaxCols = (int64_t)1 << 30;
 
 bool fmt_valid(int dt) { return dt == ZR_CKPT_E4M3 || dt == ZR_CKPT_INT8; }
 int64_t pitch_of(int64_t cols) { return (cols + 31) / 32 * 32; }
-// rows x ld, ld rounded up to whole blocks, within 2^40.
-bool size_valid(int64_t rows, int64_t ld) { return rows >= 0 && ld >= 1 && rows <= kMaxElems / pitch_of(ld); }
+// rows x ld, ld rounded up to whole blocks, within 2^40 (ld may be any number:
+// it is rounded up only where that cannot overflow).
+bool size_valid(int64_t rows, int64_t ld) {
+    if (rows <= 0 || ld < 1) return rows == 0 && ld >= 1;
+    return ld <= kMaxElems && rows <= kMaxElems / pitch_of(ld);
+}
 
 // A strided matrix's bytes: `rows` spans of `width`, `pitch` apart.
 struct Mat {
