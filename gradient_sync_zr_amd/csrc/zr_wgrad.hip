@@ -78,7 +78,8 @@ __device__ __forceinline__ void decode16(const u32x4& q, uint32_t s, uint32_t w[
 }
 
 // Three bf16 terms (upper halves of a word each) that add up to v: each takes
-// the next 8 mantissa bits. An infinity has one term.
+// the next 8 mantissa bits. (Bits of v below 2^-133, which bf16 does not reach,
+// are dropped: |v| < 2^-110 only.) An infinity has one term.
 __device__ __forceinline__ void split3(float v, uint32_t t[3]) {
     const uint32_t u = __float_as_uint(v);
     t[0] = u & 0xFFFF0000u;

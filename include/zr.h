@@ -653,7 +653,8 @@ size_t zr_ckpt_wgrad_workspace_bytes(int64_t rows, int64_t out_cols, int64_t in_
  * Gradients of a linear layer y = x W^T + b from the checkpoint of its input:
  *     dw[o, i] = sum over rows of dy[t, o] * x[t, i], dbias[o] = sum of dy[t, o]
  * with exact products (x is held exactly in bf16; fp32 dy is taken in three
- * bf16 terms) summed in fp32 on the matrix units, each rounded once to grad_dt.
+ * bf16 terms, exactly but for what lies below 2^-133, bf16's last bit) summed
+ * in fp32 on the matrix units, each rounded once to grad_dt.
  *
  *  dy         rows x out_cols, dy_dt ZR_BF16 or ZR_FP32, row stride ld_dy
  *  ckpt       checkpoint of the rows x in_cols input
