@@ -1083,7 +1083,8 @@ zr_status zr_layernorm_fwd(const void* x, zr_dtype x_dt, int64_t rows, int64_t c
         if (held && ckpt_x) return fail(ZR_ERR_INVALID, "ckpt_x is given for an x that is a checkpoint");
         ZR_TRY(check_cols(rows, cols, "cols"));
         if (!(eps >= 0.0f && eps <= 3.4e38f)) return fail(ZR_ERR_INVALID, "eps=%g is not >= 0 and finite", (double)eps);
-        if (!y && !mean && !rstd && !ckpt_x && !ckpt_y) return fail(ZR_ERR_INVALID, "no output is given");
+        // (without rows the outputs are empty, and an empty tensor's address is NULL)
+        if (rows > 0 && !y && !mean && !rstd && !ckpt_x && !ckpt_y) return fail(ZR_ERR_INVALID, "no output is given");
         Buffers b;
         ZR_TRY(held ? b.ckpt(false, x, rows, cols, "x") : b.matrix(false, x, dt_bytes(x_dt), rows, cols, ld_x, "x"));
         if (weight) ZR_TRY(b.vector(false, weight, dt_bytes(param_dt), cols, "weight"));
@@ -1124,7 +1125,7 @@ zr_status zr_layernorm_bwd(const void* dy, zr_dtype dy_dt, int64_t ld_dy, const 
                         (int)dy_dt, (int)x_dt, (int)param_dt, (int)dx_dt, (int)grad_dt);
         if (flags & ~(ZR_ACCUMULATE | ZR_ADD_DX)) return fail(ZR_ERR_INVALID, "flags=%d has unknown bits", flags);
         ZR_TRY(check_cols(rows, cols, "cols"));
-        if (!dx && !dweight && !dbias) return fail(ZR_ERR_INVALID, "no output is given");
+        if (rows > 0 && !dx && !dweight && !dbias) return fail(ZR_ERR_INVALID, "no output is given");
         Buffers b;
         ZR_TRY(b.matrix(false, dy, dt_bytes(dy_dt), rows, cols, ld_dy, "dy"));
         ZR_TRY(held ? b.ckpt(false, x, rows, cols, "x") : b.matrix(false, x, dt_bytes(x_dt), rows, cols, ld_x, "x"));

@@ -23,3 +23,18 @@ def test_arguments_are_checked_all_the_same():
                                                             dy_dtype=BF, x_dtype=BF, grad_dtype=FP, stream=0))
     expect(zr.ZR_ERR_ALIAS, lambda **k: zr.zr_ckpt_wgrad(A, B, 0, 40, 64, E, dbias=E + 4, accumulate=True, dy_dtype=BF,
                                                          grad_dtype=FP, stream=0))
+
+
+def test_outputs_without_rows_have_no_address():
+    """An empty tensor's address is 0, which is an output's that is not given, too: without rows both are no work."""
+    lib = zr.lib()
+    for x_dt in (BF, zr.ZR_CKPT_E4M3):
+        assert lib.zr_layernorm_fwd(None, x_dt, 0, 64, 64, E, F, BF, 1e-5, None, BF, 64, None, None, None, None, BF,
+                                    None) == zr.ZR_OK
+        assert lib.zr_layernorm_bwd(None, BF, 64, None, x_dt, 64, 0, 64, E, BF, None, None, None, BF, 64, None, None, FP, 0,
+                                    None, 0, None) == zr.ZR_OK
+    assert lib.zr_ckpt_pack(None, BF, 0, 64, 64, None, zr.ZR_CKPT_INT8, None) == zr.ZR_OK
+    assert lib.zr_ckpt_unpack(None, zr.ZR_CKPT_INT8, 0, 64, None, BF, 64, None) == zr.ZR_OK
+    # with rows an output is needed
+    assert lib.zr_layernorm_fwd(A, BF, 1, 64, 64, E, F, BF, 1e-5, None, BF, 64, None, None, None, None, BF,
+                                None) == zr.ZR_ERR_INVALID
