@@ -167,6 +167,15 @@ class CkptNormLinear:
     are the caller's; they come between the methods:
         forward(x, w, b, y);  z = y W^T
         backward_linear(dz);  dy = dz W;  backward_norm(dy, w, dx)
+
+    Statistics: backward_norm takes xh = (held x - mean) * rstd with the mean and
+    rstd of the forward pass, of x itself. With `recompute`, backward_linear
+    norms the held x anew, with the held values' own mean and rstd; so the y that
+    it multiplies differs from the forward pass's, and its xh from
+    backward_norm's, by what the 8 bits lost.
+
+    The layer's buffers belong to the stream that is current when it is made: it
+    has to outlive what its methods enqueue on another.
     """
 
     def __init__(self, flat_grad, offset: int, rows: int, cols: int, out_cols: int, scratch=None,

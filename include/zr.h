@@ -624,7 +624,10 @@ size_t zr_layernorm_workspace_bytes(int64_t rows, int64_t cols);
  *
  *  dy, x      dy_dt ZR_BF16 or ZR_FP32; x as in the forward pass (values or a
  *             checkpoint)
- *  mean, rstd fp32, rows elements, of the forward pass
+ *  mean, rstd fp32, rows elements, of the forward pass: over x itself, also
+ *             where x is now its checkpoint (xh is then off by what the 8 bits
+ *             lost), or over the checkpoint, whose statistics are those of the
+ *             held values
  *  dx         dx_dt ZR_BF16 or ZR_FP32, or NULL. dx may be dy or x (same
  *             address, type and row stride)
  *  dweight, dbias   cols elements of grad_dt; each may be NULL
