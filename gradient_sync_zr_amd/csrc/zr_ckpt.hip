@@ -6,7 +6,7 @@
 // vectors of 8 columns, 256 lanes apart, kCkptVecs of them with all loads in
 // front, over the rows laid end to end (each padded to whole blocks, so the 4
 // lanes of a block never part). Bound by memory: 65536x4096 bf16 to e4m3 packs in
-// 152 us (5.36 TB/s) and unpacks in 133 (6.1); with 8 vectors a lane 168 and 146,
+// 147 to 152 us (5.4 to 5.5 TB/s) and unpacks in 134 (6.1); with 8 vectors a lane 168 and 146,
 // without the accesses past the caches 172 and 143.
 #include <hip/hip_runtime.h>
 

@@ -221,11 +221,15 @@ ZR_KERNELS hipError_t launch_ckpt_unpack(const void* ckpt, zr_dtype fmt, int64_t
                                          zr_dtype dt, int64_t ld, hipStream_t stream);
 
 // How a weight gradient is cut. Both forms' times come from a model fitted to
-// sweeps over 11 shapes (rows 128 to 65,536, dW 128 x 128 to 4096 x 4096; its
-// choices are within 10% of the best measured), and the smaller one is taken:
+// sweeps with bf16 dY over 11 shapes (rows 128 to 65,536, dW 128 x 128 to 4096 x
+// 4096; its choices were within 10% of the best measured), and the smaller one is
+// taken. fp32 dY, of three products, is cut by the same numbers, though a slab of
+// it takes a small block about 4.9 us (1001x777x1000: 20 us for 4 slabs), so where
+// tiles are few it gets fewer parts than would be best:
 //  - a slab of 64 rows takes a small block 0.95 us alone, 1.05 with one block
 //    on every CU and 1.4 with two; a large block 1.46 alone, 1.9 with all;
-//  - joining costs 5 us and 0.35 us per MB of parts.
+//  - joining costs 5 us and 0.35 us per MB of parts (more than it does where the
+//    parts are small: 9.4 us for 1001x777x1000's, which take 5.2).
 //
 // Small form: tiles of 128 x 128, the sum over rows in `splits` parts of `span`
 // rows. More parts fill the chip where there are few tiles, but each writes

@@ -2,8 +2,9 @@
 // checkpoints. With xh = (x - mean) * rstd and g = dy * w, per row of n columns:
 //     dx = rstd * (g - sum(g) / n - xh * sum(g * xh) / n)
 //     dw = sum over rows of dy * xh,  db = sum over rows of dy
-// all in fp32. Rows too wide for registers (over 12288 columns) are read again
-// from memory in each pass.
+// all in fp32. Rows over 12288 columns, whose fp32 copies do not fit the registers
+// beside the column sums, are read from memory in each pass: x and dy twice for dx,
+// and once more for the parameters' gradients (4096x16384 bf16 150 us, 2.7 TB/s).
 //
 // The weight's and the bias's gradient are column sums over all rows. A block
 // keeps its columns' sums in registers over the strip of rows that it walks
@@ -16,11 +17,13 @@
 // rounded once), xh and g stay in registers between the row's sums and dx, and
 // dx is two multiply-adds. The next row's loads are in flight meanwhile.
 //
-// Bound by memory: 16384x4096 bf16 78 us (5.2 TB/s), 97 with dx added to (5.5),
-// 24576x11008 from int8 241 (5.65 TB/s; 532 before the arithmetic was cut and the
+// Bound by memory: 16384x4096 bf16 78 us (5.2 TB/s), 96 with dx added to (5.6),
+// 24576x11008 from int8 240 (5.65 TB/s; 532 before the arithmetic was cut and the
 // loads put ahead). 512 strips, two blocks of 256 or one of 512 per CU, measured
-// best up to 4096 columns (65536x1024: 78 us, with 1024 strips 90), 256 beyond,
-// where a block of 512 has the CU's registers.
+// best at 1024 columns (65536x1024: 78 us, with 1024 strips 90) and are taken up to
+// 4096, though the forms up to 512 and from 1025 to 2048 columns, of 100 to 119
+// registers, would leave room for twice as many (262144x128: 44 us, 4.6 TB/s); 256
+// beyond, where a block of 512 has the CU's registers.
 #include <hip/hip_runtime.h>
 
 #include "zr_norm.hpp"

@@ -5,19 +5,25 @@
 // Mean and variance come from the row's registers in two passes (no
 // cancellation), all in fp32. Blocks walk over the rows with the weight and
 // bias in registers and the next row's loads in flight while a row is reduced
-// and written. Rows too wide for registers (over 16384 columns) are read again
-// from memory in each pass.
+// and written. Of rows over 16384 columns the fp32 copy does not fit beside the
+// weights: they are read from memory in each of three passes (4096x20000 bf16 100
+// us, 3.3 TB/s).
 //
 // Bound by memory, and by the arithmetic of checkpoints: 16384x4096 bf16 takes 48
-// us (5.5 TB/s; 86 before the next row's loads were in flight and the weights
-// kept), 64 with x's checkpoint, 37 to 40 from an e4m3 checkpoint (5.1 to 5.5
-// TB/s; 45 while every vector was masked by the element and lanes 16 and 32 apart
-// were added through LDS); 24576x11008 179 us (6.05 TB/s, 201 so), 156 (216) from
-// e4m3, and 343 with the checkpoint of y too. A wave's own mean and squares,
-// joined with one barrier a row, instead of two passes with two: 43 us where they
-// took 40, as the vector instructions count, not the barriers. Two vectors of 8
-// columns a lane measured best: with one (512 lanes a row) 16384x4096 took 59 us
-// for 52; and 1024 blocks of 256, which are what the chip holds at once (2048: 56).
+// to 50 us (5.4 TB/s; 86 before the next row's loads were in flight and the weights
+// kept), 64 with x's checkpoint, 36 to 42 from an e4m3 checkpoint (4.8 to 5.7 TB/s;
+// 45 while every vector was masked by the element and lanes 16 and 32 apart were
+// added through LDS), 46 from one checkpoint to another (3.0 TB/s: decoding and
+// encoding); from fp32 72 us, 87 with x's checkpoint. 24576x11008 179 us (6.0 TB/s,
+// 201 so), 154 (216) from e4m3, and 343 with the checkpoint of y too: there three
+// vectors a lane take 156 to 158 registers, one block of 512 a CU, whose waves are
+// too few to hide the encoding. A wave's own mean and squares, joined with one
+// barrier a row, instead of two passes with two: 43 us where they took 40, as the
+// vector instructions count, not the barriers. Two vectors of 8 columns a lane
+// measured best: with one (512 lanes a row) 16384x4096 took 59 us for 52; and 1024
+// blocks of 256 (512 of 512), which up to 8192 columns are what the chip holds at
+// once (2048: 56). Beyond, from bf16 and fp32, it holds half of them, and they go in
+// two rounds.
 #include <hip/hip_runtime.h>
 
 #include "zr_norm.hpp"

@@ -26,10 +26,10 @@
 // LDS and writes 32 for a slab of 64 rows, 768 cycles at 128 bytes each, and
 // multiplies for 515; two blocks a CU hide each other's barriers:
 // 16384x11008x4096 in 2,168 us, 681 TFLOP/s. With fp32 dY it does three times the
-// products: 16384x4096x4096 in 1,640 us, 1,005 TFLOP/s of the matrix units. Loads
-// two slabs ahead (which leave room for one block a CU) and operands read two
-// steps ahead, as in the large form, both measured slower here (21232x176x1312:
-// 69 and 43 us, not 41).
+// products: 16384x4096x4096 in 1,600 to 1,640 us, 1,005 to 1,030 TFLOP/s of the
+// matrix units. Loads two slabs ahead (which leave room for one block a CU) and
+// operands read two steps ahead, as in the large form, both measured slower here
+// (21232x176x1312: 69 and 43 us, not 41).
 #include <hip/hip_runtime.h>
 
 #include "zr_ckpt.hpp"
@@ -349,11 +349,11 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wgrad_kernel(Wg
 // slab of 64 rows costs a CU 2,061 cycles of matrix units and reads 192 KB from
 // LDS (1,536 cycles at 128 bytes a cycle) where four tiles of 128 x 128 would
 // read 256 KB. Each wave's 128 fp32 accumulators leave 128 registers for
-// operands and the next slab. 16384x11008x4096 takes 1,370 to 1,480 us from run
-// to run (1,000 to 1,080 TFLOP/s at 2.0 GHz; 688 tiles are 2.7 rounds of 256),
+// operands and the next slab. 16384x11008x4096 takes 1,330 to 1,480 us from run
+// to run (1,000 to 1,110 TFLOP/s at 2.0 GHz; 688 tiles are 2.7 rounds of 256),
 // where the library's bf16 product of such operands takes 1,570 to 1,640;
-// 2048x4096x4096 72 to 78 us, the library's 65 to 70. The matrix units are busy
-// 55% of the time and LDS 41%: the rest is the steps' latency. Operands three
+// 2048x4096x4096 71 to 82 us, the library's 65 to 70. The matrix units are busy
+// 54% of the time and LDS 41%: the rest is the steps' latency. Operands three
 // steps ahead do not fit the registers.
 constexpr int kBigThreads = 512, kBigBK = 64;
 

@@ -602,8 +602,8 @@ zr_status zr_ckpt_unpack(const void* ckpt, zr_dtype format, int64_t rows, int64_
  *  ckpt_y     NULL, or a checkpoint that receives y as rounded to y_dt
  *             (with y NULL too): the input of the linear layer behind the norm
  *  ckpt_format    of ckpt_x and ckpt_y
- * At least one output, if there are rows; outputs overlap neither each other nor an input, but
- * y may be x (same address, type and row stride).
+ * At least one output, if there are rows; outputs overlap neither each other
+ * nor an input, but y may be x (same address, type and row stride).
  */
 zr_status zr_layernorm_fwd(const void* x, zr_dtype x_dt, int64_t rows, int64_t cols, int64_t ld_x,
                            const void* weight, const void* bias, zr_dtype param_dt, float eps,
