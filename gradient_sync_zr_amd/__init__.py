@@ -866,7 +866,9 @@ def zr_layernorm_fwd(x, rows: int, cols: int, y=None, weight=None, bias=None, ep
     """Layer norm of x's rows into y; mean and rstd (fp32), if given, receive
     the statistics, ckpt_x and ckpt_y the 8-bit checkpoints of x and y. With
     x_dtype a checkpoint format, x is a checkpoint. y_dtype: of y, and with y
-    None, what ckpt_y's values are rounded to (default bf16)."""
+    None, what ckpt_y's values are rounded to (default bf16). Buffers given as
+    addresses need their dtype argument (weight and bias: param_dtype, unless
+    one of them is a tensor)."""
     px, xd, ldx = _source(x, rows, cols, x_dtype, ld_x)
     if y is None:
         py, yd, ldy = 0, ZR_BF16 if y_dtype is None else _dtype(y_dtype), cols
@@ -890,7 +892,9 @@ def zr_layernorm_bwd(dy, x, rows: int, cols: int, mean, rstd, weight=None, dx=No
                      stream=None) -> None:
     """Gradients of zr_layernorm_fwd: of its input (dx, added to with add_dx)
     and of its weight and bias (dweight, dbias, added to with accumulate, with
-    a workspace of zr_layernorm_workspace_bytes)."""
+    a workspace of zr_layernorm_workspace_bytes). Buffers given as addresses
+    need their dtype argument (weight: param_dtype; dweight and dbias:
+    grad_dtype, unless one of them is a tensor)."""
     pdy, dyd, lddy = _matrix(dy, rows, cols, dy_dtype, ld_dy, "dy")
     px, xd, ldx = _source(x, rows, cols, x_dtype, ld_x)
     pdx, dxd, lddx = _matrix(dx, rows, cols, dx_dtype, ld_dx, "dx")
