@@ -80,8 +80,9 @@
  *                        units always move as vectors); small: every ring-order
  *                        reduce-scatter uses one-slice tiles; large: none does;
  *                        other values are reported on stderr and ignored;
- *      ZR_MAX_GRID=n     at most n blocks per launch (default 2^30), the
- *                        blocks striding over the tiles beyond them.
+ *      ZR_MAX_GRID=n     at most n blocks per launch (default 2^30; a launch
+ *                        also has fewer than 2^32 threads), the blocks
+ *                        striding over the tiles beyond them.
  */
 #ifndef ZR_H
 #define ZR_H
