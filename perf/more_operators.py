@@ -380,16 +380,18 @@ def _calls(s):
     if kind in ("clip", "step"):
         numels = s["numels"]
         ws = _workspace(s, zr.zr_grad_norm_workspace_bytes(len(numels)))
-        zr.zr_grad_norm(s["grads"], numels, s["norm"], s["coef"], max_norm=1.0 if kind == "clip" else case["max_norm"],
+        if kind == "step" and "tables" not in s:  # what an optimizer keeps of its state: a table of each list
+            s["tables"] = {k: zr.tensor_table(x, numels) for k, x in (s["views"] | {"grads": s["grads"]}).items()}
+        t = s["tables"] if kind == "step" else s
+        zr.zr_grad_norm(t["grads"], numels, s["norm"], s["coef"], max_norm=1.0 if kind == "clip" else case["max_norm"],
                         scale=case["scale"] if kind == "clip" else 1.0, workspace=ws)
         r = {"norm": s["norm"], "coef": s["coef"]}
         if kind == "clip":
             zr.zr_grad_scale(s["grads"], numels, s["coef"], s["outs"])
             return r | {"outs": s["outs"]}
-        v = s["views"]
-        zr.zr_adamw(s["grads"], numels, v["p"], v["m"], v["v"], step=STEP, lr=LR, beta1=BETA1, beta2=BETA2,
-                    eps=ADAM_EPS, weight_decay=DECAY, shards=v.get("shard"), coef=s["coef"])
-        return r | {k: s[k] for k in v}
+        zr.zr_adamw(t["grads"], numels, t["p"], t["m"], t["v"], step=STEP, lr=LR, beta1=BETA1, beta2=BETA2,
+                    eps=ADAM_EPS, weight_decay=DECAY, shards=t.get("shard"), coef=s["coef"])
+        return r | {k: s[k] for k in s["views"]}
     rows = case["rows"]
     if kind == "rms":
         zr.zr_rmsnorm_fwd(s["x"], rows, case["cols"], s["y"], s["w"], eps=EPS, residual=s.get("residual"),
