@@ -81,11 +81,12 @@ PF_EXPORTS = ("zr_pf_create", "zr_pf_fetch", "zr_pf_release", "zr_pf_full", "zr_
               "zr_pf_destroy", "zr_pf_plan")
 NORM_EXPORTS = ("zr_ckpt_pack", "zr_ckpt_unpack", "zr_layernorm_fwd", "zr_layernorm_bwd", "zr_ckpt_wgrad",
                 "zr_ckpt_bytes", "zr_layernorm_workspace_bytes", "zr_ckpt_wgrad_workspace_bytes")
+GRAD_EXPORTS = ("zr_grad_norm", "zr_grad_scale", "zr_adamw", "zr_grad_norm_workspace_bytes")
 EXPORTS = ("zr_last_error", "zr_version", "zr_workspace_bytes", "zr_flatten_bucket", "zr_reduce_scatter_avg",
            "zr_reduce_scatter_frags", "zr_all_gather", "zr_allreduce", "zr_plan_buckets", "zr_sched_create",
            "zr_sched_acquire", "zr_sched_submit_rs", "zr_sched_flush",
            "zr_sched_destroy", "zr_reduce_scatter_frags_noalloc") + COST_EXPORTS + PF_EXPORTS + \
-    RSF_PLAN_EXPORTS + FLAT_PLAN_EXPORTS + RS_PLAN_EXPORTS + NORM_EXPORTS
+    RSF_PLAN_EXPORTS + FLAT_PLAN_EXPORTS + RS_PLAN_EXPORTS + NORM_EXPORTS + GRAD_EXPORTS
 
 
 class ZrError(RuntimeError):
@@ -195,6 +196,12 @@ def lib() -> ctypes.CDLL:
         for f in NORM_EXPORTS[5:]:
             getattr(L, f).restype = _sz
         _d = ctypes.c_double
+        _I64s = ctypes.POINTER(_i64)
+        L.zr_grad_norm.argtypes = [_i32, _PP, _I64s, _i32, _d, _d, _vp, _vp, _vp, _sz, _vp]
+        L.zr_grad_scale.argtypes = [_i32, _PP, _I64s, _i32, _PP, _i32, _vp, _vp]
+        L.zr_adamw.argtypes = [_i32, _PP, _i32, _I64s, _PP, _PP, _PP, _PP] + [_d] * 5 + [_i64, _vp, _vp]
+        L.zr_grad_norm_workspace_bytes.argtypes = [_i32]
+        L.zr_grad_norm_workspace_bytes.restype = _sz
         for f in ("zr_cost_ring_allreduce", "zr_cost_ring_reduce_scatter",
                   "zr_cost_tree_allreduce", "zr_cost_naive_allreduce"):
             getattr(L, f).argtypes = [_i32, _d, _d, _d]
@@ -921,3 +928,134 @@ def zr_ckpt_wgrad(dy, ckpt, rows: int, out_cols: int, in_cols: int, dw, dbias=No
                                pdw, _one_dtype((pdw, gd), gb, ("dw", "dbias")), lddw, gb[0],
                                ZR_ACCUMULATE if accumulate else 0, ws, wsb,
                                _run_on(stream, dy, ckpt, dw, dbias, workspace)))
+
+
+# ------------------------------------- gradient norm, clipping and AdamW
+class TensorTable:
+    """A list of tensors checked once (one dtype, one GPU, contiguous, of the
+    sizes `numels`), for calls over the same buffers again and again:
+    ``tensor_table``. It keeps the tensors alive."""
+
+    def __init__(self, xs: Sequence, numels, dtype=None, name: str = "tensors"):
+        at, code, device = _list(xs, numels, dtype, name)
+        self.table, self.dtype, self.device = _table(at), code, device
+        self.numels, self._keep = _sizes(numels), list(xs)
+        self._n = len(at)
+
+    def __len__(self):
+        return self._n
+
+
+def tensor_table(xs: Sequence, numels: Sequence[int], dtype=None) -> TensorTable:
+    """A reusable, checked table of tensors (or addresses, of `dtype`)."""
+    return TensorTable(xs, numels, dtype)
+
+
+def _sizes(numels):
+    return numels if isinstance(numels, ctypes.Array) else _int64s(numels)
+
+
+def _list(xs, numels, dtype, name):
+    """(addresses, dtype, GPU or None) of a list of tensors or addresses with these numbers of elements."""
+    if len(xs) != len(numels):
+        raise ValueError(f"{name} has {len(xs)} entries, numels {len(numels)}")
+    code = None if dtype is None else _dtype(dtype)
+    device = kind = None
+    at = []
+    for x, n in zip(xs, numels):
+        if x.__class__ is int:
+            at.append(x)
+            continue
+        if x.dtype is not kind or x.get_device() != device:
+            real = _real(x.dtype)
+            if (kind is not None or code is not None) and real != code:
+                raise ValueError(f"{name} has tensors of {x.dtype} among others, or not what its dtype says")
+            if device is not None and x.get_device() != device:
+                raise ValueError(f"{name} has tensors on GPUs {device} and {x.get_device()}")
+            if x.get_device() < 0:
+                raise ValueError("a tensor is not on the GPU")
+            kind, code, device = x.dtype, real, x.get_device()
+        if x.numel() != n or not x.is_contiguous():
+            raise ValueError(f"{name} has a tensor that is not {n} contiguous elements")
+        at.append(x.data_ptr())
+    if code is None:
+        if any(at):
+            raise ValueError(f"{name} is addresses: its dtype is needed")
+        code = ZR_FP32
+    return at, code, device
+
+
+def _many(xs, numels, dtype, name, gpus):
+    """(C table, dtype) of one list of a call; its GPU joins `gpus`."""
+    if xs.__class__ is TensorTable:
+        if len(xs) != len(numels) or (xs.numels is not numels and list(xs.numels)[:len(xs)] != list(numels)[:len(xs)]):
+            raise ValueError(f"{name} is a table of other sizes")
+        if dtype is not None and _dtype(dtype) != xs.dtype:
+            raise ValueError(f"{name} is not what its dtype argument says")
+        gpus.append(xs.device)
+        return xs.table, xs.dtype
+    at, code, device = _list(xs, numels, dtype, name)
+    gpus.append(device)
+    return _table(at), code
+
+
+def _run_on_gpus(stream, gpus, *xs) -> int:
+    """_run_on for lists on these GPUs (None: addresses) and more tensors."""
+    on = _run_on(stream, *xs)
+    here = {g for g in gpus if g is not None}
+    if here:
+        if _raw_stream is None:
+            _find_lookups()
+        now = _current_gpu()
+        if here != {now}:
+            raise ValueError(f"the tensors are on GPU {sorted(here)}, the current one is {now}: make theirs current, "
+                             "and its stream")
+    return on
+
+
+def _scalar(x, name):
+    """Address of one fp32 on the device: a tensor of one element, an address, or None."""
+    return _vector(x, 1, ZR_FP32, name)[0]
+
+
+def zr_grad_norm_workspace_bytes(n: int) -> int:
+    return lib().zr_grad_norm_workspace_bytes(n)
+
+
+def zr_grad_norm(grads, numels: Sequence[int], norm=None, coef=None, max_norm: float = float("inf"), scale: float = 1.0,
+                 workspace=None, dtype=None, stream=None) -> None:
+    """The norm of all `grads` together, times scale, into `norm` (one fp32 on
+    the GPU), and scale * min(1, max_norm / norm) into `coef`. grads: a list of
+    tensors (or addresses, of `dtype`) of numels elements, or a
+    ``tensor_table``."""
+    gpus = []
+    t, dt = _many(grads, numels, dtype, "grads", gpus)
+    ws, wsb = _workspace(workspace)
+    _check(lib().zr_grad_norm(len(numels), t, _sizes(numels), dt, scale, max_norm, _scalar(norm, "norm"),
+                              _scalar(coef, "coef"), ws, wsb, _run_on_gpus(stream, gpus, norm, coef, workspace)))
+
+
+def zr_grad_scale(grads, numels: Sequence[int], coef, outs=None, dtype=None, out_dtype=None, stream=None) -> None:
+    """coef (one fp32 on the GPU) times every tensor of `grads`, into `outs` or
+    in place."""
+    gpus = []
+    t, dt = _many(grads, numels, dtype, "grads", gpus)
+    o, odt = (None, dt) if outs is None else _many(outs, numels, out_dtype, "outs", gpus)
+    _check(lib().zr_grad_scale(len(numels), t, _sizes(numels), dt, o, odt, _scalar(coef, "coef"),
+                               _run_on_gpus(stream, gpus, coef)))
+
+
+def zr_adamw(grads, numels: Sequence[int], params, exp_avg, exp_avg_sq, step: int, lr: float, beta1: float = 0.9,
+             beta2: float = 0.999, eps: float = 1e-8, weight_decay: float = 0.01, shards=None, coef=None, dtype=None,
+             stream=None) -> None:
+    """One AdamW update of the fp32 params and their moments from coef * grads
+    (coef: one fp32 on the GPU, of zr_grad_norm; the update is left out where it
+    is not finite); shards, if given, receive the params in bf16. Lists as in
+    zr_grad_norm; `dtype` is that of grads given as addresses."""
+    gpus = []
+    t, dt = _many(grads, numels, dtype, "grads", gpus)
+    p, m, v = (_many(xs, numels, ZR_FP32, name, gpus)[0]
+               for xs, name in ((params, "params"), (exp_avg, "exp_avg"), (exp_avg_sq, "exp_avg_sq")))
+    s = None if shards is None else _many(shards, numels, ZR_BF16, "shards", gpus)[0]
+    _check(lib().zr_adamw(len(numels), t, dt, _sizes(numels), p, m, v, s, lr, beta1, beta2, eps, weight_decay, step,
+                          _scalar(coef, "coef"), _run_on_gpus(stream, gpus, coef)))

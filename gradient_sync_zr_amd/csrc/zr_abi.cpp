@@ -418,6 +418,62 @@ zr_status need_workspace(Buffers& b, const void* ws, size_t ws_bytes, size_t nee
     return b.vector(true, ws, 4, (int64_t)(need / 4), "workspace");
 }
 
+// ------------------------------------------- calls over many tensors
+// What a call reads and writes, any number of ranges. Ranges that are written
+// must share no byte with any other; sorted by start, each need only be held
+// against the furthest end before it.
+struct Ranges {
+    struct Item {
+        Range r;
+        const char* name;
+        int i;
+        bool out;
+    };
+    std::vector<Item> items;
+
+    void add(bool out, const void* p, int64_t elems, int64_t es, const char* name, int i) {
+        if (elems > 0) items.push_back(Item{range_of(p, elems, es), name, i, out});
+    }
+    zr_status disjoint() {
+        auto before = [](const Item& a, const Item& b) { return a.r.lo < b.r.lo; };
+        if (!std::is_sorted(items.begin(), items.end(), before)) std::sort(items.begin(), items.end(), before);
+        const Item *in = nullptr, *out = nullptr;  // of those so far, the ones that end last
+        for (const Item& x : items) {
+            const Item* hit = out && out->r.hi > x.r.lo ? out : (x.out && in && in->r.hi > x.r.lo ? in : nullptr);
+            if (hit) return fail(ZR_ERR_ALIAS, "%s[%d] overlaps %s[%d]", hit->name, hit->i, x.name, x.i);
+            const Item** last = x.out ? &out : &in;
+            if (!*last || (*last)->r.hi < x.r.hi) *last = &x;
+        }
+        return ok();
+    }
+};
+
+zr_status check_tensors(int n, const void* grads, const int64_t* numels) {
+    if (n < 0) return fail(ZR_ERR_INVALID, "n=%d is negative", n);
+    if (n > 0 && (!grads || !numels)) return fail(ZR_ERR_INVALID, "the table of tensors or of sizes is NULL");
+    int64_t total = 0;
+    return check_sizes(numels, n, &total);
+}
+
+// A table's entries: addresses (of tensors that have elements) aligned to es bytes.
+zr_status check_list(Ranges* r, bool out, const void* const* t, const int64_t* numels, int n, int64_t es, const char* name) {
+    if (n > 0 && !t) return fail(ZR_ERR_INVALID, "%s table is NULL", name);
+    for (int i = 0; i < n; ++i) {
+        if (numels[i] == 0) continue;
+        if (!t[i]) return fail(ZR_ERR_INVALID, "%s[%d] is NULL", name, i);
+        if ((uintptr_t)t[i] & (uintptr_t)(es - 1))
+            return fail(ZR_ERR_ALIGN, "%s[%d]=%p is not aligned to %lld bytes", name, i, t[i], (long long)es);
+        r->add(out, t[i], numels[i], es, name, i);
+    }
+    return ok();
+}
+
+zr_status check_scalar(Ranges* r, bool out, const float* p, const char* name) {
+    if ((uintptr_t)p & 3) return fail(ZR_ERR_ALIGN, "%s=%p is not aligned to 4 bytes", name, (const void*)p);
+    r->add(out, p, p ? 1 : 0, 4, name, 0);
+    return ok();
+}
+
 }  // namespace
 
 // The prefetch coordinator's configuration; `buffers` also checks the shard
@@ -1191,6 +1247,102 @@ zr_status zr_ckpt_wgrad(const void* dy, zr_dtype dy_dt, int64_t ld_dy, const voi
         w.accumulate = (flags & ZR_ACCUMULATE) != 0;
         w.workspace = workspace;
         return launched(launch_ckpt_wgrad(w, (hipStream_t)stream), (hipStream_t)stream, "weight gradient launch");
+    });
+}
+
+size_t zr_grad_norm_workspace_bytes(int n) {
+    if (n < 0) return 0;
+    return (size_t)grad_norm_parts(n) * sizeof(double);
+}
+
+zr_status zr_grad_norm(int n, const void* const* grads, const int64_t* numels, zr_dtype dt, double scale, double max_norm,
+                       float* norm, float* coef, void* workspace, size_t ws_bytes, void* stream) {
+    return zr::guarded([&]() -> zr_status {
+        if (!dt_valid(dt)) return fail(ZR_ERR_UNSUPPORTED, "dtype %d not supported", (int)dt);
+        ZR_TRY(check_tensors(n, grads, numels));
+        if (!(scale > 0.0 && scale <= 3.4e38)) return fail(ZR_ERR_INVALID, "scale=%g is not > 0 and finite", scale);
+        if (!(max_norm > 0.0)) return fail(ZR_ERR_INVALID, "max_norm=%g is not > 0", max_norm);
+        if (!norm && !coef) return fail(ZR_ERR_INVALID, "no output is given");
+        Ranges r;
+        r.items.reserve((size_t)n + 3);
+        ZR_TRY(check_list(&r, false, grads, numels, n, dt_bytes(dt), "grads"));
+        ZR_TRY(check_scalar(&r, true, norm, "norm"));
+        ZR_TRY(check_scalar(&r, true, coef, "coef"));
+        const size_t need = zr_grad_norm_workspace_bytes(n);
+        if (need > 0) {
+            if (!workspace || ws_bytes < need)
+                return fail(ZR_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu bytes needed",
+                            workspace ? ws_bytes : 0, need);
+            if ((uintptr_t)workspace & 7) return fail(ZR_ERR_ALIGN, "workspace %p is not 8-byte aligned", workspace);
+            r.add(true, workspace, (int64_t)need, 1, "workspace", 0);
+        }
+        ZR_TRY(r.disjoint());
+        ZR_TRY(have(launch_grad_norm, "gradient norm"));
+        GradNorm f{};
+        f.n = n; f.grads = grads; f.numels = numels; f.dt = dt;
+        f.scale = scale; f.max_norm = max_norm;
+        f.norm = norm; f.coef = coef;
+        f.workspace = workspace;
+        return launched(launch_grad_norm(f, (hipStream_t)stream), (hipStream_t)stream, "gradient norm launch");
+    });
+}
+
+zr_status zr_grad_scale(int n, const void* const* grads, const int64_t* numels, zr_dtype dt, void* const* outs,
+                        zr_dtype out_dt, const float* coef, void* stream) {
+    return zr::guarded([&]() -> zr_status {
+        if (!dt_valid(dt) || !dt_valid(out_dt))
+            return fail(ZR_ERR_UNSUPPORTED, "dtype pair (%d, %d) not supported", (int)dt, (int)out_dt);
+        if (!outs && dt != out_dt) return fail(ZR_ERR_UNSUPPORTED, "dtype %d in place of %d", (int)out_dt, (int)dt);
+        ZR_TRY(check_tensors(n, grads, numels));
+        if (!coef) return fail(ZR_ERR_INVALID, "coef is NULL");
+        Ranges r;
+        r.items.reserve((size_t)n * 2 + 1);
+        if (outs) {
+            ZR_TRY(check_list(&r, false, grads, numels, n, dt_bytes(dt), "grads"));
+            // a tensor may be its own output where the elements are of one type
+            for (Ranges::Item& x : r.items)
+                if (dt == out_dt && outs[x.i] == grads[x.i]) x.r.hi = x.r.lo;
+        }
+        ZR_TRY(check_list(&r, true, outs ? (const void* const*)outs : grads, numels, n, dt_bytes(out_dt),
+                          outs ? "outs" : "grads"));
+        ZR_TRY(check_scalar(&r, false, coef, "coef"));
+        r.items.erase(std::remove_if(r.items.begin(), r.items.end(), [](const Ranges::Item& x) { return x.r.lo == x.r.hi; }),
+                      r.items.end());
+        ZR_TRY(r.disjoint());
+        ZR_TRY(have(launch_grad_scale, "gradient scaling"));
+        GradScale f{};
+        f.n = n; f.grads = grads; f.numels = numels; f.dt = dt; f.out_dt = out_dt; f.outs = outs; f.coef = coef;
+        return launched(launch_grad_scale(f, (hipStream_t)stream), (hipStream_t)stream, "gradient scaling launch");
+    });
+}
+
+zr_status zr_adamw(int n, const void* const* grads, zr_dtype grad_dt, const int64_t* numels, void* const* params,
+                   void* const* exp_avg, void* const* exp_avg_sq, void* const* shards, double lr, double beta1,
+                   double beta2, double eps, double weight_decay, int64_t step, const float* coef, void* stream) {
+    return zr::guarded([&]() -> zr_status {
+        if (!dt_valid(grad_dt)) return fail(ZR_ERR_UNSUPPORTED, "dtype %d not supported", (int)grad_dt);
+        ZR_TRY(check_tensors(n, grads, numels));
+        if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0))
+            return fail(ZR_ERR_INVALID, "beta1=%g or beta2=%g is not in [0, 1)", beta1, beta2);
+        if (!(lr >= 0.0 && lr <= 3.4e38) || !(eps >= 0.0 && eps <= 3.4e38) || !(weight_decay >= 0.0 && weight_decay <= 3.4e38))
+            return fail(ZR_ERR_INVALID, "lr=%g, eps=%g or weight_decay=%g is not >= 0 and finite", lr, eps, weight_decay);
+        if (step < 1) return fail(ZR_ERR_INVALID, "step=%lld is below 1", (long long)step);
+        Ranges r;
+        r.items.reserve((size_t)n * 5 + 1);
+        ZR_TRY(check_list(&r, false, grads, numels, n, dt_bytes(grad_dt), "grads"));
+        ZR_TRY(check_list(&r, true, (const void* const*)params, numels, n, 4, "params"));
+        ZR_TRY(check_list(&r, true, (const void* const*)exp_avg, numels, n, 4, "exp_avg"));
+        ZR_TRY(check_list(&r, true, (const void* const*)exp_avg_sq, numels, n, 4, "exp_avg_sq"));
+        if (shards) ZR_TRY(check_list(&r, true, (const void* const*)shards, numels, n, 2, "shards"));
+        ZR_TRY(check_scalar(&r, false, coef, "coef"));
+        ZR_TRY(r.disjoint());
+        ZR_TRY(have(launch_adamw, "AdamW"));
+        AdamW f{};
+        f.n = n; f.grads = grads; f.numels = numels; f.grad_dt = grad_dt;
+        f.params = params; f.exp_avg = exp_avg; f.exp_avg_sq = exp_avg_sq; f.shards = shards;
+        f.lr = lr; f.beta1 = beta1; f.beta2 = beta2; f.eps = eps; f.weight_decay = weight_decay;
+        f.step = step; f.coef = coef;
+        return launched(launch_adamw(f, (hipStream_t)stream), (hipStream_t)stream, "AdamW launch");
     });
 }
 

@@ -1,0 +1,90 @@
+// AdamW over many tensors, with the gradients multiplied by a coefficient that
+// lies on the device (the clipping's), so that clipping costs no pass:
+//     g' = coef * g
+//     m  = beta1 * m + (1 - beta1) * g'
+//     v  = beta2 * v + (1 - beta2) * g'^2
+//     p  = (1 - lr * decay) * p - lr / (1 - beta1^t) * m / (sqrt(v / (1 - beta2^t)) + eps)
+// in fp32, and p rounded to bf16 as the shard that the all-gather takes. A
+// coefficient that is not finite leaves everything as it was.
+#include <hip/hip_runtime.h>
+
+#include "zr_multi.hpp"
+
+namespace zr {
+namespace {
+
+typedef Multi<5, kAdamPer> AdamTable;
+
+struct AdamArgs {
+    const float* coef;
+    float beta1, rest1, beta2, rest2, keep, rate, inv2, eps;
+};
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void adamw_kernel(AdamTable t5, AdamArgs a, int shards) {
+    const float coef = a.coef ? *a.coef : 1.0f;
+    if (!(__builtin_fabsf(coef) < __builtin_inff())) return;
+    int slot = 0;
+    const int tiles = t5.tile0[t5.count];
+    for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+        slot = multi_slot(t5, slot, t);
+        const int64_t begin = (int64_t)(t - t5.tile0[slot]) * kMultiTile, left = t5.n[slot] - begin;
+        const int c = threadIdx.x * 4;
+        const T* pg = (const T*)t5.p[0][slot] + begin;
+        float* pp = (float*)t5.p[1][slot] + begin;
+        float* pm = (float*)t5.p[2][slot] + begin;
+        float* pv = (float*)t5.p[3][slot] + begin;
+        uint16_t* ps = (uint16_t*)t5.p[4][slot] + begin;
+#pragma unroll 2
+        for (int k = 0; k < kMultiQuads; ++k) {
+            const int at = c + k * kThreads * 4;
+            const int l = left - at > 4 ? 4 : (int)(left - at);
+            if (l <= 0) break;
+            float g[4], p[4], m[4], v[4];
+            load_quad4<T, true>(pg + at, l, g);
+            load_quad4<float, true>(pp + at, l, p);
+            load_quad4<float, true>(pm + at, l, m);
+            load_quad4<float, true>(pv + at, l, v);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float x = g[e] * coef;
+                m[e] = __builtin_fmaf(a.beta1, m[e], a.rest1 * x);
+                v[e] = __builtin_fmaf(a.beta2, v[e], a.rest2 * x * x);
+                const float root = __fsqrt_rn(v[e] * a.inv2) + a.eps;
+                p[e] = __builtin_fmaf(a.keep, p[e], -a.rate * __fdiv_rn(m[e], root));
+            }
+            store_quad4<float, true>(pp + at, l, p);
+            store_quad4<float, true>(pm + at, l, m);
+            store_quad4<float, true>(pv + at, l, v);
+            if (shards) store_quad4<uint16_t, true>(ps + at, l, p);
+        }
+    }
+}
+
+}  // namespace
+
+hipError_t launch_adamw(const AdamW& f, hipStream_t stream) {
+    const void* const* const lists[5] = {f.grads, (const void* const*)f.params, (const void* const*)f.exp_avg,
+                                         (const void* const*)f.exp_avg_sq, (const void* const*)f.shards};
+    AdamArgs a{};
+    a.coef = f.coef;
+    a.beta1 = (float)f.beta1; a.rest1 = (float)(1.0 - f.beta1);
+    a.beta2 = (float)f.beta2; a.rest2 = (float)(1.0 - f.beta2);
+    a.keep = (float)(1.0 - f.lr * f.weight_decay);
+    a.rate = (float)(f.lr / (1.0 - __builtin_pow(f.beta1, (double)f.step)));
+    a.inv2 = (float)(1.0 / (1.0 - __builtin_pow(f.beta2, (double)f.step)));
+    a.eps = (float)f.eps;
+    AdamTable m;
+    for (int next = multi_fill(&m, 0, f.n, lists, f.numels); m.count > 0; next = multi_fill(&m, next, f.n, lists, f.numels)) {
+        const int grid = grid_for(m.tile0[m.count], kThreads);
+        if (f.grad_dt == ZR_BF16)
+            adamw_kernel<uint16_t><<<grid, kThreads, 0, stream>>>(m, a, f.shards != nullptr);
+        else
+            adamw_kernel<float><<<grid, kThreads, 0, stream>>>(m, a, f.shards != nullptr);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+}  // namespace zr

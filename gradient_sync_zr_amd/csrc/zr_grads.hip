@@ -1,0 +1,177 @@
+// The global norm of many tensors, the coefficient that clips it, and tensors
+// multiplied by that coefficient.
+//     norm = scale * sqrt(sum g^2),  coef = scale * min(1, max_norm / norm)
+//
+// Squares are taken and summed in fp64: those of all finite fp32 values lie in
+// its normal range (2^-298 to 2^256), so nothing overflows or vanishes whatever
+// the gradients' size. Blocks walk over tiles and leave one partial sum each; a
+// single block adds them in order, so the result does not change from run to run.
+#include <hip/hip_runtime.h>
+
+#include "zr_multi.hpp"
+
+namespace zr {
+namespace {
+
+typedef Multi<1, kNormPer> NormTable;
+typedef Multi<2, kScalePer> ScaleTable;
+
+__device__ __forceinline__ double swap_add(double v, int lanes) { return v + __shfl_xor(v, lanes, 64); }
+
+// Sum of v over a block of T threads, in lane 0 of wave 0.
+template <int T>
+__device__ __forceinline__ double block_sum(double v, double* red) {
+#pragma unroll
+    for (int k = 1; k < 64; k *= 2) v = swap_add(v, k);
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x / 64] = v;
+    __syncthreads();
+    double s = 0.0;
+#pragma unroll
+    for (int w = 0; w < T / 64; ++w) s += red[w];
+    return s;
+}
+
+struct NormOut {
+    float *norm, *coef;
+    double scale, max_norm;
+};
+
+__device__ __forceinline__ void put_norm(const NormOut& o, double sum) {
+    const double norm = o.scale * sqrt(sum);
+    // a norm that is not finite leaves no coefficient
+    const bool finite = sum < __builtin_inf();
+    const double coef = finite ? (norm > o.max_norm ? o.scale * (o.max_norm / norm) : o.scale) : __builtin_nan("");
+    if (o.norm) *o.norm = (float)norm;
+    if (o.coef) *o.coef = (float)coef;
+}
+
+// The squares of this thread's share of the launch's tiles.
+template <typename T>
+__device__ __forceinline__ double squares(const NormTable& m, int first, int step) {
+    double s[4] = {0.0, 0.0, 0.0, 0.0};
+    int slot = 0;
+    const int tiles = m.tile0[m.count];
+    for (int t = first; t < tiles; t += step) {
+        slot = multi_slot(m, slot, t);
+        const T* p = (const T*)m.p[0][slot];
+        const int64_t begin = (int64_t)(t - m.tile0[slot]) * kMultiTile, left = m.n[slot] - begin;
+        const int c = threadIdx.x % kThreads * 4;
+        p += begin + c;
+        float f[kMultiQuads][4];
+#pragma unroll
+        for (int k = 0; k < kMultiQuads; ++k) {
+            const int64_t l = left - c - k * kThreads * 4;
+            load_quad4<T, false>(p + k * kThreads * 4, l > 4 ? 4 : (int)l, f[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < kMultiQuads; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[e] = __builtin_fma((double)f[k][e], (double)f[k][e], s[e]);
+    }
+    return (s[0] + s[1]) + (s[2] + s[3]);
+}
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void norm_kernel(NormTable m, double* part) {
+    __shared__ double red[kThreads / 64];
+    const double s = block_sum<kThreads>(squares<T>(m, blockIdx.x, gridDim.x), red);
+    if (threadIdx.x == 0) part[blockIdx.x] = s;
+}
+
+// Everything in one block, where there is little.
+template <typename T>
+__global__ __launch_bounds__(1024) void norm_one_kernel(NormTable m, NormOut o) {
+    __shared__ double red[16];
+    const double s = block_sum<1024>(squares<T>(m, threadIdx.x / kThreads, 1024 / kThreads), red);
+    if (threadIdx.x == 0) put_norm(o, s);
+}
+
+__global__ __launch_bounds__(1024) void norm_join_kernel(const double* part, int count, NormOut o) {
+    __shared__ double red[16];
+    double s = 0.0;
+    for (int i = threadIdx.x; i < count; i += 1024) s += part[i];
+    s = block_sum<1024>(s, red);
+    if (threadIdx.x == 0) put_norm(o, s);
+}
+
+// In place a coefficient of 1 leaves nothing to do.
+template <typename T, typename U>
+__global__ __launch_bounds__(kThreads) void scale_kernel(ScaleTable m, const float* coef, int in_place) {
+    const float k1 = *coef;
+    if (in_place && k1 == 1.0f) return;
+    int slot = 0;
+    const int tiles = m.tile0[m.count];
+    for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+        slot = multi_slot(m, slot, t);
+        const int64_t begin = (int64_t)(t - m.tile0[slot]) * kMultiTile, left = m.n[slot] - begin;
+        const int c = threadIdx.x * 4;
+        const T* p = (const T*)m.p[0][slot] + begin + c;
+        U* q = (U*)m.p[1][slot] + begin + c;
+        float f[kMultiQuads][4];
+#pragma unroll
+        for (int k = 0; k < kMultiQuads; ++k) {
+            const int64_t l = left - c - k * kThreads * 4;
+            load_quad4<T, true>(p + k * kThreads * 4, l > 4 ? 4 : (int)l, f[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < kMultiQuads; ++k) {
+            const int64_t l = left - c - k * kThreads * 4;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[k][e] *= k1;
+            store_quad4<U, true>(q + k * kThreads * 4, l > 4 ? 4 : (int)l, f[k]);
+        }
+    }
+}
+
+}  // namespace
+
+hipError_t launch_grad_norm(const GradNorm& f, hipStream_t stream) {
+    const void* const* const lists[1] = {f.grads};
+    const NormOut o{f.norm, f.coef, (double)f.scale, (double)f.max_norm};
+    double* const part = (double*)f.workspace;
+    NormTable m;
+    int next = multi_fill(&m, 0, f.n, lists, f.numels), parts = 0;
+    if (next == f.n && m.tile0[m.count] <= kNormOneTiles) {
+        if (f.dt == ZR_BF16)
+            norm_one_kernel<uint16_t><<<1, 1024, 0, stream>>>(m, o);
+        else
+            norm_one_kernel<float><<<1, 1024, 0, stream>>>(m, o);
+        return hipGetLastError();
+    }
+    while (m.count > 0) {
+        const int64_t tiles = m.tile0[m.count];
+        const int grid = grid_for(tiles < kNormBlocks ? tiles : kNormBlocks, kThreads);
+        if (f.dt == ZR_BF16)
+            norm_kernel<uint16_t><<<grid, kThreads, 0, stream>>>(m, part + parts);
+        else
+            norm_kernel<float><<<grid, kThreads, 0, stream>>>(m, part + parts);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        parts += grid;
+        next = multi_fill(&m, next, f.n, lists, f.numels);
+    }
+    norm_join_kernel<<<1, 1024, 0, stream>>>(part, parts, o);
+    return hipGetLastError();
+}
+
+hipError_t launch_grad_scale(const GradScale& f, hipStream_t stream) {
+    const bool in_place = !f.outs;
+    const void* const* const lists[2] = {f.grads, in_place ? f.grads : (const void* const*)f.outs};
+    ScaleTable m;
+    for (int next = multi_fill(&m, 0, f.n, lists, f.numels); m.count > 0; next = multi_fill(&m, next, f.n, lists, f.numels)) {
+        const int grid = grid_for(m.tile0[m.count], kThreads);
+        if (f.dt == ZR_BF16 && f.out_dt == ZR_BF16)
+            scale_kernel<uint16_t, uint16_t><<<grid, kThreads, 0, stream>>>(m, f.coef, in_place);
+        else if (f.dt == ZR_BF16)
+            scale_kernel<uint16_t, float><<<grid, kThreads, 0, stream>>>(m, f.coef, in_place);
+        else if (f.out_dt == ZR_BF16)
+            scale_kernel<float, uint16_t><<<grid, kThreads, 0, stream>>>(m, f.coef, in_place);
+        else
+            scale_kernel<float, float><<<grid, kThreads, 0, stream>>>(m, f.coef, in_place);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+}  // namespace zr

@@ -319,4 +319,44 @@ inline int64_t wgrad_workspace(int64_t rows, int64_t out, int64_t in) {
 }
 ZR_KERNELS hipError_t launch_ckpt_wgrad(const Wgrad& w, hipStream_t stream);
 
+// Norm, scaling and AdamW over many tensors: a launch carries so many in its
+// arguments (4 KiB at most), and a longer list goes out as several.
+constexpr int kNormPer = 128, kScalePer = 128, kAdamPer = 64;
+constexpr int kNormBlocks = 2048;  // partial sums of a launch at most
+constexpr int kNormOneTiles = 4;   // tiles that one block takes alone, without a join
+
+struct GradNorm {
+    int n;
+    const void* const* grads;
+    const int64_t* numels;
+    zr_dtype dt;
+    double scale, max_norm;
+    float *norm, *coef;
+    void* workspace;  // of grad_norm_parts() doubles
+};
+ZR_KERNELS hipError_t launch_grad_norm(const GradNorm& f, hipStream_t stream);
+inline int64_t grad_norm_parts(int n) { return (int64_t)((n + kNormPer - 1) / kNormPer) * kNormBlocks; }
+
+struct GradScale {
+    int n;
+    const void* const* grads;
+    const int64_t* numels;
+    zr_dtype dt, out_dt;
+    void* const* outs;  // null: in place
+    const float* coef;
+};
+ZR_KERNELS hipError_t launch_grad_scale(const GradScale& f, hipStream_t stream);
+
+struct AdamW {
+    int n;
+    const void* const* grads;
+    const int64_t* numels;
+    zr_dtype grad_dt;
+    void *const *params, *const *exp_avg, *const *exp_avg_sq, *const *shards;  // shards may be null
+    double lr, beta1, beta2, eps, weight_decay;
+    int64_t step;
+    const float* coef;
+};
+ZR_KERNELS hipError_t launch_adamw(const AdamW& f, hipStream_t stream);
+
 }  // namespace zr

@@ -674,6 +674,74 @@ zr_status zr_ckpt_wgrad(const void* dy, zr_dtype dy_dt, int64_t ld_dy, const voi
                         int64_t ld_dw, void* dbias, int flags, void* workspace, size_t ws_bytes,
                         void* stream);
 
+/* ------------------------------------- gradient norm, clipping and AdamW
+ * What stands between the reduce-scatter and the all-gather, over any number of
+ * tensors at once: the ranks' partitions, or a model's gradients one by one.
+ *
+ *  grads, outs, ...   HOST arrays of n device pointers, element-aligned; a
+ *             tensor without elements may have a NULL one. The tables are read
+ *             before the call returns
+ *  numels     HOST array of n sizes, each >= 0, at most 2^40 in all
+ *  norm, coef one fp32 each, on the device: nothing waits for the host
+ * Buffers that are written share no byte with any other of the call
+ * (ZR_ERR_ALIAS); the same gradient may be listed twice where it is only read.
+ * The calls enqueue kernels only, so they can be captured, and results do not
+ * change from run to run (no atomics). One launch takes 128 tensors (AdamW: 64);
+ * longer lists go out as several. */
+
+/* Bytes of workspace of zr_grad_norm; 0 for n <= 0. Host only. */
+size_t zr_grad_norm_workspace_bytes(int n);
+
+/*
+ * Norm of all tensors together, and the coefficient that clips them to max_norm:
+ *     norm = scale * sqrt(sum g^2),  coef = scale * min(1, max_norm / norm)
+ * with squares and sums in fp64 (no gradient's square overflows or vanishes),
+ * each rounded once to fp32. The gradients stand for scale * grads: 1 / the loss
+ * scale, or 1 / the number of micro-steps that were added up.
+ *
+ *  dt         ZR_BF16 or ZR_FP32
+ *  scale      > 0, finite
+ *  max_norm   > 0, or infinity (no clipping)
+ *  norm, coef one of the two may be NULL. Where the gradients hold a NaN or an
+ *             infinity, norm is not finite and coef is NaN. Without elements norm
+ *             is 0 and coef scale
+ *  workspace  8-byte aligned, zr_grad_norm_workspace_bytes(n) bytes
+ *             (ZR_ERR_WORKSPACE). Calls on one stream may share it; calls, or
+ *             captured graphs, that may run at the same time must not
+ */
+zr_status zr_grad_norm(int n, const void* const* grads, const int64_t* numels, zr_dtype dt, double scale,
+                       double max_norm, float* norm, float* coef, void* workspace, size_t ws_bytes,
+                       void* stream);
+
+/*
+ * out = coef * grad in fp32, rounded once to out_dt. outs NULL: in place (out_dt
+ * is dt), where a coefficient of 1 leaves the gradients untouched. outs[i] may
+ * be grads[i] where dt is out_dt; otherwise outputs overlap nothing.
+ */
+zr_status zr_grad_scale(int n, const void* const* grads, const int64_t* numels, zr_dtype dt, void* const* outs,
+                        zr_dtype out_dt, const float* coef, void* stream);
+
+/*
+ * AdamW. With g = coef * grad, for every element in fp32:
+ *     m = beta1 * m + (1 - beta1) * g,  v = beta2 * v + (1 - beta2) * g^2
+ *     p = (1 - lr * weight_decay) * p
+ *         - lr / (1 - beta1^step) * m / (sqrt(v / (1 - beta2^step)) + eps)
+ *
+ *  grads      grad_dt ZR_BF16 or ZR_FP32
+ *  params, exp_avg, exp_avg_sq   p, m and v, fp32, read and written
+ *  shards     NULL, or bf16 outputs that receive p rounded: what
+ *             zr_all_gather takes
+ *  lr, eps, weight_decay   >= 0, finite; beta1, beta2 in [0, 1)
+ *  step       >= 1, of this update. It and the rates are in the launch's
+ *             arguments: a captured graph repeats them
+ *  coef       one fp32 on the device (of zr_grad_norm), or NULL (1). Where it is
+ *             not finite the step is left out: nothing is written
+ */
+zr_status zr_adamw(int n, const void* const* grads, zr_dtype grad_dt, const int64_t* numels, void* const* params,
+                   void* const* exp_avg, void* const* exp_avg_sq, void* const* shards, double lr, double beta1,
+                   double beta2, double eps, double weight_decay, int64_t step, const float* coef,
+                   void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,179 @@
+"""Refusals of the gradient norm, scaling and AdamW calls, without a GPU: every
+bad argument is reported before any HIP call (fake addresses, nothing launched)."""
+import ctypes
+import json
+import subprocess
+import sys
+
+import pytest
+
+import gradient_sync_zr_amd as zr
+from conftest import ROOT
+from launches import LOG, launches
+from test_abi_cpu import A, expect
+
+BF, FP = zr.ZR_BF16, zr.ZR_FP32
+FAR = 1 << 36
+B, C, D, E, F, G = (A + i * FAR for i in range(1, 7))
+GAP = 1 << 24
+
+
+def at(base, n=3):
+    return [base + i * GAP for i in range(n)]
+
+
+def norm(grads=None, numels=(10, 0, 1000), norm=B, coef=B + 4, ws=(C, 1 << 20), dt=FP, **kw):
+    zr.zr_grad_norm(at(A) if grads is None else grads, numels, norm, coef, workspace=ws, dtype=dt, stream=0, **kw)
+
+
+def test_norm_refusals():
+    for bad in (0.0, -1.0, float("nan"), float("inf"), 1e39):
+        expect(zr.ZR_ERR_INVALID, norm, scale=bad)
+    for bad in (0.0, -1.0, float("nan")):
+        expect(zr.ZR_ERR_INVALID, norm, max_norm=bad)
+    expect(zr.ZR_ERR_INVALID, norm, norm=None, coef=None)
+    expect(zr.ZR_ERR_INVALID, norm, numels=(10, -1, 4))
+    expect(zr.ZR_ERR_INVALID, norm, numels=(10, 1 << 40, 4))
+    expect(zr.ZR_ERR_INVALID, norm, grads=[A, B, 0])
+    expect(zr.ZR_ERR_UNSUPPORTED, norm, dt=zr.ZR_CKPT_E4M3)
+    expect(zr.ZR_ERR_ALIGN, norm, grads=[A, B, A + FAR // 2 + 2])
+    expect(zr.ZR_ERR_ALIGN, norm, norm=B + 2)
+    expect(zr.ZR_ERR_ALIGN, norm, ws=(C + 4, 1 << 20))
+    need = zr.zr_grad_norm_workspace_bytes(3)
+    assert need > 0 and zr.zr_grad_norm_workspace_bytes(0) == 0 and zr.zr_grad_norm_workspace_bytes(-3) == 0
+    assert zr.zr_grad_norm_workspace_bytes(129) == 2 * need
+    expect(zr.ZR_ERR_WORKSPACE, norm, ws=None)
+    expect(zr.ZR_ERR_WORKSPACE, norm, ws=(C, need - 1))
+    expect(zr.ZR_ERR_ALIAS, norm, coef=B)
+    expect(zr.ZR_ERR_ALIAS, norm, norm=A + 36)
+    expect(zr.ZR_ERR_ALIAS, norm, ws=(A + 2 * GAP + 3992, need))
+    expect(zr.ZR_ERR_ALIAS, norm, ws=(B - need + 8, need))
+    with pytest.raises(ValueError, match="entries"):
+        norm(numels=(10, 20))
+    with pytest.raises(ValueError, match="dtype is needed"):
+        norm(dt=None)
+    lib = zr.lib()
+    n = (ctypes.c_int64 * 1)(5)
+    assert lib.zr_grad_norm(-1, None, None, FP, 1.0, 1.0, B, None, C, 1 << 20, None) == zr.ZR_ERR_INVALID
+    assert lib.zr_grad_norm(1, None, n, FP, 1.0, 1.0, B, None, C, 1 << 20, None) == zr.ZR_ERR_INVALID
+    assert lib.zr_grad_norm(1, zr.table([A]), None, FP, 1.0, 1.0, B, None, C, 1 << 20, None) == zr.ZR_ERR_INVALID
+
+
+def scale(grads=None, numels=(10, 0, 1000), coef=B, outs=None, dt=FP, odt=None):
+    zr.zr_grad_scale(at(A) if grads is None else grads, numels, coef, outs, dtype=dt, out_dtype=odt, stream=0)
+
+
+def test_scale_refusals():
+    expect(zr.ZR_ERR_INVALID, scale, coef=None)
+    expect(zr.ZR_ERR_ALIGN, scale, coef=B + 1)
+    expect(zr.ZR_ERR_ALIAS, scale, coef=A + 4)                          # inside a gradient that is written
+    expect(zr.ZR_ERR_ALIAS, scale, grads=[A, B, A + 36])                # in place, two that overlap
+    expect(zr.ZR_ERR_ALIAS, scale, grads=[A, C, A], numels=(8, 0, 8))   # the same twice, written
+    expect(zr.ZR_ERR_ALIAS, scale, outs=[A + 4, D, E], odt=FP)          # shifted in place
+    expect(zr.ZR_ERR_ALIAS, scale, outs=at(A), odt=BF)                  # in place, other type
+    expect(zr.ZR_ERR_ALIAS, scale, outs=[A + 2 * GAP, D, A], odt=FP)    # another's place
+    expect(zr.ZR_ERR_ALIAS, scale, outs=[D, E, D + 36], odt=FP)
+    expect(zr.ZR_ERR_ALIAS, scale, outs=[D, E, B - 8], odt=FP)          # an output over coef
+    expect(zr.ZR_ERR_INVALID, scale, outs=[D, E, 0], odt=FP)
+    expect(zr.ZR_ERR_ALIGN, scale, outs=[D, E, F + 1], odt=BF)
+    expect(zr.ZR_ERR_UNSUPPORTED, scale, outs=[D, E, F], odt=zr.ZR_CKPT_INT8)
+    lib = zr.lib()
+    n = (ctypes.c_int64 * 1)(5)
+    assert lib.zr_grad_scale(1, zr.table([A]), n, FP, None, BF, B, None) == zr.ZR_ERR_UNSUPPORTED
+
+
+def adamw(grads=None, numels=(10, 0, 1000), p=None, m=None, v=None, shards=None, step=1, coef=G, dt=BF, lr=1e-3, **kw):
+    zr.zr_adamw(at(A) if grads is None else grads, numels, p or at(B), m or at(C), v or at(D), step, lr, shards=shards,
+                coef=coef, dtype=dt, stream=0, **kw)
+
+
+def test_adamw_refusals():
+    for k in ("beta1", "beta2"):
+        for bad in (-0.1, 1.0, float("nan")):
+            expect(zr.ZR_ERR_INVALID, adamw, **{k: bad})
+    for k in ("lr", "eps", "weight_decay"):
+        for bad in (-1e-3, float("inf"), float("nan")):
+            expect(zr.ZR_ERR_INVALID, adamw, **{k: bad})
+    for step in (0, -5):
+        expect(zr.ZR_ERR_INVALID, adamw, step=step)
+    expect(zr.ZR_ERR_UNSUPPORTED, adamw, dt=9)
+    for k in ("p", "m", "v"):
+        expect(zr.ZR_ERR_INVALID, adamw, **{k: [E, F, 0]})
+        expect(zr.ZR_ERR_ALIGN, adamw, **{k: [E, F, F + 2]})
+        expect(zr.ZR_ERR_ALIAS, adamw, **{k: [E, F, A + 2 * GAP]})
+        expect(zr.ZR_ERR_ALIAS, adamw, **{k: [E, F, E + 36]})
+    expect(zr.ZR_ERR_ALIAS, adamw, m=at(B))
+    expect(zr.ZR_ERR_ALIAS, adamw, shards=at(B))
+    expect(zr.ZR_ERR_ALIAS, adamw, shards=at(A))
+    expect(zr.ZR_ERR_ALIAS, adamw, coef=B + 4)
+    expect(zr.ZR_ERR_ALIGN, adamw, shards=[E, F, F + 1])
+    with pytest.raises(ValueError, match="entries"):
+        adamw(shards=[E])
+    lib = zr.lib()
+    n = (ctypes.c_int64 * 1)(5)
+    t = zr.table([A])
+    assert lib.zr_adamw(1, t, BF, n, None, t, t, None, 1e-3, .9, .9, 1e-8, 0, 1, None, None) == zr.ZR_ERR_INVALID
+
+
+def test_tensors_are_checked():
+    import torch
+    x = [torch.zeros(10), torch.zeros(4)]
+    with pytest.raises(ValueError, match="not on the GPU"):
+        zr.zr_grad_norm(x, [10, 4], B, workspace=(C, 1 << 20), stream=0)
+    with pytest.raises(ValueError, match="not on the GPU"):
+        zr.tensor_table(x, [10, 4])
+    with pytest.raises(TypeError, match="unsupported dtype"):
+        zr.zr_grad_norm([torch.zeros(3, dtype=torch.float64)], [3], B, workspace=(C, 1 << 20), stream=0)
+    t = zr.tensor_table(at(A), [5, 6, 7], dtype=FP)
+    with pytest.raises(ValueError, match="other sizes"):
+        zr.zr_grad_norm(t, [5, 6, 8], B, workspace=(C, 1 << 20), stream=0)
+    with pytest.raises(ValueError, match="dtype argument"):
+        zr.zr_grad_norm(t, [5, 6, 7], B, workspace=(C, 1 << 20), dtype=BF, stream=0)
+
+
+def test_launches():
+    """One block up to four tiles; a block per tile and a join beyond; a launch per 128 (64) tensors."""
+    launches([])  # builds the library that writes launches down
+    code = """
+import ctypes, json, sys
+sys.path.insert(0, sys.argv[1])
+log = ctypes.CDLL(sys.argv[2], mode=ctypes.RTLD_GLOBAL)
+log.ll_launch.restype = ctypes.c_char_p
+import gradient_sync_zr_amd as zr
+A = 1 << 46
+out = []
+for what, n, numel in json.loads(sys.argv[3]):
+    log.ll_clear()
+    t = [A + i * (1 << 35) for i in range(n)]
+    far = lambda k: [x + (k << 43) for x in t]
+    if what == "norm":
+        zr.zr_grad_norm(t, [numel] * n, 4096, 8192, workspace=(1 << 20, 1 << 30), dtype=1, stream=0)
+    elif what == "scale":
+        zr.zr_grad_scale(t, [numel] * n, 4096, dtype=1, stream=0)
+    else:
+        zr.zr_adamw(t, [numel] * n, far(1), far(2), far(3), 1, 1e-3, shards=far(4), coef=4096, dtype=1, stream=0)
+    got = []
+    for i in range(log.ll_count()):
+        d = (ctypes.c_uint32 * 6)()
+        got.append([log.ll_launch(i, d).decode(), d[0], d[3]])
+    out.append(got)
+print(json.dumps(out))
+"""
+    asked = [["norm", 0, 0], ["norm", 5, 0], ["norm", 1, 16384], ["norm", 4, 4000], ["norm", 5, 4000], ["norm", 1, 1 << 34],
+             ["norm", 129, 5000], ["scale", 1, 4097], ["scale", 128, 10], ["scale", 129, 10], ["scale", 3, 0],
+             ["adamw", 64, 4096], ["adamw", 130, 4097], ["adamw", 1, 1 << 34]]
+    r = subprocess.run([sys.executable, "-c", code, ROOT, LOG, json.dumps(asked)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+    got = json.loads(r.stdout)
+    name = lambda s: next(k for k in ("norm_one", "norm_join", "norm_kernel", "scale_kernel", "adamw_kernel") if k in s)  # noqa: E731
+    got = [[(name(s), b, t) for s, b, t in g] for g in got]
+    one, join = ("norm_one", 1, 1024), ("norm_join", 1, 1024)
+    assert got[:4] == [[one]] * 4
+    assert got[4] == [("norm_kernel", 5, 256), join]
+    assert got[5] == [("norm_kernel", 2048, 256), join]
+    assert got[6] == [("norm_kernel", 256, 256), ("norm_kernel", 2, 256), join]
+    assert got[7] == [("scale_kernel", 2, 256)] and got[8] == [("scale_kernel", 128, 256)]
+    assert got[9] == [("scale_kernel", 128, 256), ("scale_kernel", 1, 256)] and got[10] == []
+    assert got[11] == [("adamw_kernel", 64, 256)]
+    assert got[12] == [("adamw_kernel", 128, 256)] * 2 + [("adamw_kernel", 4, 256)]
+    assert len(got[13]) == 1 and all(b * t < 1 << 32 for g in got for _, b, t in g)
