@@ -61,7 +61,7 @@ LIB_PATH = os.environ.get("ZR_LIBRARY") or os.path.join(_HERE, "libzr.so")
 (ZR_OK, ZR_ERR_INVALID, ZR_ERR_ALIGN, ZR_ERR_ALIAS, ZR_ERR_UNSUPPORTED, ZR_ERR_WORKSPACE, ZR_ERR_HIP,
  ZR_ERR_NOMEM) = range(8)
 ZR_BF16, ZR_FP32 = 0, 1
-ZR_CKPT_E4M3, ZR_CKPT_INT8 = 2, 3
+ZR_CKPT_E4M3, ZR_CKPT_INT8, ZR_CKPT_E2M1 = 2, 3, 4
 ZR_ORDER_RING, ZR_ORDER_FREE, ZR_ORDER_RING_WIRE = 0, 1, 2
 ZR_AVERAGE, ZR_ACCUMULATE, ZR_ADD_DX = 1, 2, 4
 ZR_MAX_RANKS, ZR_MAX_ELEMS = 64, 1 << 40
@@ -81,12 +81,14 @@ PF_EXPORTS = ("zr_pf_create", "zr_pf_fetch", "zr_pf_release", "zr_pf_full", "zr_
               "zr_pf_destroy", "zr_pf_plan")
 NORM_EXPORTS = ("zr_ckpt_pack", "zr_ckpt_unpack", "zr_layernorm_fwd", "zr_layernorm_bwd", "zr_ckpt_wgrad",
                 "zr_ckpt_bytes", "zr_layernorm_workspace_bytes", "zr_ckpt_wgrad_workspace_bytes")
+RMS_EXPORTS = ("zr_rmsnorm_fwd", "zr_rmsnorm_bwd", "zr_ckpt_pack_t", "zr_ckpt_linear", "zr_ckpt_format_bytes",
+               "zr_rmsnorm_workspace_bytes", "zr_ckpt_linear_workspace_bytes")
 GRAD_EXPORTS = ("zr_grad_norm", "zr_grad_scale", "zr_adamw", "zr_grad_norm_workspace_bytes")
 EXPORTS = ("zr_last_error", "zr_version", "zr_workspace_bytes", "zr_flatten_bucket", "zr_reduce_scatter_avg",
            "zr_reduce_scatter_frags", "zr_all_gather", "zr_allreduce", "zr_plan_buckets", "zr_sched_create",
            "zr_sched_acquire", "zr_sched_submit_rs", "zr_sched_flush",
            "zr_sched_destroy", "zr_reduce_scatter_frags_noalloc") + COST_EXPORTS + PF_EXPORTS + \
-    RSF_PLAN_EXPORTS + FLAT_PLAN_EXPORTS + RS_PLAN_EXPORTS + NORM_EXPORTS + GRAD_EXPORTS
+    RSF_PLAN_EXPORTS + FLAT_PLAN_EXPORTS + RS_PLAN_EXPORTS + NORM_EXPORTS + RMS_EXPORTS + GRAD_EXPORTS
 
 
 class ZrError(RuntimeError):
@@ -196,6 +198,18 @@ def lib() -> ctypes.CDLL:
         for f in NORM_EXPORTS[5:]:
             getattr(L, f).restype = _sz
         _d = ctypes.c_double
+        L.zr_rmsnorm_fwd.argtypes = [_vp, _i32, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i32, _vp, _i32, _f, _vp,
+                                     _i32, _i64, _vp, _vp, _vp, _i32, _vp]
+        L.zr_rmsnorm_bwd.argtypes = [_vp, _i32, _i64, _vp, _i32, _i64, _i64, _i64, _vp, _i32, _vp, _vp, _i32, _i64,
+                                     _vp, _i32, _i32, _vp, _sz, _vp]
+        L.zr_ckpt_pack_t.argtypes = [_vp, _i32, _i64, _i64, _i64, _vp, _i32, _vp]
+        L.zr_ckpt_linear.argtypes = [_vp, _i32, _vp, _i32, _i64, _i64, _i64, _vp, _i32, _vp, _i32, _i64, _i32, _vp,
+                                     _sz, _vp]
+        L.zr_ckpt_format_bytes.argtypes = [_i64, _i64, _i32]
+        L.zr_rmsnorm_workspace_bytes.argtypes = [_i64, _i64]
+        L.zr_ckpt_linear_workspace_bytes.argtypes = [_i64, _i64, _i64]
+        for f in RMS_EXPORTS[4:]:
+            getattr(L, f).restype = _sz
         _I64s = ctypes.POINTER(_i64)
         L.zr_grad_norm.argtypes = [_i32, _PP, _I64s, _i32, _d, _d, _vp, _vp, _vp, _sz, _vp]
         L.zr_grad_scale.argtypes = [_i32, _PP, _I64s, _i32, _PP, _i32, _vp, _vp]
@@ -781,13 +795,17 @@ def _one_dtype(a, b, names) -> int:
     return a[1]
 
 
-def _ckpt(x, rows: int, cols: int, name: str) -> int:
+def _ckpt(x, rows: int, cols: int, name: str, format: int = ZR_CKPT_E4M3) -> int:
     """Address of a checkpoint: a contiguous tensor of one-byte elements, of
-    zr_ckpt_bytes(rows, cols) of them at least, or an address."""
+    zr_ckpt_bytes(rows, cols) of them at least (zr_ckpt_format_bytes for 4-bit
+    blocks), or an address."""
     if x is None or x.__class__ is int:
         return x or 0
-    if x.element_size() != 1 or not x.is_contiguous() or x.numel() < zr_ckpt_bytes(rows, cols):
-        raise ValueError(f"{name} is not a contiguous buffer of zr_ckpt_bytes({rows}, {cols}) bytes")
+    small = format == ZR_CKPT_E2M1
+    if x.element_size() != 1 or not x.is_contiguous() or \
+            x.numel() < (zr_ckpt_format_bytes(rows, cols, format) if small else zr_ckpt_bytes(rows, cols)):
+        raise ValueError(f"{name} is not a contiguous buffer of "
+                         f"{'zr_ckpt_format_bytes' if small else 'zr_ckpt_bytes'}({rows}, {cols}) bytes")
     return x.data_ptr()
 
 
@@ -845,9 +863,10 @@ def zr_ckpt_wgrad_workspace_bytes(rows: int, out_cols: int, in_cols: int) -> int
 
 def zr_ckpt_pack(x, rows: int, cols: int, ckpt, format: int = ZR_CKPT_E4M3, dtype=None, ld=None,
                  stream=None) -> None:
-    """x (rows x cols, bf16 or fp32) into the checkpoint buffer `ckpt`."""
+    """x (rows x cols, bf16 or fp32) into the checkpoint buffer `ckpt` (format
+    ZR_CKPT_E2M1: 4-bit blocks, of zr_ckpt_format_bytes)."""
     px, dt, ldx = _matrix(x, rows, cols, dtype, ld, "x")
-    _check(lib().zr_ckpt_pack(px, dt, rows, cols, ldx, _ckpt(ckpt, rows, cols, "ckpt"), format,
+    _check(lib().zr_ckpt_pack(px, dt, rows, cols, ldx, _ckpt(ckpt, rows, cols, "ckpt", format), format,
                               _run_on(stream, x, ckpt)))
 
 
@@ -855,7 +874,7 @@ def zr_ckpt_unpack(ckpt, rows: int, cols: int, x, format: int = ZR_CKPT_E4M3, dt
                    stream=None) -> None:
     """The values of a checkpoint into x (rows x cols, bf16 or fp32)."""
     px, dt, ldx = _matrix(x, rows, cols, dtype, ld, "x")
-    _check(lib().zr_ckpt_unpack(_ckpt(ckpt, rows, cols, "ckpt"), format, rows, cols, px, dt, ldx,
+    _check(lib().zr_ckpt_unpack(_ckpt(ckpt, rows, cols, "ckpt", format), format, rows, cols, px, dt, ldx,
                                 _run_on(stream, x, ckpt)))
 
 
@@ -928,6 +947,97 @@ def zr_ckpt_wgrad(dy, ckpt, rows: int, out_cols: int, in_cols: int, dw, dbias=No
                                pdw, _one_dtype((pdw, gd), gb, ("dw", "dbias")), lddw, gb[0],
                                ZR_ACCUMULATE if accumulate else 0, ws, wsb,
                                _run_on(stream, dy, ckpt, dw, dbias, workspace)))
+
+
+
+# ------------------------------------- RMS norm and packed linear layers
+def zr_ckpt_format_bytes(rows: int, cols: int, format: int) -> int:
+    return lib().zr_ckpt_format_bytes(rows, cols, format)
+
+
+def zr_rmsnorm_workspace_bytes(rows: int, cols: int) -> int:
+    return lib().zr_rmsnorm_workspace_bytes(rows, cols)
+
+
+def zr_ckpt_linear_workspace_bytes(rows: int, in_cols: int, out_cols: int) -> int:
+    return lib().zr_ckpt_linear_workspace_bytes(rows, in_cols, out_cols)
+
+
+def zr_rmsnorm_fwd(x, rows: int, cols: int, y=None, weight=None, eps: float = 1e-5, residual=None, h=None, rstd=None,
+                   ckpt_h=None, ckpt_y=None, ckpt_format: int = ZR_CKPT_E4M3, x_dtype=None, y_dtype=None, h_dtype=None,
+                   param_dtype=None, ld_x=None, ld_y=None, ld_residual=None, ld_h=None, stream=None) -> None:
+    """RMS norm of h = x + residual (of x without one) into y; h receives the sum,
+    rstd (fp32) the statistics, ckpt_h and ckpt_y the 8-bit checkpoints of h and y.
+    h_dtype: of h and the residual, and what their sum is rounded to; y_dtype: of
+    y, and with y None, what ckpt_y's values are rounded to (default bf16). With
+    x_dtype a checkpoint format, x is a checkpoint. Buffers given as addresses
+    need their dtype argument (weight: param_dtype)."""
+    px, xd, ldx = _source(x, rows, cols, x_dtype, ld_x)
+    if y is None:
+        py, yd, ldy = 0, ZR_BF16 if y_dtype is None else _dtype(y_dtype), cols
+    else:
+        py, yd, ldy = _matrix(y, rows, cols, y_dtype, ld_y, "y")
+    pr = ph = 0
+    hd, ldr, ldh = ZR_BF16, cols, cols
+    if residual is not None:
+        pr, hd, ldr = _matrix(residual, rows, cols, h_dtype, ld_residual, "residual")
+    if h is not None:
+        ph, code, ldh = _matrix(h, rows, cols, h_dtype, ld_h, "h")
+        if residual is not None and code != hd:
+            raise ValueError("residual and h are of different dtypes")
+        hd = code
+    w = _vector(weight, cols, param_dtype, "weight")
+    st = lib().zr_rmsnorm_fwd(px, xd, rows, cols, ldx, pr, ldr, ph, ldh, hd, w[0],
+                              w[1] if w[1] is not None else _one_dtype(w, (0, None), ("weight",)), eps, py, yd, ldy,
+                              _vector(rstd, rows, ZR_FP32, "rstd")[0],
+                              0 if ckpt_h is None else _ckpt(ckpt_h, rows, cols, "ckpt_h"),
+                              0 if ckpt_y is None else _ckpt(ckpt_y, rows, cols, "ckpt_y"), ckpt_format,
+                              _run_on(stream, x, residual, h, y, weight, rstd, ckpt_h, ckpt_y))
+    if st:
+        _check(st)
+
+
+def zr_rmsnorm_bwd(dy, h, rows: int, cols: int, rstd, weight=None, dx=None, dweight=None, accumulate: bool = False,
+                   add_dx: bool = False, workspace=None, dy_dtype=None, h_dtype=None, dx_dtype=None, param_dtype=None,
+                   grad_dtype=None, ld_dy=None, ld_h=None, ld_dx=None, stream=None) -> None:
+    """Gradients of zr_rmsnorm_fwd: of h, which are x's and the residual's (dx,
+    added to with add_dx), and of its weight (dweight, added to with accumulate,
+    with a workspace of zr_rmsnorm_workspace_bytes). h: the normed rows, or their
+    checkpoint (h_dtype its format). Buffers given as addresses need their dtype
+    argument (weight: param_dtype, dweight: grad_dtype)."""
+    pdy, dyd, lddy = _matrix(dy, rows, cols, dy_dtype, ld_dy, "dy")
+    ph, hd, ldh = _source(h, rows, cols, h_dtype, ld_h)
+    pdx, dxd, lddx = _matrix(dx, rows, cols, dx_dtype, ld_dx, "dx")
+    w, gw = _vector(weight, cols, param_dtype, "weight"), _vector(dweight, cols, grad_dtype, "dweight")
+    ws, wsb = _workspace(workspace)
+    _check(lib().zr_rmsnorm_bwd(pdy, dyd, lddy, ph, hd, ldh, rows, cols, w[0], _one_dtype(w, (0, None), ("weight",)),
+                                _vector(rstd, rows, ZR_FP32, "rstd")[0], pdx, dxd, lddx, gw[0],
+                                _one_dtype(gw, (0, None), ("dweight",)),
+                                (ZR_ACCUMULATE if accumulate else 0) | (ZR_ADD_DX if add_dx else 0), ws, wsb,
+                                _run_on(stream, dy, h, rstd, weight, dx, dweight, workspace)))
+
+
+def zr_ckpt_pack_t(x, rows: int, cols: int, ckpt, format: int = ZR_CKPT_E4M3, dtype=None, ld=None, stream=None) -> None:
+    """The transpose of x (rows x cols, bf16 or fp32), packed: `ckpt` holds cols x
+    rows (zr_ckpt_format_bytes(cols, rows, format))."""
+    px, dt, ldx = _matrix(x, rows, cols, dtype, ld, "x")
+    _check(lib().zr_ckpt_pack_t(px, dt, rows, cols, ldx, _ckpt(ckpt, cols, rows, "ckpt", format), format,
+                                _run_on(stream, x, ckpt)))
+
+
+def zr_ckpt_linear(x, w, rows: int, in_cols: int, out_cols: int, z, bias=None, x_format: int = ZR_CKPT_E4M3,
+                   w_format: int = ZR_CKPT_E4M3, accumulate: bool = False, workspace=None, z_dtype=None, bias_dtype=None,
+                   ld_z=None, stream=None) -> None:
+    """z = x w^T + bias of packed x (rows x in_cols) and w (out_cols x in_cols),
+    e4m3 or e2m1 each; z (bf16 or fp32) is added to with accumulate."""
+    pz, zd, ldz = _matrix(z, rows, out_cols, z_dtype, ld_z, "z")
+    b = _vector(bias, out_cols, bias_dtype, "bias")
+    ws, wsb = _workspace(workspace)
+    st = lib().zr_ckpt_linear(_ckpt(x, rows, in_cols, "x", x_format), x_format, _ckpt(w, out_cols, in_cols, "w", w_format),
+                              w_format, rows, in_cols, out_cols, b[0], _one_dtype(b, (0, None), ("bias",)), pz, zd, ldz,
+                              ZR_ACCUMULATE if accumulate else 0, ws, wsb, _run_on(stream, x, w, bias, z, workspace))
+    if st:
+        _check(st)
 
 
 # ------------------------------------- gradient norm, clipping and AdamW

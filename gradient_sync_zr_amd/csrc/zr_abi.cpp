@@ -308,7 +308,10 @@ namespace {
 constexpr int64_t kMaxCols = (int64_t)1 << 30;
 
 bool fmt_valid(int dt) { return dt == ZR_CKPT_E4M3 || dt == ZR_CKPT_INT8; }
+bool pack_valid(int dt) { return fmt_valid(dt) || dt == ZR_CKPT_E2M1; }
 int64_t pitch_of(int64_t cols) { return (cols + 31) / 32 * 32; }
+// Bytes of a row's codes and exponents.
+int64_t row_bytes(int64_t cols, int dt) { return pitch_of(cols) / 32 * (dt == ZR_CKPT_E2M1 ? 17 : 33); }
 // rows x ld, ld rounded up to whole blocks, within 2^40 (ld may be any number:
 // it is rounded up only where that cannot overflow).
 bool size_valid(int64_t rows, int64_t ld) {
@@ -337,6 +340,13 @@ bool mats_overlap(const Mat& a, const Mat& b) {
 
 // Buffers of a call: outputs must be disjoint from each other and from the
 // inputs, but for the pairs that `same` allows at equal address and shape.
+// An output that may lie where an input does (same address, row stride and width), if
+// `ok`: the elements are of one type.
+struct Place {
+    const char *out, *in;
+    bool ok;
+};
+
 struct Buffers {
     struct List {  // no call has more than 8 of either
         Mat m[8];
@@ -370,12 +380,29 @@ struct Buffers {
         (output ? out : in).push_back(Mat{(uintptr_t)p, 1, n * es, n * es, name});
         return ok();
     }
-    zr_status ckpt(bool output, const void* p, int64_t rows, int64_t cols, const char* name) {
+    zr_status ckpt(bool output, const void* p, int64_t rows, int64_t cols, const char* name, int format = ZR_CKPT_E4M3) {
         if (!size_valid(rows, cols)) return fail(ZR_ERR_INVALID, "%s is larger than 2^40 elements", name);
         if (rows == 0) return ok();
         ZR_TRY(check(p, 16, name));
-        const int64_t bytes = rows * (pitch_of(cols) / 32 * 33);
+        const int64_t bytes = rows * row_bytes(cols, format);
         (output ? out : in).push_back(Mat{(uintptr_t)p, 1, bytes, bytes, name});
+        return ok();
+    }
+    zr_status disjoint(const Place* places, int n) const {
+        for (int i = 0; i < out.size(); ++i) {
+            for (int j = i + 1; j < out.size(); ++j)
+                if (mats_overlap(out[i], out[j]))
+                    return fail(ZR_ERR_ALIAS, "%s and %s overlap", out[i].name, out[j].name);
+            for (const Mat& m : in) {
+                if (!mats_overlap(out[i], m)) continue;
+                bool fine = false;
+                for (int k = 0; k < n; ++k)
+                    fine = fine || (places[k].ok && !std::strcmp(places[k].out, out[i].name) &&
+                                    !std::strcmp(places[k].in, m.name) && out[i].lo == m.lo && out[i].rows == m.rows &&
+                                    out[i].pitch == m.pitch && out[i].width == m.width);
+                if (!fine) return fail(ZR_ERR_ALIAS, "%s overlaps %s", out[i].name, m.name);
+            }
+        }
         return ok();
     }
     // in_place: this output may be an input of the same address, row stride and width
@@ -1092,37 +1119,64 @@ size_t zr_ckpt_bytes(int64_t rows, int64_t cols) {
     return (size_t)rows * (size_t)(pitch_of(cols) / 32 * 33);
 }
 
+size_t zr_ckpt_format_bytes(int64_t rows, int64_t cols, zr_dtype format) {
+    if (!pack_valid(format) || cols < 1 || cols > kMaxCols || !size_valid(rows, cols)) return 0;
+    return (size_t)rows * (size_t)row_bytes(cols, format);
+}
+
 zr_status zr_ckpt_pack(const void* x, zr_dtype dt, int64_t rows, int64_t cols, int64_t ld, void* ckpt, zr_dtype format,
                        void* stream) {
     return zr::guarded([&]() -> zr_status {
-        if (!dt_valid(dt) || !fmt_valid(format))
+        if (!dt_valid(dt) || !pack_valid(format))
             return fail(ZR_ERR_UNSUPPORTED, "dtype %d to format %d not supported", (int)dt, (int)format);
         ZR_TRY(check_cols(rows, cols, "cols"));
         Buffers b;
         ZR_TRY(b.matrix(false, x, dt_bytes(dt), rows, cols, ld, "x"));
-        ZR_TRY(b.ckpt(true, ckpt, rows, cols, "ckpt"));
+        ZR_TRY(b.ckpt(true, ckpt, rows, cols, "ckpt", format));
         ZR_TRY(b.disjoint(nullptr));
         if (rows == 0) return ok();
         ZR_TRY(have(launch_ckpt_pack, "checkpoint pack"));
-        return launched(launch_ckpt_pack(x, dt, rows, cols, ld, format, ckpt, (hipStream_t)stream), (hipStream_t)stream,
-                        "checkpoint pack launch");
+        const hipStream_t s = (hipStream_t)stream;
+        return launched(format == ZR_CKPT_E2M1 ? launch_pack_small(x, dt, rows, cols, ld, ckpt, s)
+                                               : launch_ckpt_pack(x, dt, rows, cols, ld, format, ckpt, s),
+                        s, "checkpoint pack launch");
+    });
+}
+
+zr_status zr_ckpt_pack_t(const void* x, zr_dtype dt, int64_t rows, int64_t cols, int64_t ld, void* ckpt, zr_dtype format,
+                         void* stream) {
+    return zr::guarded([&]() -> zr_status {
+        if (!dt_valid(dt) || !pack_valid(format))
+            return fail(ZR_ERR_UNSUPPORTED, "dtype %d to format %d not supported", (int)dt, (int)format);
+        ZR_TRY(check_cols(rows, cols, "cols"));
+        // the packed matrix has x's rows for columns
+        if (rows < 1 || rows > kMaxCols) return fail(ZR_ERR_INVALID, "rows=%lld not in [1, 2^30]", (long long)rows);
+        Buffers b;
+        ZR_TRY(b.matrix(false, x, dt_bytes(dt), rows, cols, ld, "x"));
+        ZR_TRY(b.ckpt(true, ckpt, cols, rows, "ckpt", format));
+        ZR_TRY(b.disjoint(nullptr));
+        ZR_TRY(have(launch_pack_t, "transposed pack"));
+        return launched(launch_pack_t(x, dt, rows, cols, ld, ckpt, format, (hipStream_t)stream), (hipStream_t)stream,
+                        "transposed pack launch");
     });
 }
 
 zr_status zr_ckpt_unpack(const void* ckpt, zr_dtype format, int64_t rows, int64_t cols, void* x, zr_dtype dt, int64_t ld,
                          void* stream) {
     return zr::guarded([&]() -> zr_status {
-        if (!dt_valid(dt) || !fmt_valid(format))
+        if (!dt_valid(dt) || !pack_valid(format))
             return fail(ZR_ERR_UNSUPPORTED, "format %d to dtype %d not supported", (int)format, (int)dt);
         ZR_TRY(check_cols(rows, cols, "cols"));
         Buffers b;
-        ZR_TRY(b.ckpt(false, ckpt, rows, cols, "ckpt"));
+        ZR_TRY(b.ckpt(false, ckpt, rows, cols, "ckpt", format));
         ZR_TRY(b.matrix(true, x, dt_bytes(dt), rows, cols, ld, "x"));
         ZR_TRY(b.disjoint(nullptr));
         if (rows == 0) return ok();
         ZR_TRY(have(launch_ckpt_unpack, "checkpoint unpack"));
-        return launched(launch_ckpt_unpack(ckpt, format, rows, cols, x, dt, ld, (hipStream_t)stream),
-                        (hipStream_t)stream, "checkpoint unpack launch");
+        const hipStream_t s = (hipStream_t)stream;
+        return launched(format == ZR_CKPT_E2M1 ? launch_unpack_small(ckpt, rows, cols, x, dt, ld, s)
+                                               : launch_ckpt_unpack(ckpt, format, rows, cols, x, dt, ld, s),
+                        s, "checkpoint unpack launch");
     });
 }
 
@@ -1247,6 +1301,130 @@ zr_status zr_ckpt_wgrad(const void* dy, zr_dtype dy_dt, int64_t ld_dy, const voi
         w.accumulate = (flags & ZR_ACCUMULATE) != 0;
         w.workspace = workspace;
         return launched(launch_ckpt_wgrad(w, (hipStream_t)stream), (hipStream_t)stream, "weight gradient launch");
+    });
+}
+
+zr_status zr_rmsnorm_fwd(const void* x, zr_dtype x_dt, int64_t rows, int64_t cols, int64_t ld_x, const void* residual,
+                         int64_t ld_res, void* h, int64_t ld_h, zr_dtype h_dt, const void* weight, zr_dtype param_dt,
+                         float eps, void* y, zr_dtype y_dt, int64_t ld_y, float* rstd, void* ckpt_h, void* ckpt_y,
+                         zr_dtype ckpt_format, void* stream) {
+    return zr::guarded([&]() -> zr_status {
+        const bool held = fmt_valid(x_dt);
+        if ((!dt_valid(x_dt) && !held) || !dt_valid(param_dt) || !dt_valid(y_dt) || !dt_valid(h_dt))
+            return fail(ZR_ERR_UNSUPPORTED, "dtypes x %d, h %d, weight %d, y %d not supported", (int)x_dt, (int)h_dt,
+                        (int)param_dt, (int)y_dt);
+        if ((ckpt_h || ckpt_y) && !fmt_valid(ckpt_format))
+            return fail(ZR_ERR_UNSUPPORTED, "checkpoint format %d not supported", (int)ckpt_format);
+        ZR_TRY(check_cols(rows, cols, "cols"));
+        if (!(eps >= 0.0f && eps <= 3.4e38f)) return fail(ZR_ERR_INVALID, "eps=%g is not >= 0 and finite", (double)eps);
+        if (rows > 0 && h && !residual) return fail(ZR_ERR_INVALID, "h is given without a residual: it would be x");
+        if (held && ckpt_h && !residual) return fail(ZR_ERR_INVALID, "ckpt_h is given for an h that is the checkpoint x");
+        if (rows > 0 && !y && !rstd && !h && !ckpt_h && !ckpt_y) return fail(ZR_ERR_INVALID, "no output is given");
+        Buffers b;
+        ZR_TRY(held ? b.ckpt(false, x, rows, cols, "x") : b.matrix(false, x, dt_bytes(x_dt), rows, cols, ld_x, "x"));
+        if (residual) ZR_TRY(b.matrix(false, residual, dt_bytes(h_dt), rows, cols, ld_res, "residual"));
+        if (weight) ZR_TRY(b.vector(false, weight, dt_bytes(param_dt), cols, "weight"));
+        if (h) ZR_TRY(b.matrix(true, h, dt_bytes(h_dt), rows, cols, ld_h, "h"));
+        if (y) ZR_TRY(b.matrix(true, y, dt_bytes(y_dt), rows, cols, ld_y, "y"));
+        if (rstd) ZR_TRY(b.vector(true, rstd, 4, rows, "rstd"));
+        if (ckpt_h) ZR_TRY(b.ckpt(true, ckpt_h, rows, cols, "ckpt_h"));
+        if (ckpt_y) ZR_TRY(b.ckpt(true, ckpt_y, rows, cols, "ckpt_y"));
+        // h or y may take x's place, or the residual's, where the elements are of one type
+        const Place places[] = {{"h", "x", x_dt == h_dt}, {"h", "residual", true}, {"y", "x", x_dt == y_dt},
+                                {"y", "residual", h_dt == y_dt}};
+        ZR_TRY(b.disjoint(places, 4));
+        if (rows == 0) return ok();
+        ZR_TRY(have(launch_rmsnorm_fwd, "RMS norm"));
+        RmsFwd f{};
+        f.x = x; f.residual = residual; f.weight = weight;
+        f.x_dt = x_dt; f.h_dt = h_dt; f.param_dt = param_dt; f.y_dt = y_dt; f.ckpt_format = ckpt_format;
+        f.rows = rows; f.cols = cols; f.ld_x = ld_x; f.ld_res = ld_res; f.ld_h = ld_h; f.ld_y = ld_y;
+        f.eps = eps;
+        f.h = h; f.y = y; f.ckpt_h = ckpt_h; f.ckpt_y = ckpt_y;
+        f.rstd = rstd;
+        return launched(launch_rmsnorm_fwd(f, (hipStream_t)stream), (hipStream_t)stream, "RMS norm launch");
+    });
+}
+
+size_t zr_rmsnorm_workspace_bytes(int64_t rows, int64_t cols) {
+    if (cols < 1 || cols > kMaxCols || !size_valid(rows, cols)) return 0;
+    return (size_t)rmsnorm_workspace(rows, cols) * sizeof(float);
+}
+
+zr_status zr_rmsnorm_bwd(const void* dy, zr_dtype dy_dt, int64_t ld_dy, const void* h, zr_dtype h_dt, int64_t ld_h,
+                         int64_t rows, int64_t cols, const void* weight, zr_dtype param_dt, const float* rstd, void* dx,
+                         zr_dtype dx_dt, int64_t ld_dx, void* dweight, zr_dtype grad_dt, int flags, void* workspace,
+                         size_t ws_bytes, void* stream) {
+    return zr::guarded([&]() -> zr_status {
+        const bool held = fmt_valid(h_dt);
+        if ((!dt_valid(h_dt) && !held) || !dt_valid(dy_dt) || !dt_valid(param_dt) || !dt_valid(dx_dt) || !dt_valid(grad_dt))
+            return fail(ZR_ERR_UNSUPPORTED, "dtypes dy %d, h %d, weight %d, dx %d, dweight %d not supported", (int)dy_dt,
+                        (int)h_dt, (int)param_dt, (int)dx_dt, (int)grad_dt);
+        if (flags & ~(ZR_ACCUMULATE | ZR_ADD_DX)) return fail(ZR_ERR_INVALID, "flags=%d has unknown bits", flags);
+        ZR_TRY(check_cols(rows, cols, "cols"));
+        if (rows > 0 && !dx && !dweight) return fail(ZR_ERR_INVALID, "no output is given");
+        Buffers b;
+        ZR_TRY(b.matrix(false, dy, dt_bytes(dy_dt), rows, cols, ld_dy, "dy"));
+        ZR_TRY(held ? b.ckpt(false, h, rows, cols, "h") : b.matrix(false, h, dt_bytes(h_dt), rows, cols, ld_h, "h"));
+        if (weight) ZR_TRY(b.vector(false, weight, dt_bytes(param_dt), cols, "weight"));
+        ZR_TRY(b.vector(false, rstd, 4, rows, "rstd"));
+        if (dx) ZR_TRY(b.matrix(true, dx, dt_bytes(dx_dt), rows, cols, ld_dx, "dx"));
+        if (dweight) {
+            ZR_TRY(b.vector(true, dweight, dt_bytes(grad_dt), cols, "dweight"));
+            ZR_TRY(need_workspace(b, workspace, ws_bytes, zr_rmsnorm_workspace_bytes(rows, cols)));
+        }
+        // dx may take dy's or h's place where the elements are of one type
+        const Place places[] = {{"dx", "dy", dx_dt == dy_dt}, {"dx", "h", dx_dt == h_dt}};
+        ZR_TRY(b.disjoint(places, 2));
+        // without rows there is nothing to add, and what is added to stays as it is
+        if (rows == 0 && (!dweight || (flags & ZR_ACCUMULATE))) return ok();
+        ZR_TRY(have(launch_rmsnorm_bwd, "RMS norm backward"));
+        RmsBwd f{};
+        f.dy = dy; f.h = h; f.weight = weight; f.rstd = rstd;
+        f.dy_dt = dy_dt; f.h_dt = h_dt; f.param_dt = param_dt; f.dx_dt = dx_dt; f.grad_dt = grad_dt;
+        f.rows = rows; f.cols = cols; f.ld_dy = ld_dy; f.ld_h = ld_h; f.ld_dx = ld_dx;
+        f.dx = dx; f.dweight = dweight;
+        f.accumulate = (flags & ZR_ACCUMULATE) != 0; f.add_dx = (flags & ZR_ADD_DX) != 0;
+        f.workspace = workspace;
+        return launched(launch_rmsnorm_bwd(f, (hipStream_t)stream), (hipStream_t)stream, "RMS norm backward launch");
+    });
+}
+
+size_t zr_ckpt_linear_workspace_bytes(int64_t rows, int64_t in_cols, int64_t out_cols) {
+    if (out_cols < 1 || out_cols > kMaxCols || in_cols < 1 || in_cols > kMaxCols || !size_valid(rows, out_cols) ||
+        !size_valid(rows, in_cols) || !size_valid(out_cols, in_cols))
+        return 0;
+    return (size_t)linear_workspace(rows, out_cols, in_cols) * sizeof(float);
+}
+
+zr_status zr_ckpt_linear(const void* x, zr_dtype x_format, const void* w, zr_dtype w_format, int64_t rows, int64_t in_cols,
+                         int64_t out_cols, const void* bias, zr_dtype bias_dt, void* z, zr_dtype z_dt, int64_t ld_z,
+                         int flags, void* workspace, size_t ws_bytes, void* stream) {
+    return zr::guarded([&]() -> zr_status {
+        auto product = [](int f) { return f == ZR_CKPT_E4M3 || f == ZR_CKPT_E2M1; };
+        if (!product(x_format) || !product(w_format) || !dt_valid(bias_dt) || !dt_valid(z_dt))
+            return fail(ZR_ERR_UNSUPPORTED, "formats x %d, w %d, dtypes bias %d, z %d not supported", (int)x_format,
+                        (int)w_format, (int)bias_dt, (int)z_dt);
+        if (flags & ~ZR_ACCUMULATE) return fail(ZR_ERR_INVALID, "flags=%d has unknown bits", flags);
+        ZR_TRY(check_cols(rows, in_cols, "in_cols"));
+        ZR_TRY(check_cols(rows, out_cols, "out_cols"));
+        Buffers b;
+        ZR_TRY(b.ckpt(false, x, rows, in_cols, "x", x_format));
+        ZR_TRY(b.ckpt(false, w, out_cols, in_cols, "w", w_format));
+        if (bias) ZR_TRY(b.vector(false, bias, dt_bytes(bias_dt), out_cols, "bias"));
+        ZR_TRY(b.matrix(true, z, dt_bytes(z_dt), rows, out_cols, ld_z, "z"));
+        if (rows > 0) ZR_TRY(need_workspace(b, workspace, ws_bytes, zr_ckpt_linear_workspace_bytes(rows, in_cols, out_cols)));
+        ZR_TRY(b.disjoint(nullptr));
+        if (rows == 0) return ok();
+        ZR_TRY(have(launch_linear, "linear layer"));
+        Linear f{};
+        f.x = x; f.w = w; f.bias = bias;
+        f.x_format = x_format; f.w_format = w_format; f.bias_dt = bias_dt; f.z_dt = z_dt;
+        f.rows = rows; f.in = in_cols; f.out = out_cols; f.ld_z = ld_z;
+        f.z = z;
+        f.accumulate = (flags & ZR_ACCUMULATE) != 0;
+        f.workspace = workspace;
+        return launched(launch_linear(f, (hipStream_t)stream), (hipStream_t)stream, "linear layer launch");
     });
 }
 

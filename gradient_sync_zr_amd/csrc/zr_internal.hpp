@@ -359,4 +359,83 @@ struct AdamW {
 };
 ZR_KERNELS hipError_t launch_adamw(const AdamW& f, hipStream_t stream);
 
+struct RmsFwd {
+    const void *x, *residual, *weight;
+    zr_dtype x_dt, h_dt, param_dt, y_dt, ckpt_format;
+    int64_t rows, cols, ld_x, ld_res, ld_h, ld_y;
+    float eps;
+    void *h, *y, *ckpt_h, *ckpt_y;
+    float* rstd;
+};
+ZR_KERNELS hipError_t launch_rmsnorm_fwd(const RmsFwd& f, hipStream_t stream);
+
+struct RmsBwd {
+    const void *dy, *h, *weight;
+    const float* rstd;
+    zr_dtype dy_dt, h_dt, param_dt, dx_dt, grad_dt;
+    int64_t rows, cols, ld_dy, ld_h, ld_dx;
+    void *dx, *dweight;
+    int accumulate, add_dx;
+    void* workspace;  // of rmsnorm_workspace() floats
+};
+ZR_KERNELS hipError_t launch_rmsnorm_bwd(const RmsBwd& f, hipStream_t stream);
+// The layer norm's strips; a strip leaves one row of sums.
+inline int64_t rmsnorm_workspace(int64_t rows, int64_t cols) {
+    const int64_t strips = layernorm_strips(rows, cols);
+    return strips > 1 || cols > 12288 ? strips * cols : 0;
+}
+
+// Packing of e2m1 blocks, and of a transpose (of any format).
+ZR_KERNELS hipError_t launch_pack_small(const void* x, zr_dtype dt, int64_t rows, int64_t cols, int64_t ld, void* ckpt,
+                                        hipStream_t stream);
+ZR_KERNELS hipError_t launch_unpack_small(const void* ckpt, int64_t rows, int64_t cols, void* x, zr_dtype dt, int64_t ld,
+                                          hipStream_t stream);
+ZR_KERNELS hipError_t launch_pack_t(const void* x, zr_dtype dt, int64_t rows, int64_t cols, int64_t ld, void* ckpt,
+                                    zr_dtype fmt, hipStream_t stream);
+
+struct Linear {
+    const void *x, *w, *bias;
+    zr_dtype x_format, w_format, bias_dt, z_dt;
+    int64_t rows, in, out, ld_z;
+    void* z;
+    int accumulate;
+    void* workspace;  // of linear_workspace() floats
+};
+ZR_KERNELS hipError_t launch_linear(const Linear& f, hipStream_t stream);
+
+// How a product of packed matrices is cut: form 0 for few rows, tiles of 128 x 128
+// (1) or 256 x 256 (2), and the columns in `parts` of `share` steps, joined from
+// the workspace.
+struct LinearCut {
+    int form, parts;
+    int64_t steps, share;
+};
+constexpr int kLinearGroup = 512;         // columns of a load of exponents
+constexpr int64_t kLinearWide = 1 << 23;  // columns up to which a tile's rows lie within 32-bit offsets
+inline LinearCut linear_cut(int64_t rows, int64_t out, int64_t in, bool both4, bool exact) {
+    (void)exact;
+    const int64_t step = both4 ? 256 : 128;
+    if (rows <= 64 || in > kLinearWide) return LinearCut{0, 1, (in + 127) / 128, (in + 127) / 128};
+    LinearCut c{2, 1, (in + step - 1) / step, 0};
+    auto tiles = [&](int64_t t) { return ((rows + t - 1) / t) * ((out + t - 1) / t); };
+    if (tiles(256) < 200) c.form = 1;
+    const int64_t n = tiles(c.form == 2 ? 256 : 128), places = c.form == 2 ? 256 : 512;
+    int64_t parts = 1;
+    while (parts * 2 * n <= places && parts * 2 <= c.steps / 2 && parts < 32) parts *= 2;
+    const int64_t whole = kLinearGroup / step;  // a part begins where a load of exponents does
+    c.share = ((c.steps + parts - 1) / parts + whole - 1) / whole * whole;
+    c.parts = (int)((c.steps + c.share - 1) / c.share);
+    return c;
+}
+// Floats of workspace that the cut needs, whatever the formats.
+inline int64_t linear_workspace(int64_t rows, int64_t out, int64_t in) {
+    int64_t need = 0;
+    for (int k = 0; k < 3; ++k) {
+        const LinearCut c = linear_cut(rows, out, in, k == 0, k == 1);
+        const int64_t n = c.parts > 1 ? c.parts * rows * out : 0;
+        need = n > need ? n : need;
+    }
+    return need;
+}
+
 }  // namespace zr

@@ -1,0 +1,611 @@
+// Product of two packed matrices, as a linear layer's forward pass has it:
+//     z[t, o] = sum_i x[t, i] * w[o, i] + bias[o]
+// with x and w in blocks of 32 columns (e4m3 or e2m1 codes and one power of two
+// each), which are the operands of the scaled matrix instructions: a lane brings
+// the codes and the exponent bytes of its row, and no value is decoded.
+//
+// What the instructions do with the products decides between two ways:
+//  - e2m1 by e2m1: products and sums are exact up to the fp32 accumulator;
+//  - with e4m3 on either side the products that one lane brings are added with 13
+//    bits below the largest of them (measured: 2^16 + 2^2 keeps both, 2^16 + 2^1 does
+//    not), which is below what a bf16 result keeps and not below fp32's. So bf16
+//    results take the scaled instructions, and for fp32 results both operands are
+//    decoded to bf16 on their way from LDS (every held value is exact there) and
+//    go through the bf16 instructions, which sum in fp32.
+#include <hip/hip_runtime.h>
+
+#include <type_traits>
+
+#include "zr_e2m1.hpp"
+#include "zr_internal.hpp"
+#include "zr_norm.hpp"
+
+namespace zr {
+namespace {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+struct LinArgs {
+    const char *w, *x;          // codes
+    const uint8_t *ws, *xs;     // exponents
+    const void* bias;
+    void* z;
+    float* part;                // parts > 1: [parts][rows][out]
+    int64_t rows, out, wrow, xrow, sp, ld_z;  // bytes of a row of codes, of exponents
+    int64_t steps, share;       // steps over the columns, of a part
+    int bias_dt, z_dt, accumulate, tiles_o, tiles_t, parts;
+};
+
+__device__ __forceinline__ int uniform(uint32_t v) { return __builtin_amdgcn_readfirstlane((int)v); }
+
+// Blocks are dealt to the 8 XCDs in turn: neighbours among `total` items for
+// the blocks of one XCD, so that their operands meet in that XCD's L2.
+__device__ __forceinline__ uint32_t by_xcd(uint32_t item, uint32_t total) {
+    const uint32_t x = item % 8, i = item / 8, q = total / 8, r = total % 8;
+    return (x < r ? x * (q + 1) : r * (q + 1) + (x - r) * q) + i;
+}
+
+// 16 codes (e4m3: 16 bytes; e2m1: 8) as two bf16 operands.
+template <int FMT>
+__device__ __forceinline__ void decode16(const u32x4& q, float scale, bf16x8 f[2]) {
+    uint32_t w[8];
+    if constexpr (FMT == kE2m1) {
+        const uint32_t c[2] = {q.x, q.y};
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            w[4 * k] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[k], scale, 0));
+            w[4 * k + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[k], scale, 1));
+            w[4 * k + 2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[k], scale, 2));
+            w[4 * k + 3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[k], scale, 3));
+        }
+    } else {
+        const uint32_t c[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            w[2 * k] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[k], scale, false));
+            w[2 * k + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[k], scale, true));
+        }
+    }
+    f[0] = __builtin_bit_cast(bf16x8, u32x4{w[0], w[1], w[2], w[3]});
+    f[1] = __builtin_bit_cast(bf16x8, u32x4{w[4], w[5], w[6], w[7]});
+}
+
+// The scale of an exponent byte for the decoding (0 where the block does not
+// exist: its codes count for nothing beside the other operand's, 0 as well).
+__device__ __forceinline__ float scale_of(uint32_t byte) { return __uint_as_float(byte << 23); }
+
+// Eight neighbouring results of a row, with bias and old values, rounded once; or,
+// into a part of the workspace, as they are.
+__device__ __forceinline__ void put8(const LinArgs& a, float* part, int64_t t, int64_t o, const float v[8]) {
+    const int64_t left = a.out - o;
+    const int n = left >= 8 ? 8 : (left > 0 ? (int)left : 0);
+    if (n == 0) return;
+    float f[8];
+    if (part) {
+        store8<false>((char*)(part + t * a.out + o), kFp32, 0, n, v);
+        return;
+    }
+    load_param8(a.bias ? (const char*)a.bias + o * (a.bias_dt == kBf16 ? 2 : 4) : nullptr, a.bias_dt, 0, n, 0.0f, f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] += v[e];
+    char* const z = (char*)a.z + (t * a.ld_z + o) * (a.z_dt == kBf16 ? 2 : 4);
+    if (a.accumulate) {
+        float old[8];
+        load_param8(z, a.z_dt, 0, n, 0.0f, old);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] += old[e];
+    }
+    store8<false>(z, a.z_dt, 0, n, f);
+}
+
+// ------------------------------------------------------------- tiled form
+// LDS holds a tile's rows of BK codes in 16-byte chunks, lines of 128 bytes (one
+// row, or two of 64). A chunk's place in its line is exchanged by the line's
+// number, so that the 8 lines that 8 lanes read at once lie in different banks. The loads
+// write LDS directly, a wave's 64 chunks in a row, so the exchange is made in
+// the addresses that the lanes load from.
+template <int RB>
+__device__ __forceinline__ int chunk_at(int row, int c) {
+    if constexpr (RB == 128) return row * 128 + ((c ^ (row & 7)) << 4);
+    const int line = row >> 1;
+    return line * 128 + ((((row & 1) * 4 + c) ^ (line & 7)) << 4);
+}
+
+// Row and chunk that belong to the LDS slot.
+template <int RB>
+__device__ __forceinline__ void chunk_of(int slot, int* row, int* c) {
+    const int line = slot >> 3, p = (slot & 7) ^ (line & 7);
+    if constexpr (RB == 128) {
+        *row = line;
+        *c = p;
+    } else {
+        *row = line * 2 + (p >> 2);
+        *c = p & 3;
+    }
+}
+
+typedef __attribute__((address_space(3))) char* lptr;
+
+// 16 bytes of every lane from base + offset to LDS, at `to` (the same for the wave)
+// plus `down` plus 16 times the lane. Written in assembly because the compiler, which cannot
+// tell the two stages apart, waits for its own such loads before every read of LDS;
+// the kernel waits once, in front of the barrier that publishes a stage. There
+// is no register that the load still writes to.
+__device__ __forceinline__ void load_lds16(const char* base, uint32_t offset, uint32_t to, int down) {
+    asm volatile("s_add_u32 m0, %0, %3\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(offset), "s"(base), "i"(down)
+                 : "m0", "scc", "memory");
+}
+
+// 16 exponent bytes of a row from byte `at` (< sp) on, the row `row` bytes behind
+// `base`; those behind the row's `sp` are 0. Nothing is read from `size` bytes on, the
+// buffer's end: the last rows' bytes are then read early, from the codes' side, and
+// moved into place.
+__device__ __forceinline__ u32x4 exponents16(const uint8_t* base, int row, int at, int sp, int size) {
+    typedef u32x4 u32x4_a1 __attribute__((aligned(1)));
+    int over = row + at + 16 - size;
+    over = over > 0 ? over : 0;
+    const u32x4 v = behind(*(const u32x4_a1*)(base + (row + at - over)), over * 8);
+    const int left = sp - at < 16 ? sp - at : 16;
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int n = left - 4 * k;  // bytes of this word that the row has
+        w[k] = n >= 4 ? w[k] : (n <= 0 ? 0u : w[k] & ((1u << (8 * n)) - 1));
+    }
+    return u32x4{w[0], w[1], w[2], w[3]};
+}
+
+// A tile's product. Eight (four) waves have WO outputs of WT tokens each; the
+// weight's rows are the matrix instructions' A, so that a lane ends with one token
+// and neighbouring outputs.
+//
+// A stage is BK codes of every row. It goes through in units of 64 codes (32 where
+// operands are decoded), and within a unit by 32 of the wave's outputs: ST steps of
+// NT matrix instructions each. The operands of a step are read one or two steps ahead. The
+// barrier that publishes the next stage stands before the last two steps, whose
+// operands are in registers by then: behind it the stage that they are from is free for the
+// loads of the one after the next, and the next stage's first operands are read.
+// A turn of the loop is the stages of 512 codes, whose exponents are loaded at once,
+// a turn ahead. There is no branch in a turn: stages behind the last have exponents
+// of 0, and the loads ahead of the last are of it once more.
+template <int FW, int FX, bool EXACT, int BO, int BT, int WO, int WT>
+__global__ __launch_bounds__((BO / WO) * (BT / WT) * 64) void linear_kernel(LinArgs a) {
+    constexpr int T = (BO / WO) * (BT / WT) * 64;
+    constexpr bool PAIR4 = FW == kE2m1 && FX == kE2m1;
+    constexpr int BK = PAIR4 ? 256 : 128;  // codes of a stage
+    constexpr int RW = FW == kE2m1 ? BK / 2 : BK, RX = FX == kE2m1 ? BK / 2 : BK;
+    constexpr int SW = BO * RW, SX = BT * RX, STAGE = SW + SX;
+    constexpr int NW = SW / 16 / T, NX = SX / 16 / T;
+    constexpr int SPG = kLinearGroup / BK, SB = BK / 32, SWORDS = SB / 4;  // stages per load of exponents; a stage's
+    constexpr int SCALES = (BO + BT) * 16;
+    constexpr int MT = WO / 32, NT = WT / 32;
+    constexpr int UNIT = EXACT ? 32 : 64, ST = BK / UNIT * MT;
+    static_assert(SW / 16 % T == 0 && SX / 16 % T == 0 && BO + BT == T, "whole chunks per thread");
+    constexpr int RESULTS = T / 64 * WO * 32 * 4, LDS = 2 * STAGE + 2 * SCALES;
+    // operands of 8 registers on both sides are read one step ahead where the results
+    // take half of the registers, the others two
+    constexpr int AHEAD = FW == kE4m3 && FX == kE4m3 && !EXACT && MT * NT == 8 ? 1 : 2;
+    static_assert(ST % 4 == 0, "the operands' ring");
+    // the weight's two stages, x's two, exponents twice: within an instruction's offset
+    __shared__ __attribute__((aligned(1024))) char lds[RESULTS > LDS ? RESULTS : LDS];
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wo = wave / (BT / WT), wt = wave % (BT / WT);
+    const int r = lane & 31, g = lane >> 5;
+    // where a lane's first chunk lies; the others are at exchanges of bits 4 to 6
+    constexpr bool HALF_W = EXACT && FW == kE2m1, HALF_X = EXACT && FX == kE2m1;
+    const int place_w = wo * WO * RW + chunk_at<RW>(r, HALF_W ? 0 : g) + (HALF_W ? 8 * g : 0);
+    const int place_x = 2 * SW + wt * WT * RX + chunk_at<RX>(r, HALF_X ? 0 : g) + (HALF_X ? 8 * g : 0);
+    const int scale_w = 2 * STAGE + (wo * WO + r) * 16, scale_x = 2 * STAGE + (BO + wt * WT + r) * 16;
+    const uint32_t to = (uint32_t)__builtin_amdgcn_readfirstlane((int)((uint32_t)(uintptr_t)(lptr)lds + (uint32_t)wave * 1024));
+    const uint32_t total = (uint32_t)a.tiles_o * (uint32_t)a.tiles_t * (uint32_t)a.parts;
+
+#pragma unroll 1
+    for (uint32_t item = blockIdx.x; item < total; item += gridDim.x) {
+        const uint32_t at = by_xcd(item, total), tiles = (uint32_t)(a.tiles_o * a.tiles_t);
+        const int part = uniform(at / tiles);
+        // tiles in groups of 8 rows of tiles
+        const uint32_t t = at % tiles, per = 8 * (uint32_t)a.tiles_o, group = t / per, in_group = t - group * per;
+        const uint32_t gm = (uint32_t)a.tiles_t - group * 8 < 8 ? (uint32_t)a.tiles_t - group * 8 : 8;
+        const int tile_o = uniform(in_group / gm), tt = uniform(group * 8 + in_group % gm);
+        const int64_t o0 = (int64_t)tile_o * BO, t0 = (int64_t)tt * BT;
+        // (stages fit 32 bits: columns do)
+        const int s0 = (int)(part * a.share), s1 = (int)((part + 1) * a.share < a.steps ? (part + 1) * a.share : a.steps);
+
+        // this thread's chunks, from the tile's first row on: rows behind the last are
+        // read from it, and not stored
+        const char* const tw = a.w + o0 * a.wrow;
+        const char* const tx = a.x + t0 * a.xrow;
+        uint32_t pw[NW], px[NX];
+        int cw = 0, cx = 0;
+#pragma unroll
+        for (int j = 0; j < NW; ++j) {
+            int row;
+            chunk_of<RW>(j * T + tid, &row, &cw);
+            const int64_t most = a.out - 1 - o0;
+            pw[j] = (uint32_t)(row < most ? row : (int)most) * (uint32_t)a.wrow;
+        }
+#pragma unroll
+        for (int j = 0; j < NX; ++j) {
+            int row;
+            chunk_of<RX>(j * T + tid, &row, &cx);
+            const int64_t most = a.rows - 1 - t0;
+            px[j] = (uint32_t)(row < most ? row : (int)most) * (uint32_t)a.xrow;
+        }
+        auto fetch = [&](auto BUF, int s) {
+            constexpr int buf = decltype(BUF)::value;
+            // columns behind the last are read from it: their exponents are 0
+            const uint32_t bw = (uint32_t)(s * RW) + cw * 16, bx = (uint32_t)(s * RX) + cx * 16;
+            const uint32_t lw = (uint32_t)a.wrow - 16, lx = (uint32_t)a.xrow - 16;
+            const uint32_t ow = bw < lw ? bw : lw, ox = bx < lx ? bx : lx;
+#pragma unroll
+            for (int j = 0; j < NW; ++j) load_lds16(tw, pw[j] + ow, to, buf * SW + j * T * 16);
+#pragma unroll
+            for (int j = 0; j < NX; ++j) load_lds16(tx, px[j] + ox, to, 2 * SW + buf * SX + j * T * 16);
+        };
+        // the row whose exponents this thread brings, 16 at a time: the weight's or x's, the
+        // same for a wave
+        const bool of_w = wave * 64 < BO;
+        const uint8_t* const eb = of_w ? a.ws + o0 * a.sp : a.xs + t0 * a.sp;
+        const int64_t erows = of_w ? a.out - o0 : a.rows - t0, ebytes = erows * a.sp;
+        const int esize = ebytes < (1 << 30) ? (int)ebytes : 1 << 30, esp = (int)a.sp;  // a tile's are below 2^27
+        const int erow = tid - (of_w ? 0 : BO), eat = (erow < erows ? erow : (int)erows - 1) * esp;
+
+        f32x16 acc[MT][NT];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int k = 0; k < 16; ++k) acc[m][n][k] = 0.0f;
+
+        typedef std::conditional_t<EXACT, u32x4, i32x8> Raw;
+        Raw fw[4], fx[2][NT];
+        bf16x8 dx[NT][2];  // decoded
+        uint32_t ew[2][MT][SWORDS], ex[2][NT][SWORDS];
+        auto operand = [&](int at, int u, int down, auto fmt) -> Raw {
+            constexpr bool four = decltype(fmt)::value == kE2m1;
+            if constexpr (EXACT) {
+                if constexpr (four) {
+                    const u32x2 h = *(const u32x2*)(lds + (at ^ (u * 16)) + down);
+                    return u32x4{h.x, h.y, 0, 0};
+                } else {
+                    return *(const u32x4*)(lds + (at ^ (u * 32)) + down);
+                }
+            } else if constexpr (four) {  // chunk g of a unit's two
+                const u32x4 q = *(const u32x4*)(lds + (at ^ (u * 32)) + down);
+                return i32x8{(int)q.x, (int)q.y, (int)q.z, (int)q.w, 0, 0, 0, 0};
+            } else {  // chunks g and 2 + g of a unit's four
+                const u32x4 p = *(const u32x4*)(lds + (at ^ (u * 64)) + down);
+                const u32x4 q = *(const u32x4*)(lds + (at ^ (u * 64 + 32)) + down);
+                return i32x8{(int)p.x, (int)p.y, (int)p.z, (int)p.w, (int)q.x, (int)q.y, (int)q.z, (int)q.w};
+            }
+        };
+        auto read_w = [&](int buf, int i) {
+            fw[i & 3] = operand(place_w, i / MT, buf * SW + (i % MT) * 32 * RW, std::integral_constant<int, FW>{});
+        };
+        auto read_x = [&](int buf, int u) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                fx[u & 1][n] = operand(place_x, u, buf * SX + n * 32 * RX, std::integral_constant<int, FX>{});
+        };
+        // exponents of a stage, as they lie; before the stage's first step they are
+        // moved so that a lane's blocks g, 2 + g, ... are in the bytes that the instructions select
+        auto read_exponents = [&](int half, int in16, int set) {
+            const int at = half + in16 * SB;
+#pragma unroll
+            for (int k = 0; k < SWORDS; ++k) {
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+                    ew[set][m][k] = *(const uint32_t*)(lds + scale_w + at + m * 512 + 4 * k);
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    ex[set][n][k] = *(const uint32_t*)(lds + scale_x + at + n * 512 + 4 * k);
+            }
+        };
+        auto align_exponents = [&](int set) {
+            if constexpr (!EXACT) {
+#pragma unroll
+                for (int k = 0; k < SWORDS; ++k) {
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) ew[set][m][k] >>= 8 * g;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) ex[set][n][k] >>= 8 * g;
+                }
+            }
+        };
+        auto multiply = [&](auto I, int set) {
+            constexpr int i = decltype(I)::value, u = i / MT, m = i % MT;
+            if constexpr (EXACT) {
+                if constexpr (m == 0) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        decode16<FX>(fx[u & 1][n], scale_of((ex[set][n][0] >> (8 * u)) & 255), dx[n]);
+                }
+                bf16x8 dw[2];
+                decode16<FW>(fw[i & 3], scale_of((ew[set][m][0] >> (8 * u)) & 255), dw);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(dw[h], dx[n][h], acc[m][n], 0, 0, 0);
+            } else {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    acc[m][n] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                        fw[i & 3], fx[u & 1][n], acc[m][n], FW == kE2m1 ? 4 : 0, FX == kE2m1 ? 4 : 0, (u & 1) * 2,
+                        (int)ew[set][m][u / 2], (u & 1) * 2, (int)ex[set][n][u / 2]);
+            }
+        };
+
+        const int g0 = s0 / SPG, g1 = (s1 + SPG - 1) / SPG;  // turns
+        __syncthreads();  // the last item's LDS is free
+        fetch(std::integral_constant<int, 0>{}, s0);
+        u32x4 e = exponents16(eb, eat, g0 * 16, esp, esize);
+        *(u32x4*)(lds + 2 * STAGE + tid * 16) = e;
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+        fetch(std::integral_constant<int, 1>{}, s0 + 1);
+        read_exponents(0, 0, 0);
+        read_x(0, 0);
+        read_w(0, 0);
+        if constexpr (AHEAD == 2) read_w(0, 1);
+        int half = 0;  // where this turn's exponents lie
+#pragma unroll 1
+        for (int turn = g0; turn < g1; ++turn) {
+            e = exponents16(eb, eat, (turn + 1 < g1 ? turn + 1 : turn) * 16, esp, esize);
+            auto steps = [&](auto self, auto J) {
+                constexpr int j = decltype(J)::value, in16 = j / ST, i = j % ST, buf = in16 & 1, set = in16 & 1;
+                if constexpr (j < SPG * ST) {
+                    if constexpr (i == 0) align_exponents(set);
+                    if constexpr (i == ST - 2) {
+                        if constexpr (AHEAD == 1) read_w(buf, ST - 1);
+                        if constexpr (in16 == SPG - 1) *(u32x4*)(lds + 2 * STAGE + (half ^ SCALES) + tid * 16) = e;
+                        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+                        __syncthreads();
+                        fetch(std::integral_constant<int, buf>{}, turn * SPG + in16 + 2);
+                        // behind the last stage what is read is not multiplied
+                        read_x(buf ^ 1, 0);
+                        if constexpr (AHEAD == 2) read_w(buf ^ 1, 0);
+                        read_exponents(in16 == SPG - 1 ? half ^ SCALES : half, (in16 + 1) % SPG, set ^ 1);
+                    } else if constexpr (i == ST - 1) {
+                        read_w(buf ^ 1, AHEAD - 1);
+                    } else {
+                        read_w(buf, i + AHEAD);
+                        if constexpr (i % MT == 0 && i / MT + 1 < ST / MT) read_x(buf, i / MT + 1);
+                    }
+                    multiply(std::integral_constant<int, i>{}, set);
+                    // keeps the step's matrix instructions here: nothing else orders
+                    // them among the loads and barriers of a turn
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) asm volatile("" : "+v"(acc[i % MT][n]));
+                    __builtin_amdgcn_sched_barrier(0);
+                    self(self, std::integral_constant<int, j + 1>{});
+                }
+            };
+            steps(steps, std::integral_constant<int, 0>{});
+            half ^= SCALES;
+        }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the loads ahead, before their places are used
+
+        // D: a lane has token lane & 31 and, four at a time, outputs (k / 4) * 8 + g * 4
+        // on. The wave's results go through LDS, 32 tokens at a time (16-byte chunks
+        // exchanged by the token), to be written as rows of neighbouring outputs.
+        __syncthreads();
+        float* const mine = a.parts > 1 ? a.part + (int64_t)part * a.rows * a.out : nullptr;
+        char* const own = lds + wave * (WO * 32 * 4);
+        constexpr int CH = WO / 4, LANES = WO / 8;  // chunks of a token, lanes of 8 outputs
+        int ol = lane;  // opaque: addresses made from it are not kept in registers through the product
+        asm volatile("" : "+v"(ol));
+        const int rr = ol & 31, rg = ol >> 5;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int c = m * 8 + k * 2 + rg;
+                    *(f32x4*)(own + rr * (WO * 4) + ((c ^ (rr & (CH - 1))) << 4)) =
+                        f32x4{acc[m][n][4 * k], acc[m][n][4 * k + 1], acc[m][n][4 * k + 2], acc[m][n][4 * k + 3]};
+                }
+            __builtin_amdgcn_sched_barrier(0);
+            const int64_t o = o0 + wo * WO + (ol % LANES) * 8;
+#pragma unroll 1
+            for (int k = 0; k < 32; k += 64 / LANES) {
+                const int q = k + ol / LANES, c = (ol % LANES) * 2;
+                const f32x4 lo = *(const f32x4*)(own + q * (WO * 4) + ((c ^ (q & (CH - 1))) << 4));
+                const f32x4 hi = *(const f32x4*)(own + q * (WO * 4) + (((c + 1) ^ (q & (CH - 1))) << 4));
+                const int64_t tok = t0 + wt * WT + n * 32 + q;
+                if (tok >= a.rows || o >= a.out) continue;
+                const float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                put8(a, mine, tok, o, v);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+}
+
+// Sums the parts, in order, eight neighbouring outputs a thread.
+__global__ __launch_bounds__(kThreads) void linear_join_kernel(LinArgs a) {
+    const int64_t eights = (a.out + 7) / 8, next = a.rows * a.out;
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < a.rows * eights; i += (int64_t)gridDim.x * kThreads) {
+        const int64_t t = i / eights, o = (i - t * eights) * 8;
+        const int n = existing(a.out, o);
+        float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        for (int p = 0; p < a.parts; ++p) {
+            float f[8];
+            load_param8(a.part + p * next + t * a.out + o, kFp32, 0, n, 0.0f, f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] += f[e];
+        }
+        put8(a, nullptr, t, o, v);
+    }
+}
+
+// -------------------------------------------------------------- few rows
+// Up to 64 tokens: the weight's bytes count, and each goes from memory to the
+// matrix instruction's registers once. A block of 8 waves takes 16 outputs; its
+// waves take every 8th step of 128 columns, with the loads of 4 steps in flight,
+// and are added in LDS. (Rows of codes too long for the tiled form's 32-bit
+// offsets come here too, 64 tokens at a time.)
+template <int FMT, bool EXACT>
+struct Piece {  // a row's 128 codes, one lane's quarter
+    u32x4 p, q;
+    uint32_t s, s2;
+};
+
+template <int FMT, bool EXACT>
+__device__ __forceinline__ Piece<FMT, EXACT> piece(const char* row, const uint8_t* exps, int64_t bytes, int64_t sp, int64_t s,
+                                                   int g) {
+    Piece<FMT, EXACT> v;
+    auto within = [&](int64_t at, int n) { return at < bytes - n ? at : bytes - n; };
+    auto byte = [&](int64_t b) { return b < sp ? (uint32_t)exps[b] : 0u; };
+    if constexpr (FMT == kE2m1 && !EXACT) {
+        v.p = *(const u32x4*)(row + within(s * 64 + g * 16, 16));
+        v.q = u32x4{0, 0, 0, 0};
+    } else if constexpr (FMT == kE2m1) {
+        const u32x2 x = *(const u32x2*)(row + within(s * 64 + g * 8, 8)), y = *(const u32x2*)(row + within(s * 64 + 32 + g * 8, 8));
+        v.p = u32x4{x.x, x.y, 0, 0};
+        v.q = u32x4{y.x, y.y, 0, 0};
+    } else {
+        v.p = *(const u32x4*)(row + within(s * 128 + g * 16, 16));
+        v.q = *(const u32x4*)(row + within(s * 128 + 64 + g * 16, 16));
+    }
+    if constexpr (EXACT) {
+        v.s = byte(s * 4 + g / 2);
+        v.s2 = byte(s * 4 + 2 + g / 2);
+    } else {
+        v.s = byte(s * 4 + g);
+        v.s2 = 0;
+    }
+    return v;
+}
+
+template <int FW, int FX, bool EXACT, int NG>
+__global__ __launch_bounds__(512) void linear_few_kernel(LinArgs a) {
+    constexpr int U = NG == 1 ? 4 : 2;
+    __shared__ f32x4 red[8][NG][64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
+    for (int64_t item = blockIdx.x; item < (int64_t)a.tiles_o * a.tiles_t; item += gridDim.x) {
+        const int64_t tt = item / a.tiles_o, t0 = tt * (NG * 16), o0 = (item - tt * a.tiles_o) * 16;
+        const int64_t o = o0 + r < a.out ? o0 + r : a.out - 1;
+        const char* const w = a.w + o * a.wrow;
+        const uint8_t* const ws = a.ws + o * a.sp;
+        f32x4 acc[NG];
+#pragma unroll
+        for (int n = 0; n < NG; ++n) acc[n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int64_t s = wave; s < a.steps; s += 8 * U) {
+            Piece<FW, EXACT> fw[U];
+            Piece<FX, EXACT> fx[U][NG];
+#pragma unroll
+            for (int u = 0; u < U; ++u) fw[u] = piece<FW, EXACT>(w, ws, a.wrow, a.sp, s + 8 * u, g);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int n = 0; n < NG; ++n) {
+                    const int64_t t = t0 + n * 16 + r < a.rows ? t0 + n * 16 + r : a.rows - 1;
+                    fx[u][n] = piece<FX, EXACT>(a.x + t * a.xrow, a.xs + t * a.sp, a.xrow, a.sp, s + 8 * u, g);
+                }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int n = 0; n < NG; ++n) {
+                    const auto &p = fw[u];
+                    const auto &q = fx[u][n];
+                    if constexpr (EXACT) {
+                        bf16x8 x[2], y[2];
+                        decode16<FW>(p.p, scale_of(p.s), x);
+                        decode16<FX>(q.p, scale_of(q.s), y);
+                        acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[0], y[0], acc[n], 0, 0, 0);
+                        acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[1], y[1], acc[n], 0, 0, 0);
+                        decode16<FW>(p.q, scale_of(p.s2), x);
+                        decode16<FX>(q.q, scale_of(q.s2), y);
+                        acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[0], y[0], acc[n], 0, 0, 0);
+                        acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[1], y[1], acc[n], 0, 0, 0);
+                    } else {
+                        const i32x8 x = {(int)p.p.x, (int)p.p.y, (int)p.p.z, (int)p.p.w, (int)p.q.x, (int)p.q.y, (int)p.q.z, (int)p.q.w};
+                        const i32x8 y = {(int)q.p.x, (int)q.p.y, (int)q.p.z, (int)q.p.w, (int)q.q.x, (int)q.q.y, (int)q.q.z, (int)q.q.w};
+                        acc[n] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, acc[n], FW == kE2m1 ? 4 : 0, FX == kE2m1 ? 4 : 0,
+                                                                                  0, (int)p.s, 0, (int)q.s);
+                    }
+                }
+        }
+#pragma unroll
+        for (int n = 0; n < NG; ++n) red[wave][n][lane] = acc[n];
+        __syncthreads();
+        // red[.][n][g * 16 + token]: outputs g * 4 on; two of them are eight neighbours
+        for (int i = threadIdx.x; i < NG * 32; i += 512) {
+            const int n = i / 32, l = (i & 15) + (i & 16) * 2;
+            float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    v[e] += red[k][n][l][e];
+                    v[4 + e] += red[k][n][l + 16][e];
+                }
+            const int64_t t = t0 + n * 16 + (l & 15);
+            if (t < a.rows) put8(a, nullptr, t, o0 + (l >> 4) * 4, v);
+        }
+        __syncthreads();
+    }
+}
+
+template <int FW, int FX, bool EXACT>
+hipError_t run(LinArgs& a, const LinearCut& cut, hipStream_t stream) {
+    if (cut.form == 0) {
+        a.tiles_o = (int)((a.out + 15) / 16);
+        a.tiles_t = (int)((a.rows + 63) / 64);
+        const int grid = grid_for((int64_t)a.tiles_o * a.tiles_t, 512);
+        if (a.rows <= 16)
+            linear_few_kernel<FW, FX, EXACT, 1><<<grid, 512, 0, stream>>>(a);
+        else if (a.rows <= 32)
+            linear_few_kernel<FW, FX, EXACT, 2><<<grid, 512, 0, stream>>>(a);
+        else
+            linear_few_kernel<FW, FX, EXACT, 4><<<grid, 512, 0, stream>>>(a);
+        return hipGetLastError();
+    }
+    const int tile = cut.form == 1 ? 128 : 256;
+    a.tiles_o = (int)((a.out + tile - 1) / tile);
+    a.tiles_t = (int)((a.rows + tile - 1) / tile);
+    const int64_t total = (int64_t)a.tiles_o * a.tiles_t * a.parts;
+    if (cut.form == 1)
+        linear_kernel<FW, FX, EXACT, 128, 128, 64, 64><<<grid_for(total, 256), 256, 0, stream>>>(a);
+    else
+        linear_kernel<FW, FX, EXACT, 256, 256, 128, 64><<<grid_for(total, 512), 512, 0, stream>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.parts == 1) return e;
+    const int64_t items = (a.rows * ((a.out + 7) / 8) + kThreads - 1) / kThreads;
+    linear_join_kernel<<<grid_for(items, kThreads), kThreads, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_linear(const Linear& f, hipStream_t stream) {
+    const bool w4 = f.w_format == ZR_CKPT_E2M1, x4 = f.x_format == ZR_CKPT_E2M1;
+    const bool exact = f.z_dt == ZR_FP32 && !(w4 && x4);
+    const LinearCut cut = linear_cut(f.rows, f.out, f.in, w4 && x4, exact);
+    const int64_t pitch = ckpt_pitch(f.in);
+    LinArgs a{};
+    a.w = (const char*)f.w; a.x = (const char*)f.x;
+    a.wrow = w4 ? pitch / 2 : pitch; a.xrow = x4 ? pitch / 2 : pitch;
+    a.ws = (const uint8_t*)f.w + f.out * a.wrow;
+    a.xs = (const uint8_t*)f.x + f.rows * a.xrow;
+    a.sp = pitch / kCkptBlock;
+    a.bias = f.bias; a.z = f.z; a.part = (float*)f.workspace;
+    a.rows = f.rows; a.out = f.out; a.ld_z = f.ld_z;
+    a.bias_dt = f.bias_dt; a.z_dt = f.z_dt; a.accumulate = f.accumulate;
+    a.steps = cut.steps; a.share = cut.share; a.parts = cut.parts;
+    if (w4 && x4) return run<kE2m1, kE2m1, false>(a, cut, stream);
+    if (exact) {
+        if (w4) return run<kE2m1, kE4m3, true>(a, cut, stream);
+        return x4 ? run<kE4m3, kE2m1, true>(a, cut, stream) : run<kE4m3, kE4m3, true>(a, cut, stream);
+    }
+    if (w4) return run<kE2m1, kE4m3, false>(a, cut, stream);
+    return x4 ? run<kE4m3, kE2m1, false>(a, cut, stream) : run<kE4m3, kE4m3, false>(a, cut, stream);
+}
+
+}  // namespace zr

@@ -115,6 +115,7 @@ typedef enum {
     ZR_FP32 = 1,
     ZR_CKPT_E4M3 = 2, /* 8-bit activation checkpoints: only the norm and checkpoint */
     ZR_CKPT_INT8 = 3, /* calls below take these */
+    ZR_CKPT_E2M1 = 4, /* 4-bit blocks: the packing and the linear layer's calls */
     ZR_DTYPE_MIN_ = -2147483647 - 1,
     ZR_DTYPE_MAX_ = 2147483647
 } zr_dtype;
@@ -579,8 +580,9 @@ zr_status zr_pf_plan(const zr_pf_config* cfg, int iterations, zr_pf_stats* out);
 size_t zr_ckpt_bytes(int64_t rows, int64_t cols);
 
 /* x (dt ZR_BF16 or ZR_FP32, row stride ld) into a checkpoint and back;
- * format ZR_CKPT_E4M3 or ZR_CKPT_INT8. Unpacking to bf16 is exact. The
- * buffers must not overlap (ZR_ERR_ALIAS). */
+ * format ZR_CKPT_E4M3 or ZR_CKPT_INT8, or ZR_CKPT_E2M1 (4-bit blocks, described
+ * at zr_ckpt_linear). Unpacking to bf16 is exact. The buffers must not overlap
+ * (ZR_ERR_ALIAS). */
 zr_status zr_ckpt_pack(const void* x, zr_dtype dt, int64_t rows, int64_t cols, int64_t ld,
                        void* ckpt, zr_dtype format, void* stream);
 zr_status zr_ckpt_unpack(const void* ckpt, zr_dtype format, int64_t rows, int64_t cols, void* x,
@@ -673,6 +675,108 @@ zr_status zr_ckpt_wgrad(const void* dy, zr_dtype dy_dt, int64_t ld_dy, const voi
                         int64_t rows, int64_t out_cols, int64_t in_cols, void* dw, zr_dtype grad_dt,
                         int64_t ld_dw, void* dbias, int flags, void* workspace, size_t ws_bytes,
                         void* stream);
+
+/* ------------------------------------- RMS norm and packed linear layers
+ * The forward operators beside the layer norm, and the products that read packed
+ * activations and packed weights. Matrices, strides and checkpoints are as above. */
+
+/*
+ * RMS norm with the residual's addition, forward. For every row:
+ *     h = x + residual, rounded to h_dt (h = x without a residual)
+ *     rstd = 1 / sqrt(sum(h^2) / cols + eps),  y = h * rstd * weight
+ * in fp32 of the rounded h, y rounded once to its type.
+ *
+ *  x          as in zr_layernorm_fwd: values, or a checkpoint
+ *  residual   rows x cols of h_dt (ZR_BF16 or ZR_FP32), row stride ld_res, or NULL
+ *  h          receives the sum, the residual stream behind this norm: h_dt, row
+ *             stride ld_h; or NULL (the sum is rounded to h_dt all the same). Only
+ *             with a residual
+ *  weight     cols elements of param_dt, or NULL (1)
+ *  eps        >= 0, finite
+ *  y          y_dt, row stride ld_y; or NULL
+ *  rstd       fp32, rows elements, or NULL
+ *  ckpt_h     NULL, or a checkpoint that receives h (not where h is the checkpoint x)
+ *  ckpt_y     NULL, or a checkpoint that receives y as rounded to y_dt (with y NULL
+ *             too): y in 8 bits with scales, what zr_ckpt_linear and zr_ckpt_wgrad read
+ *  ckpt_format    ZR_CKPT_E4M3 or ZR_CKPT_INT8, of ckpt_h and ckpt_y
+ * At least one output, if there are rows; outputs overlap neither each other nor
+ * an input, but h or y may be x or the residual (same address, type and row
+ * stride).
+ */
+zr_status zr_rmsnorm_fwd(const void* x, zr_dtype x_dt, int64_t rows, int64_t cols, int64_t ld_x, const void* residual,
+                         int64_t ld_res, void* h, int64_t ld_h, zr_dtype h_dt, const void* weight, zr_dtype param_dt,
+                         float eps, void* y, zr_dtype y_dt, int64_t ld_y, float* rstd, void* ckpt_h, void* ckpt_y,
+                         zr_dtype ckpt_format, void* stream);
+
+/* Bytes of workspace of zr_rmsnorm_bwd for dweight (none without it); 0 for
+ * sizes out of range. Host only. */
+size_t zr_rmsnorm_workspace_bytes(int64_t rows, int64_t cols);
+
+/*
+ * RMS norm, backward. With xh = h * rstd and g = dy * weight:
+ *     dx      = rstd * (g - xh * sum(g * xh) / cols)
+ *     dweight = sum over rows of dy * xh
+ * in fp32, each rounded once to its type. dx is the gradient of h, and so of x and
+ * of the residual; with ZR_ADD_DX what came to h past the norm is added.
+ *
+ *  dy, h      dy_dt ZR_BF16 or ZR_FP32; h (x where there was no residual) values of
+ *             h_dt with row stride ld_h, or a checkpoint
+ *  rstd       fp32, rows elements, of the forward pass
+ *  dx         dx_dt, or NULL. dx may be dy or h (same address, type and row stride)
+ *  dweight    cols elements of grad_dt, or NULL
+ *  flags      ZR_ACCUMULATE (dweight), ZR_ADD_DX (dx)
+ *  workspace  4-byte aligned, zr_rmsnorm_workspace_bytes(rows, cols) bytes (NULL
+ *             where that is 0), if dweight is given; shared as zr_layernorm_bwd's
+ * rows == 0: dx is untouched, dweight becomes 0 (or stays).
+ */
+zr_status zr_rmsnorm_bwd(const void* dy, zr_dtype dy_dt, int64_t ld_dy, const void* h, zr_dtype h_dt, int64_t ld_h,
+                         int64_t rows, int64_t cols, const void* weight, zr_dtype param_dt, const float* rstd, void* dx,
+                         zr_dtype dx_dt, int64_t ld_dx, void* dweight, zr_dtype grad_dt, int flags, void* workspace,
+                         size_t ws_bytes, void* stream);
+
+/* Bytes of a packed rows x cols matrix of any format; 0 for sizes or formats out
+ * of range. Host only. */
+size_t zr_ckpt_format_bytes(int64_t rows, int64_t cols, zr_dtype format);
+
+/* The transpose of x (rows x cols, dt, row stride ld), cols x rows, packed: what
+ * zr_ckpt_linear takes as weight for the gradient of a layer's input. Any format;
+ * 1 <= rows <= 2^30. */
+zr_status zr_ckpt_pack_t(const void* x, zr_dtype dt, int64_t rows, int64_t cols, int64_t ld, void* ckpt,
+                         zr_dtype format, void* stream);
+
+/* Bytes of workspace of zr_ckpt_linear (0: none needed, or sizes out of range).
+ * Host only. */
+size_t zr_ckpt_linear_workspace_bytes(int64_t rows, int64_t in_cols, int64_t out_cols);
+
+/*
+ * A linear layer on packed operands:
+ *     z[t, o] = sum over i of x[t, i] * w[o, i] + bias[o]
+ * Its backward pass is the same call, with dz packed and the weight packed by
+ * zr_ckpt_pack_t, and zr_ckpt_wgrad.
+ *
+ *  x          packed rows x in_cols, x_format ZR_CKPT_E4M3 or ZR_CKPT_E2M1
+ *  w          packed out_cols x in_cols, w_format of the same two
+ *  bias       out_cols elements of bias_dt, or NULL
+ *  z          rows x out_cols of z_dt (ZR_BF16 or ZR_FP32), row stride ld_z
+ *  flags      ZR_ACCUMULATE: z is added to (old + new in fp32)
+ *  workspace  4-byte aligned, zr_ckpt_linear_workspace_bytes bytes (NULL where that
+ *             is 0); shared as zr_layernorm_bwd's
+ *
+ * ZR_CKPT_E2M1 is the checkpoints' layout with codes of 4 bits: rows of P / 2 bytes,
+ * the even column in a byte's low half, then the exponents as there; a code's value
+ * is its e2m1 value (0, 0.5, 1, 1.5, 2, 3, 4, 6) times 2^e, M = 6. So
+ * |held - x| is at most max(2^-2 |x|, 2^(e-2)). Blocks that are not finite, zeros'
+ * signs and the range's end are as in e4m3.
+ *
+ * Products of held values are exact. They are summed in fp32, but for one case:
+ * bf16 results with e4m3 on either side take the scaled matrix instructions, which
+ * add the 16 neighbouring products (of 16 columns of a block) with 13 bits below
+ * the largest of them before they go to fp32. Each result is rounded once. A block
+ * that is not finite makes the results that it takes part in NaN.
+ */
+zr_status zr_ckpt_linear(const void* x, zr_dtype x_format, const void* w, zr_dtype w_format, int64_t rows,
+                         int64_t in_cols, int64_t out_cols, const void* bias, zr_dtype bias_dt, void* z, zr_dtype z_dt,
+                         int64_t ld_z, int flags, void* workspace, size_t ws_bytes, void* stream);
 
 /* ------------------------------------- gradient norm, clipping and AdamW
  * What stands between the reduce-scatter and the all-gather, over any number of
