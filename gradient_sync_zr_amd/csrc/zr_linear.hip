@@ -34,7 +34,7 @@ struct LinArgs {
     void* z;
     float* part;                // parts > 1: [parts][rows][out]
     int64_t rows, out, wrow, xrow, sp, ld_z;  // bytes of a row of codes, of exponents
-    int64_t steps, share;       // steps over the columns, of a part
+    int64_t turns, share;       // turns of 512 columns, of a part
     int bias_dt, z_dt, accumulate, tiles_o, tiles_t, parts;
 };
 
@@ -97,33 +97,35 @@ __device__ __forceinline__ void put8(const LinArgs& a, float* part, int64_t t, i
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] += old[e];
     }
-    store8<false>(z, a.z_dt, 0, n, f);
+    store8<true>(z, a.z_dt, 0, n, f);  // past the caches: 16384x11008x4096 of e2m1 475 us without, 431 with
 }
 
 // ------------------------------------------------------------- tiled form
-// LDS holds a tile's rows of BK codes in 16-byte chunks, lines of 128 bytes (one
-// row, or two of 64). A chunk's place in its line is exchanged by the line's
-// number, so that the 8 lines that 8 lanes read at once lie in different banks. The loads
-// write LDS directly, a wave's 64 chunks in a row, so the exchange is made in
-// the addresses that the lanes load from.
+// LDS holds a stage's rows, of 64 or 32 bytes, in 16-byte chunks: lines of 128 bytes
+// (two rows or four), two lines across its 64 banks. A chunk's place in its line is
+// exchanged by the number of the pair of lines, so that the 16 chunks of 16
+// neighbouring rows, which a read takes at once, lie in different banks. (Exchanged by
+// the line's number, half of the reads' cycles were conflicts.) The loads write LDS
+// directly, a wave's 64 chunks in a row, so the exchange is made in the addresses
+// that the lanes load from. 32 rows further down it is the same.
+template <int RB>
+__device__ __forceinline__ int chunk_swap(int line) {
+    return (line >> 1) & (RB == 64 ? 7 : 3);
+}
+
 template <int RB>
 __device__ __forceinline__ int chunk_at(int row, int c) {
-    if constexpr (RB == 128) return row * 128 + ((c ^ (row & 7)) << 4);
-    const int line = row >> 1;
-    return line * 128 + ((((row & 1) * 4 + c) ^ (line & 7)) << 4);
+    constexpr int ROWS = 128 / RB;
+    const int line = row / ROWS, at = row % ROWS * (RB / 16) + c;
+    return line * 128 + ((at ^ chunk_swap<RB>(line)) << 4);
 }
 
 // Row and chunk that belong to the LDS slot.
 template <int RB>
 __device__ __forceinline__ void chunk_of(int slot, int* row, int* c) {
-    const int line = slot >> 3, p = (slot & 7) ^ (line & 7);
-    if constexpr (RB == 128) {
-        *row = line;
-        *c = p;
-    } else {
-        *row = line * 2 + (p >> 2);
-        *c = p & 3;
-    }
+    const int line = slot >> 3, p = (slot & 7) ^ chunk_swap<RB>(line);
+    *row = line * (128 / RB) + p / (RB / 16);
+    *c = p % (RB / 16);
 }
 
 typedef __attribute__((address_space(3))) char* lptr;
@@ -146,7 +148,7 @@ __device__ __forceinline__ u32x4 exponents16(const uint8_t* base, int row, int a
     typedef u32x4 u32x4_a1 __attribute__((aligned(1)));
     int over = row + at + 16 - size;
     over = over > 0 ? over : 0;
-    const u32x4 v = behind(*(const u32x4_a1*)(base + (row + at - over)), over * 8);
+    const u32x4 v = behind((u32x4)*(const u32x4_a1*)(base + (row + at - over)), over * 8);
     const int left = sp - at < 16 ? sp - at : 16;
     uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -157,48 +159,51 @@ __device__ __forceinline__ u32x4 exponents16(const uint8_t* base, int row, int a
     return u32x4{w[0], w[1], w[2], w[3]};
 }
 
+// Waits until at most N of the wave's loads are in flight (they end in order).
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"i"(N) : "memory");
+}
+
 // A tile's product. Eight (four) waves have WO outputs of WT tokens each; the
 // weight's rows are the matrix instructions' A, so that a lane ends with one token
 // and neighbouring outputs.
 //
-// A stage is BK codes of every row. It goes through in units of 64 codes (32 where
-// operands are decoded), and within a unit by 32 of the wave's outputs: ST steps of
-// NT matrix instructions each. The operands of a step are read one or two steps ahead. The
-// barrier that publishes the next stage stands before the last two steps, whose
-// operands are in registers by then: behind it the stage that they are from is free for the
-// loads of the one after the next, and the next stage's first operands are read.
-// A turn of the loop is the stages of 512 codes, whose exponents are loaded at once,
-// a turn ahead. There is no branch in a turn: stages behind the last have exponents
-// of 0, and the loads ahead of the last are of it once more.
+// A stage is BK codes of every row, and LDS holds STAGES of them, so that loads have the
+// time of two stages and more to arrive. A stage goes through in units of 64 codes
+// (32 where operands are decoded), and a unit by 32 of the wave's outputs: steps of NT
+// matrix instructions each, whose operands are read AHEAD steps earlier. The barrier
+// that publishes a stage stands before the first of these reads; by then all of the stage
+// before has been read, and its place takes the loads of the stage STAGES - 1 behind
+// the published one. A turn of the loop is the stages of 512 codes, whose exponents
+// are loaded at once, a turn ahead. Stages behind the last have exponents of 0, and
+// the loads ahead of the last are of it once more.
 template <int FW, int FX, bool EXACT, int BO, int BT, int WO, int WT>
 __global__ __launch_bounds__((BO / WO) * (BT / WT) * 64) void linear_kernel(LinArgs a) {
     constexpr int T = (BO / WO) * (BT / WT) * 64;
     constexpr bool PAIR4 = FW == kE2m1 && FX == kE2m1;
-    constexpr int BK = PAIR4 ? 256 : 128;  // codes of a stage
+    constexpr int BK = PAIR4 ? 128 : 64, STAGES = 4;
     constexpr int RW = FW == kE2m1 ? BK / 2 : BK, RX = FX == kE2m1 ? BK / 2 : BK;
-    constexpr int SW = BO * RW, SX = BT * RX, STAGE = SW + SX;
-    constexpr int NW = SW / 16 / T, NX = SX / 16 / T;
-    constexpr int SPG = kLinearGroup / BK, SB = BK / 32, SWORDS = SB / 4;  // stages per load of exponents; a stage's
+    constexpr int SW = BO * RW, SX = BT * RX;
+    constexpr int NW = SW / 16 / T, NX = SX / 16 / T, LOADS = NW + NX;
+    constexpr int SPT = kLinearGroup / BK;  // stages of a turn
     constexpr int SCALES = (BO + BT) * 16;
     constexpr int MT = WO / 32, NT = WT / 32;
-    constexpr int UNIT = EXACT ? 32 : 64, ST = BK / UNIT * MT;
+    constexpr int UNIT = EXACT ? 32 : 64, ST = BK / UNIT * MT, STEPS = SPT * ST, AHEAD = 2;
     static_assert(SW / 16 % T == 0 && SX / 16 % T == 0 && BO + BT == T, "whole chunks per thread");
-    constexpr int RESULTS = T / 64 * WO * 32 * 4, LDS = 2 * STAGE + 2 * SCALES;
-    // operands of 8 registers on both sides are read one step ahead where the results
-    // take half of the registers, the others two
-    constexpr int AHEAD = FW == kE4m3 && FX == kE4m3 && !EXACT && MT * NT == 8 ? 1 : 2;
-    static_assert(ST % 4 == 0, "the operands' ring");
-    // the weight's two stages, x's two, exponents twice: within an instruction's offset
+    static_assert(ST >= AHEAD && STEPS % 4 == 0 && SPT % STAGES == 0 && STAGES == 4, "the rings' turns");
+    constexpr int RESULTS = T / 64 * WO * 32 * 4, EXPS = STAGES * (SW + SX), LDS = EXPS + 2 * SCALES;
+    // the weight's stages, x's, exponents twice; the stages within an instruction's offset
     __shared__ __attribute__((aligned(1024))) char lds[RESULTS > LDS ? RESULTS : LDS];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wo = wave / (BT / WT), wt = wave % (BT / WT);
     const int r = lane & 31, g = lane >> 5;
-    // where a lane's first chunk lies; the others are at exchanges of bits 4 to 6
+    // where a lane's first chunk lies; the others are at exchanges of bits 4 and 5
     constexpr bool HALF_W = EXACT && FW == kE2m1, HALF_X = EXACT && FX == kE2m1;
     const int place_w = wo * WO * RW + chunk_at<RW>(r, HALF_W ? 0 : g) + (HALF_W ? 8 * g : 0);
-    const int place_x = 2 * SW + wt * WT * RX + chunk_at<RX>(r, HALF_X ? 0 : g) + (HALF_X ? 8 * g : 0);
-    const int scale_w = 2 * STAGE + (wo * WO + r) * 16, scale_x = 2 * STAGE + (BO + wt * WT + r) * 16;
+    const int place_x = STAGES * SW + wt * WT * RX + chunk_at<RX>(r, HALF_X ? 0 : g) + (HALF_X ? 8 * g : 0);
+    const int scale_w = EXPS + (wo * WO + r) * 16, scale_x = EXPS + (BO + wt * WT + r) * 16;
     const uint32_t to = (uint32_t)__builtin_amdgcn_readfirstlane((int)((uint32_t)(uintptr_t)(lptr)lds + (uint32_t)wave * 1024));
     const uint32_t total = (uint32_t)a.tiles_o * (uint32_t)a.tiles_t * (uint32_t)a.parts;
 
@@ -211,8 +216,8 @@ __global__ __launch_bounds__((BO / WO) * (BT / WT) * 64) void linear_kernel(LinA
         const uint32_t gm = (uint32_t)a.tiles_t - group * 8 < 8 ? (uint32_t)a.tiles_t - group * 8 : 8;
         const int tile_o = uniform(in_group / gm), tt = uniform(group * 8 + in_group % gm);
         const int64_t o0 = (int64_t)tile_o * BO, t0 = (int64_t)tt * BT;
-        // (stages fit 32 bits: columns do)
-        const int s0 = (int)(part * a.share), s1 = (int)((part + 1) * a.share < a.steps ? (part + 1) * a.share : a.steps);
+        // the part's turns (they fit 32 bits: columns do)
+        const int g0 = (int)(part * a.share), g1 = (int)((part + 1) * a.share < a.turns ? (part + 1) * a.share : a.turns);
 
         // this thread's chunks, from the tile's first row on: rows behind the last are
         // read from it, and not stored
@@ -243,7 +248,7 @@ __global__ __launch_bounds__((BO / WO) * (BT / WT) * 64) void linear_kernel(LinA
 #pragma unroll
             for (int j = 0; j < NW; ++j) load_lds16(tw, pw[j] + ow, to, buf * SW + j * T * 16);
 #pragma unroll
-            for (int j = 0; j < NX; ++j) load_lds16(tx, px[j] + ox, to, 2 * SW + buf * SX + j * T * 16);
+            for (int j = 0; j < NX; ++j) load_lds16(tx, px[j] + ox, to, STAGES * SW + buf * SX + j * T * 16);
         };
         // the row whose exponents this thread brings, 16 at a time: the weight's or x's, the
         // same for a wave
@@ -252,6 +257,15 @@ __global__ __launch_bounds__((BO / WO) * (BT / WT) * 64) void linear_kernel(LinA
         const int64_t erows = of_w ? a.out - o0 : a.rows - t0, ebytes = erows * a.sp;
         const int esize = ebytes < (1 << 30) ? (int)ebytes : 1 << 30, esp = (int)a.sp;  // a tile's are below 2^27
         const int erow = tid - (of_w ? 0 : BO), eat = (erow < erows ? erow : (int)erows - 1) * esp;
+        // exponents of a turn to half h: directly, where rows are whole words of them and the
+        // row has all 16, else by registers, where all loads are waited for
+        auto fetch_exponents = [&](int turn, int half) {
+            if (esp % 4 == 0 && turn * 16 + 16 <= esp) {
+                load_lds16((const char*)eb, (uint32_t)(eat + turn * 16), to + (uint32_t)half, EXPS);
+            } else {
+                *(u32x4*)(lds + EXPS + half + tid * 16) = exponents16(eb, eat, turn * 16, esp, esize);
+            }
+        };
 
         f32x16 acc[MT][NT];
 #pragma unroll
@@ -264,7 +278,7 @@ __global__ __launch_bounds__((BO / WO) * (BT / WT) * 64) void linear_kernel(LinA
         typedef std::conditional_t<EXACT, u32x4, i32x8> Raw;
         Raw fw[4], fx[2][NT];
         bf16x8 dx[NT][2];  // decoded
-        uint32_t ew[2][MT][SWORDS], ex[2][NT][SWORDS];
+        uint32_t ew[2][MT], ex[2][NT];
         auto operand = [&](int at, int u, int down, auto fmt) -> Raw {
             constexpr bool four = decltype(fmt)::value == kE2m1;
             if constexpr (EXACT) {
@@ -278,54 +292,50 @@ __global__ __launch_bounds__((BO / WO) * (BT / WT) * 64) void linear_kernel(LinA
                 const u32x4 q = *(const u32x4*)(lds + (at ^ (u * 32)) + down);
                 return i32x8{(int)q.x, (int)q.y, (int)q.z, (int)q.w, 0, 0, 0, 0};
             } else {  // chunks g and 2 + g of a unit's four
-                const u32x4 p = *(const u32x4*)(lds + (at ^ (u * 64)) + down);
-                const u32x4 q = *(const u32x4*)(lds + (at ^ (u * 64 + 32)) + down);
+                const u32x4 p = *(const u32x4*)(lds + at + down);
+                const u32x4 q = *(const u32x4*)(lds + (at ^ 32) + down);
                 return i32x8{(int)p.x, (int)p.y, (int)p.z, (int)p.w, (int)q.x, (int)q.y, (int)q.z, (int)q.w};
             }
         };
-        auto read_w = [&](int buf, int i) {
-            fw[i & 3] = operand(place_w, i / MT, buf * SW + (i % MT) * 32 * RW, std::integral_constant<int, FW>{});
+        // operands of step j of a turn
+        auto read_w = [&](auto J) {
+            constexpr int j = decltype(J)::value % STEPS, buf = j / ST % STAGES, i = j % ST;
+            fw[j & 3] = operand(place_w, i / MT, buf * SW + (i % MT) * 32 * RW, std::integral_constant<int, FW>{});
         };
-        auto read_x = [&](int buf, int u) {
+        auto read_x = [&](auto J) {
+            constexpr int j = decltype(J)::value % STEPS, buf = j / ST % STAGES, u = j % ST / MT;
 #pragma unroll
             for (int n = 0; n < NT; ++n)
-                fx[u & 1][n] = operand(place_x, u, buf * SX + n * 32 * RX, std::integral_constant<int, FX>{});
+                fx[j / MT & 1][n] = operand(place_x, u, buf * SX + n * 32 * RX, std::integral_constant<int, FX>{});
         };
-        // exponents of a stage, as they lie; before the stage's first step they are
-        // moved so that a lane's blocks g, 2 + g, ... are in the bytes that the instructions select
-        auto read_exponents = [&](int half, int in16, int set) {
-            const int at = half + in16 * SB;
+        // exponents of 128 codes: a word of each row, moved so that a lane's blocks (g and
+        // 2 + g) are in the bytes that the instructions select
+        auto read_exponents = [&](auto Q, int half) {
+            constexpr int q = decltype(Q)::value;
 #pragma unroll
-            for (int k = 0; k < SWORDS; ++k) {
+            for (int m = 0; m < MT; ++m) ew[q & 1][m] = *(const uint32_t*)(lds + scale_w + half + m * 512 + 4 * q);
 #pragma unroll
-                for (int m = 0; m < MT; ++m)
-                    ew[set][m][k] = *(const uint32_t*)(lds + scale_w + at + m * 512 + 4 * k);
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-                    ex[set][n][k] = *(const uint32_t*)(lds + scale_x + at + n * 512 + 4 * k);
-            }
+            for (int n = 0; n < NT; ++n) ex[q & 1][n] = *(const uint32_t*)(lds + scale_x + half + n * 512 + 4 * q);
         };
-        auto align_exponents = [&](int set) {
+        auto align_exponents = [&](auto Q) {
+            constexpr int q = decltype(Q)::value;
             if constexpr (!EXACT) {
 #pragma unroll
-                for (int k = 0; k < SWORDS; ++k) {
+                for (int m = 0; m < MT; ++m) ew[q & 1][m] >>= 8 * g;
 #pragma unroll
-                    for (int m = 0; m < MT; ++m) ew[set][m][k] >>= 8 * g;
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) ex[set][n][k] >>= 8 * g;
-                }
+                for (int n = 0; n < NT; ++n) ex[q & 1][n] >>= 8 * g;
             }
         };
-        auto multiply = [&](auto I, int set) {
-            constexpr int i = decltype(I)::value, u = i / MT, m = i % MT;
+        auto multiply = [&](auto J) {
+            constexpr int j = decltype(J)::value, m = j % MT, unit = j / MT;  // of the turn
+            constexpr int q = unit * UNIT / 128 & 1, in = unit * UNIT % 128 / UNIT;
             if constexpr (EXACT) {
                 if constexpr (m == 0) {
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        decode16<FX>(fx[u & 1][n], scale_of((ex[set][n][0] >> (8 * u)) & 255), dx[n]);
+                    for (int n = 0; n < NT; ++n) decode16<FX>(fx[unit & 1][n], scale_of((ex[q][n] >> (8 * in)) & 255), dx[n]);
                 }
                 bf16x8 dw[2];
-                decode16<FW>(fw[i & 3], scale_of((ew[set][m][0] >> (8 * u)) & 255), dw);
+                decode16<FW>(fw[j & 3], scale_of((ew[q][m] >> (8 * in)) & 255), dw);
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -335,60 +345,59 @@ __global__ __launch_bounds__((BO / WO) * (BT / WT) * 64) void linear_kernel(LinA
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
                     acc[m][n] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                        fw[i & 3], fx[u & 1][n], acc[m][n], FW == kE2m1 ? 4 : 0, FX == kE2m1 ? 4 : 0, (u & 1) * 2,
-                        (int)ew[set][m][u / 2], (u & 1) * 2, (int)ex[set][n][u / 2]);
+                        fw[j & 3], fx[unit & 1][n], acc[m][n], FW == kE2m1 ? 4 : 0, FX == kE2m1 ? 4 : 0, in * 2, (int)ew[q][m],
+                        in * 2, (int)ex[q][n]);
             }
+            // keeps the step's matrix instructions here: nothing else orders them among
+            // the loads and barriers of a turn
+#pragma unroll
+            for (int n = 0; n < NT; ++n) asm volatile("" : "+v"(acc[m][n]));
+            __builtin_amdgcn_sched_barrier(0);
         };
 
-        const int g0 = s0 / SPG, g1 = (s1 + SPG - 1) / SPG;  // turns
         __syncthreads();  // the last item's LDS is free
-        fetch(std::integral_constant<int, 0>{}, s0);
-        u32x4 e = exponents16(eb, eat, g0 * 16, esp, esize);
-        *(u32x4*)(lds + 2 * STAGE + tid * 16) = e;
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        fetch_exponents(g0, 0);
+        fetch(std::integral_constant<int, 0>{}, g0 * SPT);
+        fetch(std::integral_constant<int, 1>{}, g0 * SPT + 1);
+        fetch(std::integral_constant<int, 2>{}, g0 * SPT + 2);
+        wait_loads<2 * LOADS>();
         __syncthreads();
-        fetch(std::integral_constant<int, 1>{}, s0 + 1);
-        read_exponents(0, 0, 0);
-        read_x(0, 0);
-        read_w(0, 0);
-        if constexpr (AHEAD == 2) read_w(0, 1);
+        fetch(std::integral_constant<int, 3>{}, g0 * SPT + 3);
+        read_exponents(std::integral_constant<int, 0>{}, 0);
+        read_x(std::integral_constant<int, 0>{});
+        read_w(std::integral_constant<int, 0>{});
+        read_w(std::integral_constant<int, 1>{});
         int half = 0;  // where this turn's exponents lie
 #pragma unroll 1
         for (int turn = g0; turn < g1; ++turn) {
-            e = exponents16(eb, eat, (turn + 1 < g1 ? turn + 1 : turn) * 16, esp, esize);
+            // behind the last turn the last exponents once more, which no product takes
+            fetch_exponents(turn + 1 < g1 ? turn + 1 : turn, half ^ SCALES);
             auto steps = [&](auto self, auto J) {
-                constexpr int j = decltype(J)::value, in16 = j / ST, i = j % ST, buf = in16 & 1, set = in16 & 1;
-                if constexpr (j < SPG * ST) {
-                    if constexpr (i == 0) align_exponents(set);
-                    if constexpr (i == ST - 2) {
-                        if constexpr (AHEAD == 1) read_w(buf, ST - 1);
-                        if constexpr (in16 == SPG - 1) *(u32x4*)(lds + 2 * STAGE + (half ^ SCALES) + tid * 16) = e;
-                        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+                constexpr int j = decltype(J)::value, next = j + AHEAD;
+                if constexpr (j < STEPS) {
+                    if constexpr (next % ST == 0) {  // the first reads of a stage
+                        constexpr int s = next / ST, code = s % SPT * BK;
+                        wait_loads<2 * LOADS>();
                         __syncthreads();
-                        fetch(std::integral_constant<int, buf>{}, turn * SPG + in16 + 2);
-                        // behind the last stage what is read is not multiplied
-                        read_x(buf ^ 1, 0);
-                        if constexpr (AHEAD == 2) read_w(buf ^ 1, 0);
-                        read_exponents(in16 == SPG - 1 ? half ^ SCALES : half, (in16 + 1) % SPG, set ^ 1);
-                    } else if constexpr (i == ST - 1) {
-                        read_w(buf ^ 1, AHEAD - 1);
+                        fetch(std::integral_constant<int, (s + STAGES - 1) % STAGES>{}, turn * SPT + s + STAGES - 1);
+                        read_x(std::integral_constant<int, next>{});
+                        read_w(std::integral_constant<int, next>{});
+                        if constexpr (code % 128 == 0)
+                            read_exponents(std::integral_constant<int, code / 128>{}, s == SPT ? half ^ SCALES : half);
                     } else {
-                        read_w(buf, i + AHEAD);
-                        if constexpr (i % MT == 0 && i / MT + 1 < ST / MT) read_x(buf, i / MT + 1);
+                        if constexpr (next % MT == 0) read_x(std::integral_constant<int, next>{});
+                        read_w(std::integral_constant<int, next>{});
                     }
-                    multiply(std::integral_constant<int, i>{}, set);
-                    // keeps the step's matrix instructions here: nothing else orders
-                    // them among the loads and barriers of a turn
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) asm volatile("" : "+v"(acc[i % MT][n]));
-                    __builtin_amdgcn_sched_barrier(0);
+                    if constexpr (j * UNIT / MT % 128 == 0 && j % MT == 0)
+                        align_exponents(std::integral_constant<int, j / MT * UNIT / 128>{});
+                    multiply(J);
                     self(self, std::integral_constant<int, j + 1>{});
                 }
             };
             steps(steps, std::integral_constant<int, 0>{});
             half ^= SCALES;
         }
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the loads ahead, before their places are used
+        wait_loads<0>();  // the loads ahead, before their places are used
 
         // D: a lane has token lane & 31 and, four at a time, outputs (k / 4) * 8 + g * 4
         // on. The wave's results go through LDS, 32 tokens at a time (16-byte chunks
@@ -496,7 +505,7 @@ __global__ __launch_bounds__(512) void linear_few_kernel(LinArgs a) {
         f32x4 acc[NG];
 #pragma unroll
         for (int n = 0; n < NG; ++n) acc[n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        for (int64_t s = wave; s < a.steps; s += 8 * U) {
+        for (int64_t s = wave; s < a.turns * (kLinearGroup / 128); s += 8 * U) {
             Piece<FW, EXACT> fw[U];
             Piece<FX, EXACT> fx[U][NG];
 #pragma unroll
@@ -570,11 +579,12 @@ hipError_t run(LinArgs& a, const LinearCut& cut, hipStream_t stream) {
     const int tile = cut.form == 1 ? 128 : 256;
     a.tiles_o = (int)((a.out + tile - 1) / tile);
     a.tiles_t = (int)((a.rows + tile - 1) / tile);
-    const int64_t total = (int64_t)a.tiles_o * a.tiles_t * a.parts;
+    const int64_t total = (int64_t)a.tiles_o * a.tiles_t * a.parts, places = device_cu_count() * (cut.form == 1 ? 2 : 1);
+    const int64_t blocks = total < places ? total : places;  // blocks walk over the tiles
     if (cut.form == 1)
-        linear_kernel<FW, FX, EXACT, 128, 128, 64, 64><<<grid_for(total, 256), 256, 0, stream>>>(a);
+        linear_kernel<FW, FX, EXACT, 128, 128, 64, 64><<<grid_for(blocks, 256), 256, 0, stream>>>(a);
     else
-        linear_kernel<FW, FX, EXACT, 256, 256, 128, 64><<<grid_for(total, 512), 512, 0, stream>>>(a);
+        linear_kernel<FW, FX, EXACT, 256, 256, 128, 64><<<grid_for(blocks, 512), 512, 0, stream>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.parts == 1) return e;
     const int64_t items = (a.rows * ((a.out + 7) / 8) + kThreads - 1) / kThreads;
@@ -586,8 +596,8 @@ hipError_t run(LinArgs& a, const LinearCut& cut, hipStream_t stream) {
 
 hipError_t launch_linear(const Linear& f, hipStream_t stream) {
     const bool w4 = f.w_format == ZR_CKPT_E2M1, x4 = f.x_format == ZR_CKPT_E2M1;
-    const bool exact = f.z_dt == ZR_FP32 && !(w4 && x4);
-    const LinearCut cut = linear_cut(f.rows, f.out, f.in, w4 && x4, exact);
+    const LinearKind kind = w4 && x4 ? kLinearFour : (f.z_dt == ZR_FP32 ? kLinearDecoded : kLinearScaled);
+    const LinearCut cut = linear_cut(f.rows, f.out, f.in, kind);
     const int64_t pitch = ckpt_pitch(f.in);
     LinArgs a{};
     a.w = (const char*)f.w; a.x = (const char*)f.x;
@@ -598,9 +608,9 @@ hipError_t launch_linear(const Linear& f, hipStream_t stream) {
     a.bias = f.bias; a.z = f.z; a.part = (float*)f.workspace;
     a.rows = f.rows; a.out = f.out; a.ld_z = f.ld_z;
     a.bias_dt = f.bias_dt; a.z_dt = f.z_dt; a.accumulate = f.accumulate;
-    a.steps = cut.steps; a.share = cut.share; a.parts = cut.parts;
-    if (w4 && x4) return run<kE2m1, kE2m1, false>(a, cut, stream);
-    if (exact) {
+    a.turns = cut.turns; a.share = cut.share; a.parts = cut.parts;
+    if (kind == kLinearFour) return run<kE2m1, kE2m1, false>(a, cut, stream);
+    if (kind == kLinearDecoded) {
         if (w4) return run<kE2m1, kE4m3, true>(a, cut, stream);
         return x4 ? run<kE4m3, kE2m1, true>(a, cut, stream) : run<kE4m3, kE4m3, true>(a, cut, stream);
     }

@@ -96,15 +96,13 @@ __global__ __launch_bounds__(kThreads) void unpack_small_kernel(const char* ckpt
     }
 }
 
-// The transpose: a wave takes 64 columns of x and, in turn, kBlocksT blocks of 32
+// The transpose: a wave takes 64 columns of x and, in turn, `turns` blocks of 32
 // rows, a column to a lane. A lane holds a whole block, so its largest magnitude
 // needs no other lane; loads are 64 neighbouring elements of a row, and a lane
 // writes its blocks side by side.
-constexpr int kBlocksT = 4;
-
 template <int DT, int FMT>
 __global__ __launch_bounds__(kThreads) void pack_t_kernel(const void* x, int64_t ld, int64_t rows, int64_t cols, char* ckpt,
-                                                          int64_t tiles_c, int64_t tiles) {
+                                                          int turns, int64_t tiles_c, int64_t tiles) {
     const int64_t blocks = ckpt_pitch(rows) / kCkptBlock;  // of an output row
     const int64_t codes = code_bytes<FMT>(rows);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -112,8 +110,8 @@ __global__ __launch_bounds__(kThreads) void pack_t_kernel(const void* x, int64_t
         const int64_t tr = t / tiles_c, c = ((t - tr * tiles_c) * (kThreads / 64) + wave) * 64 + lane;
         if (c >= cols) continue;
 #pragma unroll 1
-        for (int b = 0; b < kBlocksT; ++b) {
-            const int64_t block = tr * kBlocksT + b, row = block * kCkptBlock;
+        for (int b = 0; b < turns; ++b) {
+            const int64_t block = tr * turns + b, row = block * kCkptBlock;
             if (block >= blocks) break;
             float f[kCkptBlock];
 #pragma unroll
@@ -150,15 +148,17 @@ __global__ __launch_bounds__(kThreads) void pack_t_kernel(const void* x, int64_t
 
 template <int DT>
 void pack_t_run(const void* x, int64_t ld, int64_t rows, int64_t cols, char* ckpt, zr_dtype fmt, hipStream_t stream) {
-    const int64_t tiles_c = (cols + kThreads - 1) / kThreads, per = kBlocksT * kCkptBlock;
-    const int64_t tiles = tiles_c * ((rows + per - 1) / per);
+    const int64_t tiles_c = (cols + kThreads - 1) / kThreads, blocks = (rows + kCkptBlock - 1) / kCkptBlock;
+    // four blocks to a lane (a line of codes) where that leaves enough for the chip
+    const int turns = tiles_c * blocks >= 4096 ? 4 : 1;
+    const int64_t tiles = tiles_c * ((blocks + turns - 1) / turns);
     const dim3 grid(grid_for(tiles, kThreads)), block(kThreads);
     if (fmt == ZR_CKPT_E2M1)
-        pack_t_kernel<DT, kE2m1><<<grid, block, 0, stream>>>(x, ld, rows, cols, ckpt, tiles_c, tiles);
+        pack_t_kernel<DT, kE2m1><<<grid, block, 0, stream>>>(x, ld, rows, cols, ckpt, turns, tiles_c, tiles);
     else if (fmt == ZR_CKPT_E4M3)
-        pack_t_kernel<DT, kE4m3><<<grid, block, 0, stream>>>(x, ld, rows, cols, ckpt, tiles_c, tiles);
+        pack_t_kernel<DT, kE4m3><<<grid, block, 0, stream>>>(x, ld, rows, cols, ckpt, turns, tiles_c, tiles);
     else
-        pack_t_kernel<DT, kInt8><<<grid, block, 0, stream>>>(x, ld, rows, cols, ckpt, tiles_c, tiles);
+        pack_t_kernel<DT, kInt8><<<grid, block, 0, stream>>>(x, ld, rows, cols, ckpt, turns, tiles_c, tiles);
 }
 
 int64_t tiles_of(int64_t rows, int64_t cols) { return (rows * (ckpt_pitch(cols) / 8) + kTile - 1) / kTile; }

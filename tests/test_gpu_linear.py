@@ -98,7 +98,7 @@ def check(rows, inn, out, xf, wf, zd, rng, bias=None, accumulate=False, gap=0, s
 PAIRS = [("e4m3", "e4m3"), ("e4m3", "e2m1"), ("e2m1", "e4m3"), ("e2m1", "e2m1")]
 # few rows (groups of 16 and all 64), their borders, one tile and its borders, split columns, several tiles
 SHAPES = [(1, 1, 1), (1, 4096, 300), (2, 33, 17), (15, 100, 16), (16, 128, 15), (17, 129, 40), (33, 1000, 31), (64, 545, 100),
-          (65, 512, 128), (128, 513, 127), (129, 31, 129), (100, 4100, 60), (200, 2048, 257), (300, 777, 1000), (1, 20000, 9)]
+          (65, 512, 128), (128, 513, 127), (129, 31, 129), (100, 4100, 60), (40, 600, 9000), (200, 2048, 257), (300, 777, 1000), (1, 20000, 9)]
 
 
 @pytest.mark.parametrize("zd", ["bf16", "fp32"])
