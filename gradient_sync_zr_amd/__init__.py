@@ -36,6 +36,16 @@ streams default to torch's current stream):
 * ``zr_ckpt_pack``, ``zr_ckpt_unpack``, ``zr_ckpt_wgrad``: 8-bit activation
   checkpoints (uint8 buffers of ``zr_ckpt_bytes(rows, cols)``), and a linear
   layer's weight gradient from the checkpoint of its input.
+* ``zr_rmsnorm_fwd(x, rows, cols, y, weight, residual=..., h=..., ...)`` and
+  ``zr_rmsnorm_bwd(dy, h, rows, cols, rstd, weight, dx=..., dweight=...)``: RMS norm
+  with the residual's addition; its output may be packed in 8 bits.
+* ``zr_ckpt_linear(x, w, rows, in_cols, out_cols, z, bias=...)``: a linear layer on
+  packed operands (e4m3, or 4-bit ``ZR_CKPT_E2M1`` blocks of
+  ``zr_ckpt_format_bytes``); ``zr_ckpt_pack_t`` packs a transpose.
+* ``zr_grad_norm(grads, numels, norm, coef, max_norm=...)``,
+  ``zr_grad_scale(grads, numels, coef)`` and ``zr_adamw(grads, numels, params,
+  exp_avg, exp_avg_sq, step, lr, shards=..., coef=...)``: the global gradient norm,
+  clipping and AdamW over lists of tensors; ``tensor_table`` checks a list once.
 * Host only: ``zr_pf_plan``, ``zr_plan_buckets``, ``zr_cost_*``.
 
 Example: eight ranks' bf16 gradients of N elements reduced into fp32
@@ -1049,7 +1059,7 @@ class TensorTable:
     def __init__(self, xs: Sequence, numels, dtype=None, name: str = "tensors"):
         at, code, device = _list(xs, numels, dtype, name)
         self.table, self.dtype, self.device = _table(at), code, device
-        self.numels, self._keep = _sizes(numels), list(xs)
+        self._bytes, self._keep = bytes(_sizes(numels)), list(xs)
         self._n = len(at)
 
     def __len__(self):
@@ -1095,10 +1105,11 @@ def _list(xs, numels, dtype, name):
     return at, code, device
 
 
-def _many(xs, numels, dtype, name, gpus):
-    """(C table, dtype) of one list of a call; its GPU joins `gpus`."""
+def _many(xs, numels, sizes, dtype, name, gpus):
+    """(C table, dtype) of one list of a call; its GPU joins `gpus`. sizes: the C
+    array of numels."""
     if xs.__class__ is TensorTable:
-        if len(xs) != len(numels) or (xs.numels is not numels and list(xs.numels)[:len(xs)] != list(numels)[:len(xs)]):
+        if xs._n != len(numels) or xs._bytes != bytes(sizes):
             raise ValueError(f"{name} is a table of other sizes")
         if dtype is not None and _dtype(dtype) != xs.dtype:
             raise ValueError(f"{name} is not what its dtype argument says")
@@ -1111,16 +1122,15 @@ def _many(xs, numels, dtype, name, gpus):
 
 def _run_on_gpus(stream, gpus, *xs) -> int:
     """_run_on for lists on these GPUs (None: addresses) and more tensors."""
-    on = _run_on(stream, *xs)
-    here = {g for g in gpus if g is not None}
-    if here:
-        if _raw_stream is None:
-            _find_lookups()
-        now = _current_gpu()
-        if here != {now}:
-            raise ValueError(f"the tensors are on GPU {sorted(here)}, the current one is {now}: make theirs current, "
+    if _raw_stream is None:
+        _find_lookups()
+    for g in gpus:
+        if g is not None and g != _current_gpu():
+            raise ValueError(f"the tensors are on GPU {g}, the current one is {_current_gpu()}: make theirs current, "
                              "and its stream")
-    return on
+        if g is not None and stream is not None and getattr(getattr(stream, "device", None), "index", g) != g:
+            raise ValueError(f"the tensors are on GPU {g}, the stream is not")
+    return _run_on(stream, *xs)
 
 
 def _scalar(x, name):
@@ -1138,20 +1148,20 @@ def zr_grad_norm(grads, numels: Sequence[int], norm=None, coef=None, max_norm: f
     the GPU), and scale * min(1, max_norm / norm) into `coef`. grads: a list of
     tensors (or addresses, of `dtype`) of numels elements, or a
     ``tensor_table``."""
-    gpus = []
-    t, dt = _many(grads, numels, dtype, "grads", gpus)
+    gpus, sizes = [], _sizes(numels)
+    t, dt = _many(grads, numels, sizes, dtype, "grads", gpus)
     ws, wsb = _workspace(workspace)
-    _check(lib().zr_grad_norm(len(numels), t, _sizes(numels), dt, scale, max_norm, _scalar(norm, "norm"),
+    _check(lib().zr_grad_norm(len(numels), t, sizes, dt, scale, max_norm, _scalar(norm, "norm"),
                               _scalar(coef, "coef"), ws, wsb, _run_on_gpus(stream, gpus, norm, coef, workspace)))
 
 
 def zr_grad_scale(grads, numels: Sequence[int], coef, outs=None, dtype=None, out_dtype=None, stream=None) -> None:
     """coef (one fp32 on the GPU) times every tensor of `grads`, into `outs` or
     in place."""
-    gpus = []
-    t, dt = _many(grads, numels, dtype, "grads", gpus)
-    o, odt = (None, dt) if outs is None else _many(outs, numels, out_dtype, "outs", gpus)
-    _check(lib().zr_grad_scale(len(numels), t, _sizes(numels), dt, o, odt, _scalar(coef, "coef"),
+    gpus, sizes = [], _sizes(numels)
+    t, dt = _many(grads, numels, sizes, dtype, "grads", gpus)
+    o, odt = (None, dt) if outs is None else _many(outs, numels, sizes, out_dtype, "outs", gpus)
+    _check(lib().zr_grad_scale(len(numels), t, sizes, dt, o, odt, _scalar(coef, "coef"),
                                _run_on_gpus(stream, gpus, coef)))
 
 
@@ -1162,10 +1172,10 @@ def zr_adamw(grads, numels: Sequence[int], params, exp_avg, exp_avg_sq, step: in
     (coef: one fp32 on the GPU, of zr_grad_norm; the update is left out where it
     is not finite); shards, if given, receive the params in bf16. Lists as in
     zr_grad_norm; `dtype` is that of grads given as addresses."""
-    gpus = []
-    t, dt = _many(grads, numels, dtype, "grads", gpus)
-    p, m, v = (_many(xs, numels, ZR_FP32, name, gpus)[0]
+    gpus, sizes = [], _sizes(numels)
+    t, dt = _many(grads, numels, sizes, dtype, "grads", gpus)
+    p, m, v = (_many(xs, numels, sizes, ZR_FP32, name, gpus)[0]
                for xs, name in ((params, "params"), (exp_avg, "exp_avg"), (exp_avg_sq, "exp_avg_sq")))
-    s = None if shards is None else _many(shards, numels, ZR_BF16, "shards", gpus)[0]
-    _check(lib().zr_adamw(len(numels), t, dt, _sizes(numels), p, m, v, s, lr, beta1, beta2, eps, weight_decay, step,
+    s = None if shards is None else _many(shards, numels, sizes, ZR_BF16, "shards", gpus)[0]
+    _check(lib().zr_adamw(len(numels), t, dt, sizes, p, m, v, s, lr, beta1, beta2, eps, weight_decay, step,
                           _scalar(coef, "coef"), _run_on_gpus(stream, gpus, coef)))

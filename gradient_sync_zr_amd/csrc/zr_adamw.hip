@@ -75,7 +75,7 @@ hipError_t launch_adamw(const AdamW& f, hipStream_t stream) {
     a.inv2 = (float)(1.0 / (1.0 - __builtin_pow(f.beta2, (double)f.step)));
     a.eps = (float)f.eps;
     AdamTable m;
-    for (int next = multi_fill(&m, 0, f.n, lists, f.numels); m.count > 0; next = multi_fill(&m, next, f.n, lists, f.numels)) {
+    for (int next = multi_fill<kMultiTile>(&m, 0, f.n, lists, f.numels); m.count > 0; next = multi_fill<kMultiTile>(&m, next, f.n, lists, f.numels)) {
         const int grid = grid_for(m.tile0[m.count], kThreads);
         if (f.grad_dt == ZR_BF16)
             adamw_kernel<uint16_t><<<grid, kThreads, 0, stream>>>(m, a, f.shards != nullptr);

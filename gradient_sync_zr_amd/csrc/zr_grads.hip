@@ -8,6 +8,7 @@
 // single block adds them in order, so the result does not change from run to run.
 #include <hip/hip_runtime.h>
 
+#include "zr_ckpt.hpp"
 #include "zr_multi.hpp"
 
 namespace zr {
@@ -45,36 +46,65 @@ __device__ __forceinline__ void put_norm(const NormOut& o, double sum) {
     if (o.coef) *o.coef = (float)coef;
 }
 
-// The squares of this thread's share of the launch's tiles.
+// Vectors of a lane in a tile: of 16 bytes (16 of 4 elements, or 8 of 8).
 template <typename T>
+constexpr int kNormVecs = kNormTile / kThreads / (16 / (int)sizeof(T));
+
+// The squares of this thread's share of the launch's tiles, all of a tile's loads in
+// front. NT: past the caches.
+template <typename T, bool NT>
 __device__ __forceinline__ double squares(const NormTable& m, int first, int step) {
+    constexpr int E = 16 / (int)sizeof(T), V = kNormVecs<T>;
     double s[4] = {0.0, 0.0, 0.0, 0.0};
     int slot = 0;
     const int tiles = m.tile0[m.count];
     for (int t = first; t < tiles; t += step) {
         slot = multi_slot(m, slot, t);
-        const T* p = (const T*)m.p[0][slot];
-        const int64_t begin = (int64_t)(t - m.tile0[slot]) * kMultiTile, left = m.n[slot] - begin;
-        const int c = threadIdx.x % kThreads * 4;
-        p += begin + c;
-        float f[kMultiQuads][4];
+        const int64_t begin = (int64_t)(t - m.tile0[slot]) * kNormTile, left = m.n[slot] - begin;
+        const int c = (int)(threadIdx.x % kThreads) * E;
+        const T* p = (const T*)m.p[0][slot] + begin + c;
+        auto add = [&](const float f[E]) {
 #pragma unroll
-        for (int k = 0; k < kMultiQuads; ++k) {
-            const int64_t l = left - c - k * kThreads * 4;
-            load_quad4<T, false>(p + k * kThreads * 4, l > 4 ? 4 : (int)l, f[k]);
+            for (int e = 0; e < E; ++e) s[e & 3] = __builtin_fma((double)f[e], (double)f[e], s[e & 3]);
+        };
+        if (left >= kNormTile) {  // the same for the block
+            u32x4 raw[V];
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                if constexpr (sizeof(T) == 2)
+                    raw[k] = ld16<NT>((const uint16_t*)p + k * kThreads * E);
+                else
+                    raw[k] = __builtin_bit_cast(u32x4, ld32<NT>((const float*)p + k * kThreads * E));
+            }
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                float f[E];
+                if constexpr (sizeof(T) == 2) {
+                    widen8(Raw8<kBf16>{raw[k]}, f);
+                } else {
+                    const f32x4 v = __builtin_bit_cast(f32x4, raw[k]);
+                    f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+                }
+                add(f);
+            }
+        } else {
+#pragma unroll 1
+            for (int k = 0; k < V; ++k) {
+                const int64_t l = left - c - (int64_t)k * kThreads * E;
+                float f[E];
+#pragma unroll
+                for (int e = 0; e < E; ++e) f[e] = e < l ? load_elem(p + k * kThreads * E + e) : 0.0f;
+                add(f);
+            }
         }
-#pragma unroll
-        for (int k = 0; k < kMultiQuads; ++k)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[e] = __builtin_fma((double)f[k][e], (double)f[k][e], s[e]);
     }
     return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
-template <typename T>
+template <typename T, bool NT>
 __global__ __launch_bounds__(kThreads) void norm_kernel(NormTable m, double* part) {
     __shared__ double red[kThreads / 64];
-    const double s = block_sum<kThreads>(squares<T>(m, blockIdx.x, gridDim.x), red);
+    const double s = block_sum<kThreads>(squares<T, NT>(m, blockIdx.x, gridDim.x), red);
     if (threadIdx.x == 0) part[blockIdx.x] = s;
 }
 
@@ -82,7 +112,7 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(NormTable m, double* par
 template <typename T>
 __global__ __launch_bounds__(1024) void norm_one_kernel(NormTable m, NormOut o) {
     __shared__ double red[16];
-    const double s = block_sum<1024>(squares<T>(m, threadIdx.x / kThreads, 1024 / kThreads), red);
+    const double s = block_sum<1024>(squares<T, false>(m, threadIdx.x / kThreads, 1024 / kThreads), red);
     if (threadIdx.x == 0) put_norm(o, s);
 }
 
@@ -129,9 +159,13 @@ hipError_t launch_grad_norm(const GradNorm& f, hipStream_t stream) {
     const void* const* const lists[1] = {f.grads};
     const NormOut o{f.norm, f.coef, (double)f.scale, (double)f.max_norm};
     double* const part = (double*)f.workspace;
+    // what the caches hold stays there for the call that scales it or takes the step
+    int64_t total = 0;
+    for (int i = 0; i < f.n; ++i) total += f.numels[i];
+    const bool far = total * (f.dt == ZR_BF16 ? 2 : 4) > kCachedBytes;
     NormTable m;
-    int next = multi_fill(&m, 0, f.n, lists, f.numels), parts = 0;
-    if (next == f.n && m.tile0[m.count] <= kNormOneTiles) {
+    int next = multi_fill<kNormTile>(&m, 0, f.n, lists, f.numels), parts = 0;
+    if (next == f.n && m.tile0[m.count] <= 4 && total <= kNormOneElems) {
         if (f.dt == ZR_BF16)
             norm_one_kernel<uint16_t><<<1, 1024, 0, stream>>>(m, o);
         else
@@ -141,14 +175,18 @@ hipError_t launch_grad_norm(const GradNorm& f, hipStream_t stream) {
     while (m.count > 0) {
         const int64_t tiles = m.tile0[m.count];
         const int grid = grid_for(tiles < kNormBlocks ? tiles : kNormBlocks, kThreads);
-        if (f.dt == ZR_BF16)
-            norm_kernel<uint16_t><<<grid, kThreads, 0, stream>>>(m, part + parts);
+        if (f.dt == ZR_BF16 && far)
+            norm_kernel<uint16_t, true><<<grid, kThreads, 0, stream>>>(m, part + parts);
+        else if (f.dt == ZR_BF16)
+            norm_kernel<uint16_t, false><<<grid, kThreads, 0, stream>>>(m, part + parts);
+        else if (far)
+            norm_kernel<float, true><<<grid, kThreads, 0, stream>>>(m, part + parts);
         else
-            norm_kernel<float><<<grid, kThreads, 0, stream>>>(m, part + parts);
+            norm_kernel<float, false><<<grid, kThreads, 0, stream>>>(m, part + parts);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         parts += grid;
-        next = multi_fill(&m, next, f.n, lists, f.numels);
+        next = multi_fill<kNormTile>(&m, next, f.n, lists, f.numels);
     }
     norm_join_kernel<<<1, 1024, 0, stream>>>(part, parts, o);
     return hipGetLastError();
@@ -158,7 +196,7 @@ hipError_t launch_grad_scale(const GradScale& f, hipStream_t stream) {
     const bool in_place = !f.outs;
     const void* const* const lists[2] = {f.grads, in_place ? f.grads : (const void* const*)f.outs};
     ScaleTable m;
-    for (int next = multi_fill(&m, 0, f.n, lists, f.numels); m.count > 0; next = multi_fill(&m, next, f.n, lists, f.numels)) {
+    for (int next = multi_fill<kMultiTile>(&m, 0, f.n, lists, f.numels); m.count > 0; next = multi_fill<kMultiTile>(&m, next, f.n, lists, f.numels)) {
         const int grid = grid_for(m.tile0[m.count], kThreads);
         if (f.dt == ZR_BF16 && f.out_dt == ZR_BF16)
             scale_kernel<uint16_t, uint16_t><<<grid, kThreads, 0, stream>>>(m, f.coef, in_place);

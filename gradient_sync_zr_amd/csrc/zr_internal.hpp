@@ -323,7 +323,9 @@ ZR_KERNELS hipError_t launch_ckpt_wgrad(const Wgrad& w, hipStream_t stream);
 // arguments (4 KiB at most), and a longer list goes out as several.
 constexpr int kNormPer = 128, kScalePer = 128, kAdamPer = 64;
 constexpr int kNormBlocks = 2048;  // partial sums of a launch at most
-constexpr int kNormOneTiles = 4;   // tiles that one block takes alone, without a join
+constexpr int kNormTile = 8192;    // elements
+constexpr int kNormOneElems = 16384;  // in as many tiles as one block has groups of lanes: taken by it alone
+constexpr int64_t kCachedBytes = 256ll << 20;  // of the last cache
 
 struct GradNorm {
     int n;

@@ -24,9 +24,9 @@ struct Multi {
     int32_t count;
 };
 
-// Fills `m` with the tensors from `first` on (lists[k] may be null); those of no
-// elements are stepped over. Returns the first tensor that is left.
-template <int NP, int PER>
+// Fills `m` with the tensors from `first` on (lists[k] may be null) in tiles of TILE
+// elements; tensors of no elements are stepped over. Returns the first that is left.
+template <int TILE, int NP, int PER>
 inline int multi_fill(Multi<NP, PER>* m, int first, int n, const void* const* const (&lists)[NP], const int64_t* numels) {
     m->count = 0;
     m->tile0[0] = 0;
@@ -36,7 +36,7 @@ inline int multi_fill(Multi<NP, PER>* m, int first, int n, const void* const* co
         const int at = m->count++;
         for (int k = 0; k < NP; ++k) m->p[k][at] = lists[k] ? lists[k][i] : nullptr;
         m->n[at] = numels[i];
-        m->tile0[at + 1] = m->tile0[at] + (int32_t)((numels[i] + kMultiTile - 1) / kMultiTile);
+        m->tile0[at + 1] = m->tile0[at] + (int32_t)((numels[i] + TILE - 1) / TILE);
     }
     while (i < n && numels[i] == 0) ++i;
     return i;

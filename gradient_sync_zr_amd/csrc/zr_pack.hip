@@ -113,16 +113,20 @@ __global__ __launch_bounds__(kThreads) void pack_t_kernel(const void* x, int64_t
         for (int b = 0; b < turns; ++b) {
             const int64_t block = tr * turns + b, row = block * kCkptBlock;
             if (block >= blocks) break;
+            // rows behind the last are read from it, and are zeros
             float f[kCkptBlock];
+            const int have = rows - row < kCkptBlock ? (int)(rows - row) : kCkptBlock;
 #pragma unroll
             for (int k = 0; k < kCkptBlock; ++k) {
-                f[k] = 0.0f;
-                if (row + k < rows) {
-                    if constexpr (DT == kBf16)
-                        f[k] = load_elem((const uint16_t*)x + (row + k) * ld + c);
-                    else
-                        f[k] = load_elem((const float*)x + (row + k) * ld + c);
-                }
+                const int64_t at = (row + (k < have ? k : have - 1)) * ld + c;
+                if constexpr (DT == kBf16)
+                    f[k] = load_elem((const uint16_t*)x + at);
+                else
+                    f[k] = load_elem((const float*)x + at);
+            }
+            if (have < kCkptBlock) {
+#pragma unroll
+                for (int k = 0; k < kCkptBlock; ++k) f[k] = k < have ? f[k] : 0.0f;
             }
             uint32_t amax = 0;
 #pragma unroll

@@ -16,6 +16,10 @@ reducer does with the C ABI, one step at a time.
   writes the weight gradients into the rank's flat gradient, where
   :class:`Zero2GradSync` takes them (its ``produce`` hook is the place to call
   the backward pass from).
+* :class:`PackedNormLinear` - the same place in a layer with an RMS norm, whose
+  products run on packed activations and packed weights too.
+* :class:`ClipAdamW` - the step behind the reduction: the partitions' global
+  norm, clipping, AdamW, and the bf16 shards that :class:`Zero3Gather` gathers.
 
 All tensors are torch CUDA tensors used only as device memory; every
 computation happens in libzr's kernels.
@@ -24,9 +28,11 @@ from __future__ import annotations
 
 from typing import Callable, List, Optional, Sequence
 
-from . import (ZR_BF16, ZR_CKPT_E4M3, ZR_FP32, ZR_ORDER_RING, Sched, zr_all_gather, zr_ckpt_bytes,
-               zr_ckpt_wgrad, zr_ckpt_wgrad_workspace_bytes, zr_layernorm_bwd, zr_layernorm_fwd,
-               zr_layernorm_workspace_bytes, zr_plan_buckets, _dtype)
+from . import (ZR_BF16, ZR_CKPT_E4M3, ZR_FP32, ZR_ORDER_RING, Sched, tensor_table, zr_adamw, zr_all_gather,
+               zr_ckpt_bytes, zr_ckpt_format_bytes, zr_ckpt_linear, zr_ckpt_linear_workspace_bytes, zr_ckpt_pack,
+               zr_ckpt_pack_t, zr_ckpt_wgrad, zr_ckpt_wgrad_workspace_bytes, zr_grad_norm,
+               zr_grad_norm_workspace_bytes, zr_layernorm_bwd, zr_layernorm_fwd, zr_layernorm_workspace_bytes,
+               zr_plan_buckets, zr_rmsnorm_bwd, zr_rmsnorm_fwd, zr_rmsnorm_workspace_bytes, _dtype)
 
 
 def ceil_div(a: int, b: int) -> int:
@@ -244,3 +250,143 @@ class CkptNormLinear:
 
     def _workspace(self):
         return self.scratch[:self._ws_bytes]
+
+
+class PackedNormLinear:
+    """RMS norm of a rank's residual stream (rows x cols), and the linear layer
+    that reads it (out_cols x cols), on packed operands: activations and output
+    gradients in e4m3, the weight in `weight_format` (e4m3 or e2m1), packed once
+    per update for both directions.
+
+    flat_grad : the rank's flat gradient; the layer's part of it starts at
+                element `offset` and holds, in order, the norm's weight (cols),
+                the linear layer's weight (out_cols x cols) and, with `bias`, its
+                bias (out_cols): `numel` elements
+    scratch   : a uint8 tensor of `scratch_bytes` elements, the calls' workspace;
+                layers that run one after another on a stream may share it, others
+                must not
+
+        pack_weight(W)                                   after every update of W
+        forward(x, norm_weight, z, residual=r, h=h)      z = norm(x + r) W^T + b
+        backward(dz, norm_weight, dx)                    the flat gradient, and dx
+
+    dx is the gradient of h = x + r, so of x and of the residual; with add_dx it is
+    added to what passed by the norm. h is kept as an 8-bit checkpoint: h, x and the
+    residual are not needed after the forward pass. dW takes dz as it is, dx takes
+    it packed.
+
+    The layer's buffers belong to the stream that is current when it is made: it
+    has to outlive what its methods enqueue on another.
+    """
+
+    def __init__(self, flat_grad, offset: int, rows: int, cols: int, out_cols: int, scratch=None,
+                 weight_format: int = ZR_CKPT_E4M3, eps: float = 1e-5, bias: bool = True):
+        import torch
+        self.rows, self.cols, self.out_cols = rows, cols, out_cols
+        self.weight_format, self.eps = weight_format, eps
+        sizes = [cols, out_cols * cols] + ([out_cols] if bias else [])
+        self.numel = sum(sizes)
+        if offset < 0 or offset + self.numel > flat_grad.numel():
+            raise ValueError(f"the flat gradient holds {flat_grad.numel()} elements, the layer needs {self.numel} "
+                             f"at {offset}")
+        parts = flat_grad[offset:offset + self.numel].split(sizes)
+        self.dw_norm = parts[0]
+        self.dw = parts[1].view(out_cols, cols)
+        self.db = parts[2] if bias else None
+        self.scratch_bytes = max(1, zr_rmsnorm_workspace_bytes(rows, cols),
+                                 zr_ckpt_linear_workspace_bytes(rows, cols, out_cols),
+                                 zr_ckpt_linear_workspace_bytes(rows, out_cols, cols),
+                                 zr_ckpt_wgrad_workspace_bytes(rows, out_cols, cols))
+        dev = flat_grad.device
+
+        def buffer(r, c, fmt):
+            return torch.empty(zr_ckpt_format_bytes(r, c, fmt), dtype=torch.uint8, device=dev)
+
+        if scratch is None:
+            scratch = torch.empty(self.scratch_bytes, dtype=torch.uint8, device=dev)
+        if scratch.numel() < self.scratch_bytes:
+            raise ValueError(f"scratch holds {scratch.numel()} bytes, needs {self.scratch_bytes}")
+        self.scratch = scratch[:self.scratch_bytes]
+        self.w, self.w_t = buffer(out_cols, cols, weight_format), buffer(cols, out_cols, weight_format)
+        self.ckpt_h, self.ckpt_y = buffer(rows, cols, ZR_CKPT_E4M3), buffer(rows, cols, ZR_CKPT_E4M3)
+        self.dz = buffer(rows, out_cols, ZR_CKPT_E4M3)
+        self.dy = torch.empty(rows, cols, dtype=torch.bfloat16, device=dev)
+        self.rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+        self._packed = self._ran = False
+
+    def pack_weight(self, weight, stream=None) -> None:
+        """weight (out_cols x cols, bf16 or fp32) and its transpose, packed."""
+        zr_ckpt_pack(weight, self.out_cols, self.cols, self.w, format=self.weight_format, stream=stream)
+        zr_ckpt_pack_t(weight, self.out_cols, self.cols, self.w_t, format=self.weight_format, stream=stream)
+        self._packed = True
+
+    def forward(self, x, norm_weight, z, residual=None, h=None, bias=None, stream=None) -> None:
+        """z (rows x out_cols) of x and the residual, whose sum goes to h."""
+        if not self._packed:
+            raise ValueError("forward before pack_weight")
+        zr_rmsnorm_fwd(x, self.rows, self.cols, None, norm_weight, eps=self.eps, residual=residual, h=h,
+                       rstd=self.rstd, ckpt_h=self.ckpt_h, ckpt_y=self.ckpt_y, stream=stream)
+        zr_ckpt_linear(self.ckpt_y, self.w, self.rows, self.cols, self.out_cols, z, bias=bias,
+                       w_format=self.weight_format, workspace=self.scratch, stream=stream)
+        self._ran = True
+
+    def backward(self, dz, norm_weight, dx=None, accumulate: bool = False, add_dx: bool = False,
+                 stream=None) -> None:
+        """The layer's gradients from its output's, dz (rows x out_cols): the
+        weights' and the bias's into the flat gradient (added to with accumulate: a
+        later micro-step), the input's into dx (added to with add_dx)."""
+        if not self._ran:
+            raise ValueError("backward before forward")
+        rows, cols, out = self.rows, self.cols, self.out_cols
+        zr_ckpt_wgrad(dz, self.ckpt_y, rows, out, cols, self.dw, dbias=self.db, accumulate=accumulate,
+                      workspace=self.scratch, stream=stream)
+        zr_ckpt_pack(dz, rows, out, self.dz, stream=stream)
+        zr_ckpt_linear(self.dz, self.w_t, rows, out, cols, self.dy, w_format=self.weight_format,
+                       workspace=self.scratch, stream=stream)
+        zr_rmsnorm_bwd(self.dy, self.ckpt_h, rows, cols, self.rstd, norm_weight, dx=dx, dweight=self.dw_norm,
+                       accumulate=accumulate, add_dx=add_dx, workspace=self.scratch, h_dtype=ZR_CKPT_E4M3,
+                       stream=stream)
+
+
+class ClipAdamW:
+    """The optimizer step of K ranks' partitions: their gradients' global norm,
+    clipped to max_norm, and AdamW, without a pass for the clipping and without the
+    host waiting for the norm.
+
+    grads      : the ranks' fp32 partitions as the reduction leaves them (or any
+                 list of gradients, bf16 or fp32)
+    params     : fp32 parameters of the same sizes, with exp_avg and exp_avg_sq
+    shards     : bf16 copies of the parameters, written with them (or None)
+    scale      : the gradients stand for scale * grads (1 / micro-steps, 1 / loss
+                 scale)
+
+    step() counts the updates that it enqueues. `norm` and `coef` hold the last
+    step's; where the gradients are not finite, coef is not, and the step leaves the
+    parameters as they are (it counts all the same). The buffers keep their
+    addresses; on another stream than the one that is current when it is made, the
+    object has to outlive what step() enqueues.
+    """
+
+    def __init__(self, grads: Sequence, params: Sequence, exp_avg: Sequence, exp_avg_sq: Sequence,
+                 shards: Optional[Sequence] = None, lr: float = 1e-3, beta1: float = 0.9, beta2: float = 0.999,
+                 eps: float = 1e-8, weight_decay: float = 0.01, max_norm: float = 1.0, scale: float = 1.0):
+        import torch
+        self.numels = [g.numel() for g in grads]
+        self._tables = [tensor_table(xs, self.numels) for xs in (grads, params, exp_avg, exp_avg_sq)]
+        self._shards = None if shards is None else tensor_table(shards, self.numels)
+        self.lr, self.beta1, self.beta2, self.eps, self.weight_decay = lr, beta1, beta2, eps, weight_decay
+        self.max_norm, self.scale = max_norm, scale
+        dev = params[0].device
+        self.norm, self.coef = torch.zeros(1, device=dev), torch.zeros(1, device=dev)
+        self._workspace = torch.empty(zr_grad_norm_workspace_bytes(len(self.numels)), dtype=torch.uint8, device=dev)
+        self.steps = 0
+
+    def step(self, lr: Optional[float] = None, stream=None) -> None:
+        """One update, at rate lr (default: the object's)."""
+        g, p, m, v = self._tables
+        zr_grad_norm(g, self.numels, self.norm, self.coef, max_norm=self.max_norm, scale=self.scale,
+                     workspace=self._workspace, stream=stream)
+        self.steps += 1
+        zr_adamw(g, self.numels, p, m, v, self.steps, self.lr if lr is None else lr, beta1=self.beta1,
+                 beta2=self.beta2, eps=self.eps, weight_decay=self.weight_decay, shards=self._shards,
+                 coef=self.coef, stream=stream)

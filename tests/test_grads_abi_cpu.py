@@ -132,7 +132,7 @@ def test_tensors_are_checked():
 
 
 def test_launches():
-    """One block up to four tiles; a block per tile and a join beyond; a launch per 128 (64) tensors."""
+    """One block up to 16384 elements in four tiles; a block per tile and a join beyond; a launch per 128 (64) tensors."""
     launches([])  # builds the library that writes launches down
     code = """
 import ctypes, json, sys
@@ -168,10 +168,11 @@ print(json.dumps(out))
     name = lambda s: next(k for k in ("norm_one", "norm_join", "norm_kernel", "scale_kernel", "adamw_kernel") if k in s)  # noqa: E731
     got = [[(name(s), b, t) for s, b, t in g] for g in got]
     one, join = ("norm_one", 1, 1024), ("norm_join", 1, 1024)
+    # (tiles of the norm have 8192 elements, of the others 4096)
     assert got[:4] == [[one]] * 4
     assert got[4] == [("norm_kernel", 5, 256), join]
     assert got[5] == [("norm_kernel", 2048, 256), join]
-    assert got[6] == [("norm_kernel", 256, 256), ("norm_kernel", 2, 256), join]
+    assert got[6] == [("norm_kernel", 128, 256), ("norm_kernel", 1, 256), join]
     assert got[7] == [("scale_kernel", 2, 256)] and got[8] == [("scale_kernel", 128, 256)]
     assert got[9] == [("scale_kernel", 128, 256), ("scale_kernel", 1, 256)] and got[10] == []
     assert got[11] == [("adamw_kernel", 64, 256)]
