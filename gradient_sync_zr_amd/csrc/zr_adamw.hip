@@ -28,18 +28,17 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamTable t5, AdamArgs 
     const int tiles = t5.tile0[t5.count];
     for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
         slot = multi_slot(t5, slot, t);
-        const int64_t begin = (int64_t)(t - t5.tile0[slot]) * kMultiTile, left = t5.n[slot] - begin;
-        const int c = threadIdx.x * 4;
-        const T* pg = (const T*)t5.p[0][slot] + begin;
-        float* pp = (float*)t5.p[1][slot] + begin;
-        float* pm = (float*)t5.p[2][slot] + begin;
-        float* pv = (float*)t5.p[3][slot] + begin;
-        uint16_t* ps = (uint16_t*)t5.p[4][slot] + begin;
+        float* const pp = (float*)t5.p[1][slot];
+        const int64_t begin = (int64_t)(t - t5.tile0[slot]) * kMultiTile - line_skew(pp, 4), n = t5.n[slot];
+        const T* const pg = (const T*)t5.p[0][slot];
+        float* const pm = (float*)t5.p[2][slot];
+        float* const pv = (float*)t5.p[3][slot];
+        uint16_t* const ps = (uint16_t*)t5.p[4][slot];
 #pragma unroll 2
         for (int k = 0; k < kMultiQuads; ++k) {
-            const int at = c + k * kThreads * 4;
-            const int l = left - at > 4 ? 4 : (int)(left - at);
-            if (l <= 0) break;
+            const int64_t at = begin + (threadIdx.x + k * kThreads) * 4;
+            if (at >= n) break;
+            const Span l = quad_span(at, n);
             float g[4], p[4], m[4], v[4];
             load_quad4<T, true>(pg + at, l, g);
             load_quad4<float, true>(pp + at, l, p);
@@ -75,7 +74,7 @@ hipError_t launch_adamw(const AdamW& f, hipStream_t stream) {
     a.inv2 = (float)(1.0 / (1.0 - __builtin_pow(f.beta2, (double)f.step)));
     a.eps = (float)f.eps;
     AdamTable m;
-    for (int next = multi_fill<kMultiTile>(&m, 0, f.n, lists, f.numels); m.count > 0; next = multi_fill<kMultiTile>(&m, next, f.n, lists, f.numels)) {
+    for (int next = multi_fill<kMultiTile, 1>(&m, 0, f.n, lists, f.numels); m.count > 0; next = multi_fill<kMultiTile, 1>(&m, next, f.n, lists, f.numels)) {
         const int grid = grid_for(m.tile0[m.count], kThreads);
         if (f.grad_dt == ZR_BF16)
             adamw_kernel<uint16_t><<<grid, kThreads, 0, stream>>>(m, a, f.shards != nullptr);

@@ -133,22 +133,21 @@ __global__ __launch_bounds__(kThreads) void scale_kernel(ScaleTable m, const flo
     const int tiles = m.tile0[m.count];
     for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
         slot = multi_slot(m, slot, t);
-        const int64_t begin = (int64_t)(t - m.tile0[slot]) * kMultiTile, left = m.n[slot] - begin;
-        const int c = threadIdx.x * 4;
-        const T* p = (const T*)m.p[0][slot] + begin + c;
-        U* q = (U*)m.p[1][slot] + begin + c;
+        const T* const p = (const T*)m.p[0][slot];
+        U* const q = (U*)m.p[1][slot];
+        const int64_t begin = (int64_t)(t - m.tile0[slot]) * kMultiTile - line_skew(q, sizeof(U)), n = m.n[slot];
         float f[kMultiQuads][4];
 #pragma unroll
         for (int k = 0; k < kMultiQuads; ++k) {
-            const int64_t l = left - c - k * kThreads * 4;
-            load_quad4<T, true>(p + k * kThreads * 4, l > 4 ? 4 : (int)l, f[k]);
+            const int64_t at = begin + (threadIdx.x + k * kThreads) * 4;
+            load_quad4<T, true>(p + at, quad_span(at, n), f[k]);
         }
 #pragma unroll
         for (int k = 0; k < kMultiQuads; ++k) {
-            const int64_t l = left - c - k * kThreads * 4;
+            const int64_t at = begin + (threadIdx.x + k * kThreads) * 4;
 #pragma unroll
             for (int e = 0; e < 4; ++e) f[k][e] *= k1;
-            store_quad4<U, true>(q + k * kThreads * 4, l > 4 ? 4 : (int)l, f[k]);
+            store_quad4<U, true>(q + at, quad_span(at, n), f[k]);
         }
     }
 }
@@ -164,7 +163,7 @@ hipError_t launch_grad_norm(const GradNorm& f, hipStream_t stream) {
     for (int i = 0; i < f.n; ++i) total += f.numels[i];
     const bool far = total * (f.dt == ZR_BF16 ? 2 : 4) > kCachedBytes;
     NormTable m;
-    int next = multi_fill<kNormTile>(&m, 0, f.n, lists, f.numels), parts = 0;
+    int next = multi_fill<kNormTile, -1>(&m, 0, f.n, lists, f.numels), parts = 0;
     if (next == f.n && m.tile0[m.count] <= 4 && total <= kNormOneElems) {
         if (f.dt == ZR_BF16)
             norm_one_kernel<uint16_t><<<1, 1024, 0, stream>>>(m, o);
@@ -186,7 +185,7 @@ hipError_t launch_grad_norm(const GradNorm& f, hipStream_t stream) {
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         parts += grid;
-        next = multi_fill<kNormTile>(&m, next, f.n, lists, f.numels);
+        next = multi_fill<kNormTile, -1>(&m, next, f.n, lists, f.numels);
     }
     norm_join_kernel<<<1, 1024, 0, stream>>>(part, parts, o);
     return hipGetLastError();
@@ -196,7 +195,9 @@ hipError_t launch_grad_scale(const GradScale& f, hipStream_t stream) {
     const bool in_place = !f.outs;
     const void* const* const lists[2] = {f.grads, in_place ? f.grads : (const void* const*)f.outs};
     ScaleTable m;
-    for (int next = multi_fill<kMultiTile>(&m, 0, f.n, lists, f.numels); m.count > 0; next = multi_fill<kMultiTile>(&m, next, f.n, lists, f.numels)) {
+    const int es = f.out_dt == ZR_BF16 ? 2 : 4;
+    for (int next = multi_fill<kMultiTile, 1>(&m, 0, f.n, lists, f.numels, es); m.count > 0;
+         next = multi_fill<kMultiTile, 1>(&m, next, f.n, lists, f.numels, es)) {
         const int grid = grid_for(m.tile0[m.count], kThreads);
         if (f.dt == ZR_BF16 && f.out_dt == ZR_BF16)
             scale_kernel<uint16_t, uint16_t><<<grid, kThreads, 0, stream>>>(m, f.coef, in_place);

@@ -321,7 +321,7 @@ ZR_KERNELS hipError_t launch_ckpt_wgrad(const Wgrad& w, hipStream_t stream);
 
 // Norm, scaling and AdamW over many tensors: a launch carries so many in its
 // arguments (4 KiB at most), and a longer list goes out as several.
-constexpr int kNormPer = 128, kScalePer = 128, kAdamPer = 64;
+constexpr int kNormPer = 192, kScalePer = 128, kAdamPer = 64;
 constexpr int kNormBlocks = 2048;  // partial sums of a launch at most
 constexpr int kNormTile = 8192;    // elements
 constexpr int kNormOneElems = 16384;  // in as many tiles as one block has groups of lanes: taken by it alone

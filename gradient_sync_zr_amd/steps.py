@@ -386,7 +386,7 @@ class ClipAdamW:
         g, p, m, v = self._tables
         zr_grad_norm(g, self.numels, self.norm, self.coef, max_norm=self.max_norm, scale=self.scale,
                      workspace=self._workspace, stream=stream)
-        self.steps += 1
-        zr_adamw(g, self.numels, p, m, v, self.steps, self.lr if lr is None else lr, beta1=self.beta1,
+        zr_adamw(g, self.numels, p, m, v, self.steps + 1, self.lr if lr is None else lr, beta1=self.beta1,
                  beta2=self.beta2, eps=self.eps, weight_decay=self.weight_decay, shards=self._shards,
                  coef=self.coef, stream=stream)
+        self.steps += 1

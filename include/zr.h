@@ -790,8 +790,8 @@ zr_status zr_ckpt_linear(const void* x, zr_dtype x_format, const void* w, zr_dty
  * Buffers that are written share no byte with any other of the call
  * (ZR_ERR_ALIAS); the same gradient may be listed twice where it is only read.
  * The calls enqueue kernels only, so they can be captured, and results do not
- * change from run to run (no atomics). One launch takes 128 tensors (AdamW: 64);
- * longer lists go out as several. */
+ * change from run to run (no atomics). One launch takes 128 tensors (the norm's 192,
+ * AdamW's 64); longer lists go out as several. */
 
 /* Bytes of workspace of zr_grad_norm; 0 for n <= 0. Host only. */
 size_t zr_grad_norm_workspace_bytes(int n);

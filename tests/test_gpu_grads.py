@@ -78,7 +78,7 @@ LISTS = [[1], [3], [0, 5, 0], [16384], [16385], [4096, 4096, 4096, 4096, 1], [40
 def test_norm_and_scaled(numels, dt):
     rng = np.random.default_rng(len(numels) + max(numels))
     z = zr()
-    for shift, scale, limit in ((0, 1.0, 1.0), (1, 1 / 3, 1e30), (3, 0.5, float("inf"))):
+    for shift, scale, limit in ((0, 1.0, 1.0), (1, 1 / 3, 1e30), (29, 0.5, float("inf"))):
         xs = make(rng, numels, dt)
         gs = [guarded(x, dt, shift * (k % 3)) for k, x in enumerate(xs)]
         got = run_norm([g.ptr() for g in gs], numels, dt, scale=scale, max_norm=limit)
@@ -91,7 +91,7 @@ def test_norm_and_scaled(numels, dt):
         k32 = np.float32(got[1])
         c = torch.full((1,), float(k32), device="cuda")
         for odt in ("bf16", "fp32"):
-            outs = [Guarded(n, td(odt), (k + shift) % 4) for k, n in enumerate(numels)]
+            outs = [Guarded(n, td(odt), (k * 5 + shift) % 67) for k, n in enumerate(numels)]
             z.zr_grad_scale([g.ptr() for g in gs], numels, c, [o.ptr() for o in outs],
                             dtype=z.ZR_BF16 if dt == "bf16" else z.ZR_FP32,
                             out_dtype=z.ZR_BF16 if odt == "bf16" else z.ZR_FP32)
@@ -176,9 +176,9 @@ def state(rng, numels, dt, shift):
     g = make(rng, numels, dt, 1e-3)
     p, m = make(rng, numels, "fp32", 0.02), make(rng, numels, "fp32", 1e-4)
     v = [x * x for x in make(rng, numels, "fp32", 1e-3)]
-    bufs = [[guarded(x, d, (shift * (j + k)) % 4) for k, x in enumerate(xs)]
+    bufs = [[guarded(x, d, shift * (j * 7 + k * 5) % 67) for k, x in enumerate(xs)]
             for j, (xs, d) in enumerate(((g, dt), (p, "fp32"), (m, "fp32"), (v, "fp32")))]
-    shards = [Guarded(n, td("bf16"), (shift * (k + 1)) % 4) for k, n in enumerate(numels)]
+    shards = [Guarded(n, td("bf16"), shift * (k * 3 + 1) % 67) for k, n in enumerate(numels)]
     return (g, p, m, v), bufs, shards
 
 

@@ -1,15 +1,10 @@
 """Refusals of the gradient norm, scaling and AdamW calls, without a GPU: every
 bad argument is reported before any HIP call (fake addresses, nothing launched)."""
 import ctypes
-import json
-import subprocess
-import sys
 
 import pytest
 
 import gradient_sync_zr_amd as zr
-from conftest import ROOT
-from launches import LOG, launches
 from test_abi_cpu import A, expect
 
 BF, FP = zr.ZR_BF16, zr.ZR_FP32
@@ -41,7 +36,7 @@ def test_norm_refusals():
     expect(zr.ZR_ERR_ALIGN, norm, ws=(C + 4, 1 << 20))
     need = zr.zr_grad_norm_workspace_bytes(3)
     assert need > 0 and zr.zr_grad_norm_workspace_bytes(0) == 0 and zr.zr_grad_norm_workspace_bytes(-3) == 0
-    assert zr.zr_grad_norm_workspace_bytes(129) == 2 * need
+    assert zr.zr_grad_norm_workspace_bytes(192) == need and zr.zr_grad_norm_workspace_bytes(193) == 2 * need
     expect(zr.ZR_ERR_WORKSPACE, norm, ws=None)
     expect(zr.ZR_ERR_WORKSPACE, norm, ws=(C, need - 1))
     expect(zr.ZR_ERR_ALIAS, norm, coef=B)
@@ -129,52 +124,3 @@ def test_tensors_are_checked():
         zr.zr_grad_norm(t, [5, 6, 8], B, workspace=(C, 1 << 20), stream=0)
     with pytest.raises(ValueError, match="dtype argument"):
         zr.zr_grad_norm(t, [5, 6, 7], B, workspace=(C, 1 << 20), dtype=BF, stream=0)
-
-
-def test_launches():
-    """One block up to 16384 elements in four tiles; a block per tile and a join beyond; a launch per 128 (64) tensors."""
-    launches([])  # builds the library that writes launches down
-    code = """
-import ctypes, json, sys
-sys.path.insert(0, sys.argv[1])
-log = ctypes.CDLL(sys.argv[2], mode=ctypes.RTLD_GLOBAL)
-log.ll_launch.restype = ctypes.c_char_p
-import gradient_sync_zr_amd as zr
-A = 1 << 46
-out = []
-for what, n, numel in json.loads(sys.argv[3]):
-    log.ll_clear()
-    t = [A + i * (1 << 35) for i in range(n)]
-    far = lambda k: [x + (k << 43) for x in t]
-    if what == "norm":
-        zr.zr_grad_norm(t, [numel] * n, 4096, 8192, workspace=(1 << 20, 1 << 30), dtype=1, stream=0)
-    elif what == "scale":
-        zr.zr_grad_scale(t, [numel] * n, 4096, dtype=1, stream=0)
-    else:
-        zr.zr_adamw(t, [numel] * n, far(1), far(2), far(3), 1, 1e-3, shards=far(4), coef=4096, dtype=1, stream=0)
-    got = []
-    for i in range(log.ll_count()):
-        d = (ctypes.c_uint32 * 6)()
-        got.append([log.ll_launch(i, d).decode(), d[0], d[3]])
-    out.append(got)
-print(json.dumps(out))
-"""
-    asked = [["norm", 0, 0], ["norm", 5, 0], ["norm", 1, 16384], ["norm", 4, 4000], ["norm", 5, 4000], ["norm", 1, 1 << 34],
-             ["norm", 129, 5000], ["scale", 1, 4097], ["scale", 128, 10], ["scale", 129, 10], ["scale", 3, 0],
-             ["adamw", 64, 4096], ["adamw", 130, 4097], ["adamw", 1, 1 << 34]]
-    r = subprocess.run([sys.executable, "-c", code, ROOT, LOG, json.dumps(asked)], capture_output=True, text=True, timeout=300)
-    assert r.returncode == 0, r.stderr[-2000:]
-    got = json.loads(r.stdout)
-    name = lambda s: next(k for k in ("norm_one", "norm_join", "norm_kernel", "scale_kernel", "adamw_kernel") if k in s)  # noqa: E731
-    got = [[(name(s), b, t) for s, b, t in g] for g in got]
-    one, join = ("norm_one", 1, 1024), ("norm_join", 1, 1024)
-    # (tiles of the norm have 8192 elements, of the others 4096)
-    assert got[:4] == [[one]] * 4
-    assert got[4] == [("norm_kernel", 5, 256), join]
-    assert got[5] == [("norm_kernel", 2048, 256), join]
-    assert got[6] == [("norm_kernel", 128, 256), ("norm_kernel", 1, 256), join]
-    assert got[7] == [("scale_kernel", 2, 256)] and got[8] == [("scale_kernel", 128, 256)]
-    assert got[9] == [("scale_kernel", 128, 256), ("scale_kernel", 1, 256)] and got[10] == []
-    assert got[11] == [("adamw_kernel", 64, 256)]
-    assert got[12] == [("adamw_kernel", 128, 256)] * 2 + [("adamw_kernel", 4, 256)]
-    assert len(got[13]) == 1 and all(b * t < 1 << 32 for g in got for _, b, t in g)
