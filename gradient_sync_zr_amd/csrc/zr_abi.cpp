@@ -1384,7 +1384,7 @@ zr_status zr_rmsnorm_bwd(const void* dy, zr_dtype dy_dt, int64_t ld_dy, const vo
         f.dy_dt = dy_dt; f.h_dt = h_dt; f.param_dt = param_dt; f.dx_dt = dx_dt; f.grad_dt = grad_dt;
         f.rows = rows; f.cols = cols; f.ld_dy = ld_dy; f.ld_h = ld_h; f.ld_dx = ld_dx;
         f.dx = dx; f.dweight = dweight;
-        f.accumulate = (flags & ZR_ACCUMULATE) != 0; f.add_dx = (flags & ZR_ADD_DX) != 0;
+        f.accumulate = (flags & ZR_ACCUMULATE) != 0; f.add_dx = dx && (flags & ZR_ADD_DX);
         f.workspace = workspace;
         return launched(launch_rmsnorm_bwd(f, (hipStream_t)stream), (hipStream_t)stream, "RMS norm backward launch");
     });

@@ -279,6 +279,8 @@ def test_backward_in_place_parts_and_no_rows():
         z.zr_rmsnorm_bwd(dy, h, rows, cols, rstd, w, dx=only)
         z.zr_rmsnorm_bwd(dy, h, rows, cols, rstd, w, dweight=onlyw, workspace=ws)
         assert torch.equal(only, dx) and torch.equal(onlyw, dw)
+        z.zr_rmsnorm_bwd(dy, h, rows, cols, rstd, w, dweight=onlyw, add_dx=True, workspace=ws)   # no dx to add to
+        assert torch.equal(onlyw, dw)
         a, b = dy.clone(), h.clone()
         z.zr_rmsnorm_bwd(a, h, rows, cols, rstd, w, dx=a, dweight=onlyw, workspace=ws)
         z.zr_rmsnorm_bwd(dy, b, rows, cols, rstd, w, dx=b, dweight=onlyw, workspace=ws)
