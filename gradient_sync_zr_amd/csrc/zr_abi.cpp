@@ -1261,7 +1261,7 @@ zr_status zr_layernorm_bwd(const void* dy, zr_dtype dy_dt, int64_t ld_dy, const 
         f.dy_dt = dy_dt; f.x_dt = x_dt; f.param_dt = param_dt; f.dx_dt = dx_dt; f.grad_dt = grad_dt;
         f.rows = rows; f.cols = cols; f.ld_dy = ld_dy; f.ld_x = ld_x; f.ld_dx = ld_dx;
         f.dx = dx; f.dweight = dweight; f.dbias = dbias;
-        f.accumulate = (flags & ZR_ACCUMULATE) != 0; f.add_dx = (flags & ZR_ADD_DX) != 0;
+        f.accumulate = (flags & ZR_ACCUMULATE) != 0; f.add_dx = dx && (flags & ZR_ADD_DX);
         f.workspace = workspace;
         return launched(launch_layernorm_bwd(f, (hipStream_t)stream), (hipStream_t)stream, "layer norm backward launch");
     });
