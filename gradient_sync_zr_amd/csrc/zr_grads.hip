@@ -6,6 +6,14 @@
 // its normal range (2^-298 to 2^256), so nothing overflows or vanishes whatever
 // the gradients' size. Blocks walk over tiles and leave one partial sum each; a
 // single block adds them in order, so the result does not change from run to run.
+//
+// The norm is one read: tiles of 8192 elements, whose loads are all in front, past
+// the caches where the tensors exceed them (2^30 bf16 elements 320 us for 396 with
+// 4096 and cached). 2^30 elements take 615 to 670 us of fp32 (6.4 to 7.0 TB/s) and
+// 320 of bf16 (6.7); 2^27 take 81 and 44. The fp64 arithmetic, 2 operations per
+// element, is hidden. Up to 16384 elements go through one block in one launch, where
+// two launches cost 3.6 us more. Scaling reads and writes once: 2^30 elements of fp32
+// in place 5.6 TB/s, to bf16 6.28.
 #include <hip/hip_runtime.h>
 
 #include "zr_ckpt.hpp"

