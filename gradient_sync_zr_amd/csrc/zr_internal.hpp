@@ -407,12 +407,13 @@ ZR_KERNELS hipError_t launch_linear(const Linear& f, hipStream_t stream);
 
 // How a product of packed matrices is cut: form 0 for few rows, tiles of 128 x 128
 // (1) or 256 x 256 (2), and the columns in `parts` of `share` turns of 512, joined
-// from the workspace. The fastest by a model fitted to a sweep of 11 shapes (70 to 8192
-// rows) in both forms and up to 22 parts; its choices took at most 18% longer than the
-// best measured, and 1% in the mean:
-//  - a tile takes kStart and, for every turn, between kTurn[0] (few blocks on the chip)
-//    and kTurn[1] us (all places taken: 512 of form 1, 256 of form 2);
-//  - joining costs 3 us and 0.25 us per MB of parts;
+// from the workspace. The fastest by a model fitted to sweeps of 20 shapes (70 to 16384
+// rows) in both forms and up to 22 parts; its choices took at most 13% longer than the
+// best measured (decoded; 10% else), and 1% in the mean:
+//  - a tile takes kStart, which has the results' writing in it, and kTurn for every turn,
+//    the first of each with few blocks on the chip, the second with all places taken
+//    (512 of form 1, 256 of form 2), in us;
+//  - joining costs 4 us and 0.4 us per MB of parts;
 //  - form 0 reads the tokens again for every 16 outputs: 4.5 us, and kFew for every turn
 //    of up to 16, 32 and 64 tokens (half of the first for a single one), more beyond
 //    4096 outputs, which are more blocks than the chip has places (33 to 64 tokens of
@@ -420,17 +421,18 @@ ZR_KERNELS hipError_t launch_linear(const Linear& f, hipStream_t stream);
 constexpr int kLinearGroup = 512;         // columns of a turn, of a load of exponents
 constexpr int64_t kLinearWide = 1 << 23;  // columns up to which a tile's rows lie within 32-bit offsets
 // What multiplies: scaled instructions with e4m3 on a side, or with e2m1 on both, or
-// bf16 instructions on decoded operands.
-enum LinearKind { kLinearScaled = 0, kLinearFour = 1, kLinearDecoded = 2 };
+// bf16 instructions on decoded operands (fp32 results, as of kLinearFourWide).
+enum LinearKind { kLinearScaled = 0, kLinearFour = 1, kLinearDecoded = 2, kLinearFourWide = 3 };
 struct LinearCut {
     int form, parts;
     int64_t turns, share;
 };
 inline LinearCut linear_cut(int64_t rows, int64_t out, int64_t in, LinearKind kind) {
-    static constexpr float kStart[2][3] = {{6.0f, 6.0f, 7.0f}, {10.0f, 10.0f, 14.0f}};
-    static constexpr float kTurn[2][3][2] = {{{3.4f, 6.3f}, {2.7f, 4.3f}, {7.1f, 13.0f}},
-                                             {{4.0f, 6.9f}, {2.2f, 4.2f}, {7.0f, 12.2f}}};
-    static constexpr float kFew[3][3] = {{0.5f, 0.9f, 1.45f}, {0.26f, 0.5f, 0.95f}, {0.75f, 1.2f, 2.1f}};
+    static constexpr float kStart[2][4][2] = {{{4.7f, 4.7f}, {5.4f, 5.4f}, {5.0f, 7.0f}, {6.0f, 6.0f}},
+                                              {{8.2f, 8.2f}, {8.7f, 8.7f}, {8.0f, 16.0f}, {8.0f, 16.0f}}};
+    static constexpr float kTurn[2][4][2] = {{{1.5f, 4.2f}, {0.7f, 2.4f}, {2.4f, 6.6f}, {0.7f, 2.8f}},
+                                             {{3.6f, 6.5f}, {1.9f, 4.0f}, {5.2f, 12.5f}, {1.7f, 4.2f}}};
+    static constexpr float kFew[4][3] = {{0.5f, 0.9f, 1.45f}, {0.26f, 0.5f, 0.95f}, {0.75f, 1.2f, 2.1f}, {0.26f, 0.5f, 0.95f}};
     const int64_t turns = (in + kLinearGroup - 1) / kLinearGroup;
     LinearCut best{0, 1, turns, turns};
     if (in > kLinearWide) return best;
@@ -440,14 +442,17 @@ inline LinearCut linear_cut(int64_t rows, int64_t out, int64_t in, LinearKind ki
     for (int f = 0; f < 2; ++f) {
         const int64_t edge = f ? 256 : 128, places = f ? 256 : 512;
         const int64_t tiles = ((rows + edge - 1) / edge) * ((out + edge - 1) / edge);
-        const float *t = kTurn[f][kind], start = kStart[f][kind];
+        const float *s = kStart[f][kind], *t = kTurn[f][kind];
         for (int64_t n = 1; n <= 32 && n <= turns; ++n) {
             const int64_t share = (turns + n - 1) / n;
             if (n > 1 && ((turns + share - 1) / share != n || tiles * n > 2 * places)) continue;
             const int64_t blocks = tiles * n, rounds = blocks / places, rest = blocks % places;
-            auto tile = [&](int64_t on) { return start + (float)share * (t[0] + (t[1] - t[0]) * (float)on / (float)places); };
+            auto tile = [&](int64_t on) {
+                const float full = (float)on / (float)places;
+                return s[0] + (s[1] - s[0]) * full + (float)share * (t[0] + (t[1] - t[0]) * full);
+            };
             float us = (float)rounds * tile(places) + (rest ? tile(rest) : 0.0f);
-            if (n > 1) us += 3.0f + 1e-6f * (float)n * (float)rows * (float)out;
+            if (n > 1) us += 4.0f + 1.6e-6f * (float)n * (float)rows * (float)out;
             if (us < least) {
                 best = LinearCut{f + 1, (int)n, turns, share};
                 least = us;
@@ -459,7 +464,7 @@ inline LinearCut linear_cut(int64_t rows, int64_t out, int64_t in, LinearKind ki
 // Floats of workspace that the cut needs, whatever the formats.
 inline int64_t linear_workspace(int64_t rows, int64_t out, int64_t in) {
     int64_t need = 0;
-    for (LinearKind k : {kLinearScaled, kLinearFour, kLinearDecoded}) {
+    for (LinearKind k : {kLinearScaled, kLinearFour, kLinearDecoded, kLinearFourWide}) {
         const LinearCut c = linear_cut(rows, out, in, k);
         const int64_t n = c.parts > 1 ? c.parts * rows * out : 0;
         need = n > need ? n : need;

@@ -188,8 +188,12 @@ __device__ __forceinline__ void wait_loads() {
 // the published one. A turn of the loop is the stages of 512 codes, whose exponents
 // are loaded at once, a turn ahead. Stages behind the last have exponents of 0, and
 // the loads ahead of the last are of it once more.
+//
+// (Two waves a SIMD are asked for so that the accumulators stay in VGPRs: with room for
+// more registers they were kept as AGPRs, and moved back and forth in every step. 2048^3
+// of e2m1 took 19.7 us for 11.3.)
 template <int FW, int FX, bool EXACT, int BO, int BT, int WO, int WT>
-__global__ __launch_bounds__((BO / WO) * (BT / WT) * 64) void linear_kernel(LinArgs a) {
+__global__ __launch_bounds__((BO / WO) * (BT / WT) * 64, 2) void linear_kernel(LinArgs a) {
     constexpr int T = (BO / WO) * (BT / WT) * 64;
     constexpr bool PAIR4 = FW == kE2m1 && FX == kE2m1;
     constexpr int BK = PAIR4 ? 128 : 64, STAGES = 4;
@@ -607,7 +611,8 @@ hipError_t run(LinArgs& a, const LinearCut& cut, hipStream_t stream) {
 
 hipError_t launch_linear(const Linear& f, hipStream_t stream) {
     const bool w4 = f.w_format == ZR_CKPT_E2M1, x4 = f.x_format == ZR_CKPT_E2M1;
-    const LinearKind kind = w4 && x4 ? kLinearFour : (f.z_dt == ZR_FP32 ? kLinearDecoded : kLinearScaled);
+    const LinearKind kind = w4 && x4 ? (f.z_dt == ZR_FP32 ? kLinearFourWide : kLinearFour)
+                                     : (f.z_dt == ZR_FP32 ? kLinearDecoded : kLinearScaled);
     const LinearCut cut = linear_cut(f.rows, f.out, f.in, kind);
     const int64_t pitch = ckpt_pitch(f.in);
     LinArgs a{};
@@ -620,7 +625,7 @@ hipError_t launch_linear(const Linear& f, hipStream_t stream) {
     a.rows = f.rows; a.out = f.out; a.ld_z = f.ld_z;
     a.bias_dt = f.bias_dt; a.z_dt = f.z_dt; a.accumulate = f.accumulate;
     a.turns = cut.turns; a.share = cut.share; a.parts = cut.parts;
-    if (kind == kLinearFour) return run<kE2m1, kE2m1, false>(a, cut, stream);
+    if (w4 && x4) return run<kE2m1, kE2m1, false>(a, cut, stream);
     if (kind == kLinearDecoded) {
         if (w4) return run<kE2m1, kE4m3, true>(a, cut, stream);
         return x4 ? run<kE4m3, kE2m1, true>(a, cut, stream) : run<kE4m3, kE4m3, true>(a, cut, stream);

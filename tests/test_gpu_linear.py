@@ -136,6 +136,32 @@ def test_large_tiles(xf, wf):
         assert torch.equal(acc, (want + b.double() + old.double()).to(td(zd)))
 
 
+@pytest.mark.parametrize("rows,inn,out,pairs,zds", [(32847, 600, 131, PAIRS, ("bf16", "fp32")),
+                                                    (8662, 13958, 130, PAIRS[:1], ("bf16",)), (2047, 2047, 2047, PAIRS, ("bf16", "fp32"))])
+def test_tall_and_square(rows, inn, out, pairs, zds):
+    """Tiles of 256 x 256 for every pair of formats and type of result, their columns in parts, and a chip full of 128 x
+    128; integers, so that every sum is exact."""
+    import torch
+    z = zr()
+    g = torch.Generator("cuda").manual_seed(rows)
+    x = torch.randint(-3, 4, (rows, inn), generator=g, device="cuda").bfloat16()
+    w = torch.randint(-2, 3, (out, inn), generator=g, device="cuda").bfloat16()
+    want = x.double() @ w.double().t().contiguous()
+    for xf, wf in pairs:
+        px, pw = (torch.empty(pk.nbytes(k, inn, FMT[f]), dtype=torch.uint8, device="cuda") for k, f in ((rows, xf), (out, wf)))
+        for v, k, b, f in ((x, rows, px, xf), (w, out, pw, wf)):
+            z.zr_ckpt_pack(v, k, inn, b, format=FMT[f])
+            back = torch.empty_like(v)
+            z.zr_ckpt_unpack(b, k, inn, back, format=FMT[f])
+            assert torch.equal(back, v)
+        for zd in zds:
+            print(xf, wf, zd, flush=True)
+            zt = torch.full((rows + 1, out), 9.0, dtype=td(zd), device="cuda")
+            z.zr_ckpt_linear(px, pw, rows, inn, out, zt[:rows], x_format=FMT[xf], w_format=FMT[wf],
+                             workspace=workspace(rows, inn, out))
+            assert torch.equal(zt[:rows], want.to(td(zd))) and bool((zt[rows:] == 9.0).all())
+
+
 @pytest.mark.parametrize("xf,wf", PAIRS)
 @pytest.mark.parametrize("rows,inn,out", [(3, 300, 40), (90, 5000, 70), (300, 96, 200)])
 def test_scales_of_every_size_and_blocks_that_are_not_finite(rows, inn, out, xf, wf):

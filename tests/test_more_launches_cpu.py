@@ -56,9 +56,13 @@ def test_forms_of_the_product():
     assert got[0] == [(few, 256, 512)] and got[1] == [(few, 49, 512)]
     assert got[2][0][0] == tiles
     assert got[3] == [(tiles, 64, 256)] and got[4] == [(tiles, 256, 512)]
-    assert got[5][0] == (tiles, 256, 256) and got[5][1][0] == join
+    assert got[5][0] == (tiles, 128, 256) and got[5][1][0] == join
     assert [k for k, _, _ in got[6]] == [tiles]
-    assert zr.zr_ckpt_linear_workspace_bytes(128, 4096, 4096) == 4 * 8 * 128 * 4096
+    assert zr.zr_ckpt_linear_workspace_bytes(128, 4096, 4096) == 4 * 4 * 128 * 4096
+    # 256 x 256 for a tall product in every kind (129 tiles), and in 7 parts
+    got = launches([lin(32847, 600, 131, E4, E4, BF), lin(32847, 600, 131, E2, E2, BF), lin(32847, 600, 131, E4, E4, FP),
+                    lin(32847, 600, 131, E2, E2, FP), lin(8662, 13958, 130)])
+    assert [g[0] for g in got] == [(tiles, 129, 512)] * 4 + [(tiles, 238, 512)] and got[4][1][0] == join
 
 
 def test_launches():
