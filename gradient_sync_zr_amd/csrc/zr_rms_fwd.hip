@@ -1,7 +1,7 @@
 // RMS norm, forward, with the residual's addition in front. Per row of n columns:
 //     h    = x + r, rounded to the residual stream's type (h = x without r)
 //     rstd = 1 / sqrt(sum h^2 / n + eps),  y = h * rstd * w
-// all in fp32, of h as its later readers have it. One pass over the row's
+// in fp32 (waves' sums joined in fp64), of h as its later readers have it. One pass over the row's
 // registers: blocks walk over the rows with the weight in registers and the next
 // row's loads in flight while a row is summed and written. Rows over 16384
 // columns are read twice (and h is then summed up twice).
@@ -26,6 +26,28 @@ struct RmsFwdArgs {
     int param_dt, h_dt, y_dt, e4m3;
     float eps;
 };
+
+// Sum over the TPR lanes of a row, those of its waves in fp64. With the formula's own
+// roundings behind it that makes rstd the same as that of sums in another order in
+// three rows of four or more (with a reciprocal square root in one of two), and its
+// last bit moves one value in 10^5 over the border between two in bf16. red: a float per
+// wave, free again once every wave has passed a later barrier.
+template <int TPR>
+__device__ __forceinline__ double row_sum64(float v, float* red) {
+    v = wave_sum<(TPR < 64 ? TPR : 64)>(v);
+    if constexpr (TPR <= 64) return v;
+    constexpr int W = TPR / 64;
+    const int wave = threadIdx.x / 64, first = wave / W * W;
+    if ((threadIdx.x & 63) == 0) red[wave] = v;
+    __syncthreads();
+    double s = 0.0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) s += (double)red[first + w];
+    return s;
+}
+__device__ __forceinline__ float rstd_of(double sum, double inv_n, float eps) {
+    return 1.0f / sqrtf((float)(sum * inv_n) + eps);
+}
 
 // A vector of bf16 or fp32 by a type known at run time, bf16 in the first half.
 __device__ __forceinline__ Raw8<kFp32> fetch_as(const char* row, int dt, int c, int n) {
@@ -88,10 +110,10 @@ template <int XD, int TPR, int NV>
 __global__ __launch_bounds__(norm_block(TPR)) void rms_fwd_kernel(RmsFwdArgs a) {
     constexpr int B = norm_block(TPR), G = B / TPR;
     static_assert(TPR <= 64 || G == 1, "barriers need one row per block");
-    __shared__ float red[2][B / 64][1];
+    __shared__ float red[2][B / 64];
     const int lane = threadIdx.x % TPR, group = row_group<TPR>();
     const int64_t pitch = ckpt_pitch(a.cols);
-    const float inv_n = 1.0f / (float)a.cols;
+    const double inv_n = 1.0 / (double)a.cols;
     float w[NV][8];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
@@ -115,7 +137,7 @@ __global__ __launch_bounds__(norm_block(TPR)) void rms_fwd_kernel(RmsFwdArgs a) 
     if (first < a.rows) fetch(first);
     for (int64_t row = first; row < a.rows; row += step) {
         float f[NV][8];
-        float s[1] = {0.0f};
+        float s = 0.0f;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int c = (v * TPR + lane) * 8, n = existing(a.cols, c);
@@ -124,14 +146,13 @@ __global__ __launch_bounds__(norm_block(TPR)) void rms_fwd_kernel(RmsFwdArgs a) 
             if (XD > kFp32 && n < 8) keep_first(f[v], n);
             if (a.res) add_residual(a, row, c, n, res[v], f[v]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s[0] = __builtin_fmaf(f[v][e], f[v][e], s[0]);
+            for (int e = 0; e < 8; ++e) s = __builtin_fmaf(f[v][e], f[v][e], s);
         }
         if (row + step < a.rows) fetch(row + step);
         // two sets of slots in turn: a set is written again only after the other
         // set's barrier, which every reader of the first has passed
-        row_sums<TPR>(s, red[parity]);
+        const float rstd = rstd_of(row_sum64<TPR>(s, red[parity]), inv_n, a.eps);
         parity ^= 1;
-        const float rstd = rsqrtf(s[0] * inv_n + a.eps);
         if (lane == 0 && a.rstd) a.rstd[row] = rstd;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
@@ -147,7 +168,7 @@ __global__ __launch_bounds__(norm_block(TPR)) void rms_fwd_kernel(RmsFwdArgs a) 
 // the residual's place: the second pass then reads h.
 template <int XD>
 __global__ __launch_bounds__(1024) void rms_fwd_wide_kernel(RmsFwdArgs a) {
-    __shared__ float red[2][16][1];
+    __shared__ float red[2][16];
     int parity = 0;
     const int64_t pitch = ckpt_pitch(a.cols);
     const int es = a.h_dt == kBf16 ? 2 : 4;
@@ -166,7 +187,7 @@ __global__ __launch_bounds__(1024) void rms_fwd_wide_kernel(RmsFwdArgs a) {
                 if (a.h_dt == kBf16) as_bf16(f);
             }
         };
-        float s[1] = {0.0f};
+        float s = 0.0f;
         for (int64_t c = threadIdx.x * 8; c < pitch; c += 8192) {
             const int n = existing(a.cols, c);
             float f[8];
@@ -176,11 +197,10 @@ __global__ __launch_bounds__(1024) void rms_fwd_wide_kernel(RmsFwdArgs a) {
             float t = 0.0f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) t = __builtin_fmaf(f[e], f[e], t);
-            s[0] += t;
+            s += t;
         }
-        row_sums<1024>(s, red[parity]);
+        const float rstd = rstd_of(row_sum64<1024>(s, red[parity]), 1.0 / (double)a.cols, a.eps);
         parity ^= 1;
-        const float rstd = rsqrtf(s[0] / (float)a.cols + a.eps);
         if (threadIdx.x == 0 && a.rstd) a.rstd[row] = rstd;
         for (int64_t c = threadIdx.x * 8; c < pitch; c += 8192) {
             const int n = existing(a.cols, c);
