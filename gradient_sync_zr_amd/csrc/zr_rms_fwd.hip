@@ -6,7 +6,7 @@
 // row's loads in flight while a row is summed and written. Rows over 16384
 // columns are read twice (and h is then summed up twice).
 //
-// Memory bounds it: 16384x4096 bf16 with residual, h and y takes 91 us (5.9 TB/s).
+// Memory bounds it: 16384x4096 bf16 with residual, h and y takes 91 to 92 us (5.9 TB/s).
 // With y packed (8192x4096 from fp32 x, h written) 47 us. A row is summed once by
 // its wave or block, so the shuffles and the one barrier of a row are what the next
 // row's loads cover.
