@@ -136,6 +136,15 @@ def test_large_tiles(xf, wf):
         assert torch.equal(acc, (want + b.double() + old.double()).to(td(zd)))
 
 
+@pytest.mark.parametrize("xf,wf", PAIRS)
+def test_rows_of_exponents_off_16_bytes(xf, wf):
+    """Rows of 20, 36, 68 and 100 exponents: their loads start at every multiple of 4 bytes."""
+    for rows, inn, out in ((300, 640, 200), (129, 1152, 257), (70, 2176, 100), (513, 3200, 130)):
+        for zd in ("bf16", "fp32"):
+            print(rows, inn, out, zd, flush=True)
+            check(rows, inn, out, xf, wf, zd, np.random.default_rng(inn))
+
+
 @pytest.mark.parametrize("rows,inn,out,pairs,zds", [(32847, 600, 131, PAIRS, ("bf16", "fp32")),
                                                     (8662, 13958, 130, PAIRS[:1], ("bf16",)), (2047, 2047, 2047, PAIRS, ("bf16", "fp32"))])
 def test_tall_and_square(rows, inn, out, pairs, zds):
