@@ -221,9 +221,10 @@ def lib() -> ctypes.CDLL:
         for f in RMS_EXPORTS[4:]:
             getattr(L, f).restype = _sz
         _I64s = ctypes.POINTER(_i64)
-        L.zr_grad_norm.argtypes = [_i32, _PP, _I64s, _i32, _d, _d, _vp, _vp, _vp, _sz, _vp]
-        L.zr_grad_scale.argtypes = [_i32, _PP, _I64s, _i32, _PP, _i32, _vp, _vp]
-        L.zr_adamw.argtypes = [_i32, _PP, _i32, _I64s, _PP, _PP, _PP, _PP] + [_d] * 5 + [_i64, _vp, _vp]
+        # tables and sizes as addresses: a ctypes array costs a small call a microsecond
+        L.zr_grad_norm.argtypes = [_i32, _vp, _vp, _i32, _d, _d, _vp, _vp, _vp, _sz, _vp]
+        L.zr_grad_scale.argtypes = [_i32, _vp, _vp, _i32, _vp, _i32, _vp, _vp]
+        L.zr_adamw.argtypes = [_i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp] + [_d] * 5 + [_i64, _vp, _vp]
         L.zr_grad_norm_workspace_bytes.argtypes = [_i32]
         L.zr_grad_norm_workspace_bytes.restype = _sz
         for f in ("zr_cost_ring_allreduce", "zr_cost_ring_reduce_scatter",
@@ -1058,8 +1059,8 @@ class TensorTable:
 
     def __init__(self, xs: Sequence, numels, dtype=None, name: str = "tensors"):
         at, code, device = _list(xs, numels, dtype, name)
-        self.table, self.dtype, self.device = _table(at), code, device
-        self._bytes, self._keep = bytes(_sizes(numels)), list(xs)
+        self.table, self.dtype, self.device = array.array("Q", at or [0]), code, device
+        self._sizes, self._keep = _sizes(numels), list(xs)
         self._n = len(at)
 
     def __len__(self):
@@ -1072,7 +1073,12 @@ def tensor_table(xs: Sequence, numels: Sequence[int], dtype=None) -> TensorTable
 
 
 def _sizes(numels):
-    return numels if isinstance(numels, ctypes.Array) else _int64s(numels)
+    return array.array("q", numels if len(numels) else [0])
+
+
+def _at(a) -> int:
+    """Address of an array's items, for as long as it is kept."""
+    return a.buffer_info()[0]
 
 
 def _list(xs, numels, dtype, name):
@@ -1106,10 +1112,10 @@ def _list(xs, numels, dtype, name):
 
 
 def _many(xs, numels, sizes, dtype, name, gpus):
-    """(C table, dtype) of one list of a call; its GPU joins `gpus`. sizes: the C
-    array of numels."""
+    """(array of addresses, dtype) of one list of a call; its GPU joins `gpus`.
+    sizes: the array of numels."""
     if xs.__class__ is TensorTable:
-        if xs._n != len(numels) or xs._bytes != bytes(sizes):
+        if xs._n != len(numels) or xs._sizes != sizes:
             raise ValueError(f"{name} is a table of other sizes")
         if dtype is not None and _dtype(dtype) != xs.dtype:
             raise ValueError(f"{name} is not what its dtype argument says")
@@ -1117,7 +1123,7 @@ def _many(xs, numels, sizes, dtype, name, gpus):
         return xs.table, xs.dtype
     at, code, device = _list(xs, numels, dtype, name)
     gpus.append(device)
-    return _table(at), code
+    return array.array("Q", at or [0]), code
 
 
 def _run_on_gpus(stream, gpus, *xs) -> int:
@@ -1135,6 +1141,10 @@ def _run_on_gpus(stream, gpus, *xs) -> int:
 
 def _scalar(x, name):
     """Address of one fp32 on the device: a tensor of one element, an address, or None."""
+    if x is None or x.__class__ is int:
+        return x or 0
+    if x.numel() == 1 and _dtypes.get(x.dtype) == ZR_FP32:
+        return x.data_ptr()
     return _vector(x, 1, ZR_FP32, name)[0]
 
 
@@ -1151,8 +1161,10 @@ def zr_grad_norm(grads, numels: Sequence[int], norm=None, coef=None, max_norm: f
     gpus, sizes = [], _sizes(numels)
     t, dt = _many(grads, numels, sizes, dtype, "grads", gpus)
     ws, wsb = _workspace(workspace)
-    _check(lib().zr_grad_norm(len(numels), t, sizes, dt, scale, max_norm, _scalar(norm, "norm"),
-                              _scalar(coef, "coef"), ws, wsb, _run_on_gpus(stream, gpus, norm, coef, workspace)))
+    st = lib().zr_grad_norm(len(numels), _at(t), _at(sizes), dt, scale, max_norm, _scalar(norm, "norm"),
+                            _scalar(coef, "coef"), ws, wsb, _run_on_gpus(stream, gpus, norm, coef, workspace))
+    if st:
+        _check(st)
 
 
 def zr_grad_scale(grads, numels: Sequence[int], coef, outs=None, dtype=None, out_dtype=None, stream=None) -> None:
@@ -1161,8 +1173,10 @@ def zr_grad_scale(grads, numels: Sequence[int], coef, outs=None, dtype=None, out
     gpus, sizes = [], _sizes(numels)
     t, dt = _many(grads, numels, sizes, dtype, "grads", gpus)
     o, odt = (None, dt) if outs is None else _many(outs, numels, sizes, out_dtype, "outs", gpus)
-    _check(lib().zr_grad_scale(len(numels), t, sizes, dt, o, odt, _scalar(coef, "coef"),
-                               _run_on_gpus(stream, gpus, coef)))
+    st = lib().zr_grad_scale(len(numels), _at(t), _at(sizes), dt, None if o is None else _at(o), odt,
+                             _scalar(coef, "coef"), _run_on_gpus(stream, gpus, coef))
+    if st:
+        _check(st)
 
 
 def zr_adamw(grads, numels: Sequence[int], params, exp_avg, exp_avg_sq, step: int, lr: float, beta1: float = 0.9,
@@ -1177,5 +1191,7 @@ def zr_adamw(grads, numels: Sequence[int], params, exp_avg, exp_avg_sq, step: in
     p, m, v = (_many(xs, numels, sizes, ZR_FP32, name, gpus)[0]
                for xs, name in ((params, "params"), (exp_avg, "exp_avg"), (exp_avg_sq, "exp_avg_sq")))
     s = None if shards is None else _many(shards, numels, sizes, ZR_BF16, "shards", gpus)[0]
-    _check(lib().zr_adamw(len(numels), t, dt, sizes, p, m, v, s, lr, beta1, beta2, eps, weight_decay, step,
-                          _scalar(coef, "coef"), _run_on_gpus(stream, gpus, coef)))
+    st = lib().zr_adamw(len(numels), _at(t), dt, _at(sizes), _at(p), _at(m), _at(v), None if s is None else _at(s), lr,
+                        beta1, beta2, eps, weight_decay, step, _scalar(coef, "coef"), _run_on_gpus(stream, gpus, coef))
+    if st:
+        _check(st)
