@@ -8,10 +8,13 @@
 // coefficient that is not finite leaves everything as it was.
 //
 // A stream of 30 bytes per element (fp32 gradients, shards written), read and
-// written past the caches: 2^26 elements take 363 to 367 us (5.5 TB/s), 328 to 331
-// (5.3) from bf16 gradients; with cached accesses 389. The seven streams bound it, not
-// a lane's loads: one, two or four vectors a lane take the same time.
+// written past the caches: 2^26 elements take 359 us (5.6 TB/s), 335 (5.6) from bf16
+// gradients, which is what the card moves with as much written as read (a scaling from
+// fp32 to fp32: 5.6); with cached accesses 389. Tiles inside a tensor have a path
+// without the quads' borders, whose branches held the loads apart (bf16 365 without it).
 #include <hip/hip_runtime.h>
+
+#include <type_traits>
 
 #include "zr_multi.hpp"
 
@@ -39,29 +42,36 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamTable t5, AdamArgs 
         float* const pm = (float*)t5.p[2][slot];
         float* const pv = (float*)t5.p[3][slot];
         uint16_t* const ps = (uint16_t*)t5.p[4][slot];
-#pragma unroll 2
-        for (int k = 0; k < kMultiQuads; ++k) {
-            const int64_t at = begin + (threadIdx.x + k * kThreads) * 4;
-            if (at >= n) break;
-            const Span l = quad_span(at, n);
-            float g[4], p[4], m[4], v[4];
-            load_quad4<T, true>(pg + at, l, g);
-            load_quad4<float, true>(pp + at, l, p);
-            load_quad4<float, true>(pm + at, l, m);
-            load_quad4<float, true>(pv + at, l, v);
+        auto quads = [&](auto whole) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float x = g[e] * coef;
-                m[e] = __builtin_fmaf(a.beta1, m[e], a.rest1 * x);
-                v[e] = __builtin_fmaf(a.beta2, v[e], a.rest2 * x * x);
-                const float root = __fsqrt_rn(v[e] * a.inv2) + a.eps;
-                p[e] = __builtin_fmaf(a.keep, p[e], -a.rate * __fdiv_rn(m[e], root));
+            for (int k = 0; k < kMultiQuads; ++k) {
+                const int64_t at = begin + (threadIdx.x + k * kThreads) * 4;
+                if (!whole && at >= n) break;
+                const Span l = whole ? Span{0, 4} : quad_span(at, n);
+                float g[4], p[4], m[4], v[4];
+                load_quad4<float, true>(pp + at, l, p);
+                load_quad4<float, true>(pm + at, l, m);
+                load_quad4<float, true>(pv + at, l, v);
+                load_quad4<T, true>(pg + at, l, g);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float x = g[e] * coef;
+                    m[e] = __builtin_fmaf(a.beta1, m[e], a.rest1 * x);
+                    v[e] = __builtin_fmaf(a.beta2, v[e], a.rest2 * x * x);
+                    const float root = __fsqrt_rn(v[e] * a.inv2) + a.eps;
+                    p[e] = __builtin_fmaf(a.keep, p[e], -a.rate * __fdiv_rn(m[e], root));
+                }
+                store_quad4<float, true>(pp + at, l, p);
+                store_quad4<float, true>(pm + at, l, m);
+                store_quad4<float, true>(pv + at, l, v);
+                if (shards) store_quad4<uint16_t, true>(ps + at, l, p);
             }
-            store_quad4<float, true>(pp + at, l, p);
-            store_quad4<float, true>(pm + at, l, m);
-            store_quad4<float, true>(pv + at, l, v);
-            if (shards) store_quad4<uint16_t, true>(ps + at, l, p);
-        }
+        };
+        // the same for the block; without the quads' borders all loads go out in front
+        if (begin >= 0 && n - begin >= kMultiTile)
+            quads(std::true_type{});
+        else
+            quads(std::false_type{});
     }
 }
 
