@@ -43,6 +43,25 @@ __device__ __forceinline__ uint32_t e2m1_encode8(const float f[8], uint32_t s) {
     return s == kCkptNan ? 0u : q;
 }
 
+// The same of 8 bf16 values as they lie in memory: the conversion divides by the scale,
+// and nothing is widened.
+__device__ __forceinline__ uint32_t e2m1_encode8(const u32x4& w, uint32_t s) {
+    if (s == 253u) {
+        float f[8];
+        widen8(Raw8<kBf16>{w}, f);
+        return e2m1_encode8(f, s);
+    }
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    auto pair = [](uint32_t a) { return __builtin_bit_cast(bf16x2, a); };
+    const float scale = __uint_as_float(s << 23);
+    uint32_t q = 0;
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, pair(w.x), scale, 0);
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, pair(w.y), scale, 1);
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, pair(w.z), scale, 2);
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, pair(w.w), scale, 3);
+    return s == kCkptNan ? 0u : q;
+}
+
 // Values of 8 codes of a block with scale 2^e.
 __device__ __forceinline__ void e2m1_decode8(uint32_t q, float scale, float f[8]) {
     const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.0f, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.0f, 1);

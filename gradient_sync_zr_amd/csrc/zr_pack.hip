@@ -2,9 +2,11 @@
 // transpose in every format (the backward pass multiplies by a weight's transpose,
 // whose blocks run along the other axis).
 //
-// Streams: 65536x4096 of bf16 to e2m1 takes 131 to 136 us (5.0 to 5.2 TB/s), back
-// 112 to 118; 16384x4096 35.
+// Streams: 65536x4096 of bf16 to e2m1 takes 106 us (6.4 TB/s), back 116 (5.9);
+// 16384x4096 28 and 32.
 #include <hip/hip_runtime.h>
+
+#include <type_traits>
 
 #include "zr_e2m1.hpp"
 #include "zr_internal.hpp"
@@ -22,6 +24,81 @@ __device__ __forceinline__ void place(uint32_t rem, uint32_t i, uint32_t V, uint
     const uint32_t r = at / V;
     *drow = r;
     *c = (int)(at - r * V) * 8;
+}
+
+// Codes and exponent of vector i of the rows laid end to end.
+__device__ __forceinline__ void put_small(uint32_t* codes, uint8_t* scales, int64_t i, uint32_t q, uint32_t s) {
+    st<true>(codes + i, q);
+    if ((i & 3) == 0) scales[i / 4] = (uint8_t)s;
+}
+
+// Rows of whole blocks without gaps are one row, and a vector's place is its number.
+// (With rows, columns and their division the instructions take longer than memory:
+// 65536x4096 of bf16 136 us.)
+template <int DT>
+__global__ __launch_bounds__(kThreads) void pack_flat_kernel(const void* x, int64_t vectors, char* ckpt) {
+    uint8_t* const scales = (uint8_t*)ckpt + vectors * 4;
+    const int64_t tiles = (vectors + kTile - 1) / kTile;
+    for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+        const int64_t first = t * kTile;
+        auto tile = [&](auto whole) {
+            Raw8<DT> raw[kVecs];
+#pragma unroll
+            for (int k = 0; k < kVecs; ++k) {
+                const int64_t i = first + threadIdx.x + k * kThreads;
+                if (whole || i < vectors) raw[k] = fetch8<DT, true>({(const char*)x + i * (DT == kBf16 ? 16 : 32), nullptr}, 0, 8);
+            }
+#pragma unroll
+            for (int k = 0; k < kVecs; ++k) {
+                const int64_t i = first + threadIdx.x + k * kThreads;
+                if (!whole && i >= vectors) continue;  // a block's lanes leave together
+                settle8(raw[k], 0, 8);
+                if constexpr (DT == kBf16) {
+                    const uint32_t s = e2m1_byte(block_amax(raw[k].v));
+                    put_small((uint32_t*)ckpt, scales, i, e2m1_encode8(raw[k].v, s), s);
+                } else {
+                    float f[8];
+                    widen8(raw[k], f);
+                    const uint32_t s = e2m1_byte(block_amax(f));
+                    put_small((uint32_t*)ckpt, scales, i, e2m1_encode8(f, s), s);
+                }
+            }
+        };
+        if (vectors - first >= kTile)  // the same for the block
+            tile(std::true_type{});
+        else
+            tile(std::false_type{});
+    }
+}
+
+__global__ __launch_bounds__(kThreads) void unpack_flat_kernel(const char* ckpt, int64_t vectors, char* x, int dt) {
+    const uint8_t* const scales = (const uint8_t*)ckpt + vectors * 4;
+    const int64_t tiles = (vectors + kTile - 1) / kTile, es = dt == kBf16 ? 16 : 32;
+    for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+        const int64_t first = t * kTile;
+        auto tile = [&](auto whole) {
+            uint32_t q[kVecs], s[kVecs];
+#pragma unroll
+            for (int k = 0; k < kVecs; ++k) {
+                const int64_t i = first + threadIdx.x + k * kThreads;
+                if (!whole && i >= vectors) continue;
+                q[k] = __builtin_nontemporal_load((const uint32_t*)ckpt + i);
+                s[k] = scales[i / 4];
+            }
+#pragma unroll
+            for (int k = 0; k < kVecs; ++k) {
+                const int64_t i = first + threadIdx.x + k * kThreads;
+                if (!whole && i >= vectors) continue;
+                float f[8];
+                e2m1_decode8(q[k], ckpt_scale(s[k]), f);
+                store8<true>(x + i * es, dt, 0, 8, f);
+            }
+        };
+        if (vectors - first >= kTile)
+            tile(std::true_type{});
+        else
+            tile(std::false_type{});
+    }
 }
 
 // As the 8-bit pack: lanes take vectors of 8 columns over the rows laid end to
@@ -58,9 +135,8 @@ __global__ __launch_bounds__(kThreads) void pack_small_kernel(const void* x, int
             else
                 amax = block_amax(f);
             const uint32_t s = e2m1_byte(amax);
-            st<true>((uint32_t*)(ckpt + row[k] * (pitch / 2) + c[k] / 2), e2m1_encode8(f, s));
-            if ((c[k] & (kCkptBlock - 1)) == 0)
-                ((uint8_t*)ckpt)[rows * (pitch / 2) + row[k] * (pitch / kCkptBlock) + c[k] / kCkptBlock] = (uint8_t)s;
+            put_small((uint32_t*)ckpt, (uint8_t*)ckpt + rows * (pitch / 2), first + threadIdx.x + k * kThreads,
+                      e2m1_encode8(f, s), s);
         }
     }
 }
@@ -172,12 +248,21 @@ void pack_t_run(const void* x, int64_t ld, int64_t rows, int64_t cols, char* ckp
 
 int64_t tiles_of(int64_t rows, int64_t cols) { return (rows * (ckpt_pitch(cols) / 8) + kTile - 1) / kTile; }
 
+bool flat(int64_t rows, int64_t cols, int64_t ld) { return cols % kCkptBlock == 0 && (ld == cols || rows == 1); }
+
 }  // namespace
 
 hipError_t launch_pack_small(const void* x, zr_dtype dt, int64_t rows, int64_t cols, int64_t ld, void* ckpt,
                              hipStream_t stream) {
     const int64_t tiles = tiles_of(rows, cols);
     const dim3 grid(grid_for(tiles, kThreads)), block(kThreads);
+    if (flat(rows, cols, ld)) {
+        if (dt == ZR_BF16)
+            pack_flat_kernel<kBf16><<<grid, block, 0, stream>>>(x, rows * (cols / 8), (char*)ckpt);
+        else
+            pack_flat_kernel<kFp32><<<grid, block, 0, stream>>>(x, rows * (cols / 8), (char*)ckpt);
+        return hipGetLastError();
+    }
     if (dt == ZR_BF16)
         pack_small_kernel<kBf16><<<grid, block, 0, stream>>>(x, ld, rows, cols, (char*)ckpt, tiles);
     else
@@ -188,6 +273,10 @@ hipError_t launch_pack_small(const void* x, zr_dtype dt, int64_t rows, int64_t c
 hipError_t launch_unpack_small(const void* ckpt, int64_t rows, int64_t cols, void* x, zr_dtype dt, int64_t ld,
                                hipStream_t stream) {
     const int64_t tiles = tiles_of(rows, cols);
+    if (flat(rows, cols, ld)) {
+        unpack_flat_kernel<<<grid_for(tiles, kThreads), kThreads, 0, stream>>>((const char*)ckpt, rows * (cols / 8), (char*)x, dt);
+        return hipGetLastError();
+    }
     unpack_small_kernel<<<grid_for(tiles, kThreads), kThreads, 0, stream>>>((const char*)ckpt, rows, cols, (char*)x, ld, dt,
                                                                             tiles);
     return hipGetLastError();

@@ -63,6 +63,33 @@ def test_pack_and_unpack(rows, cols):
             assert (v[:, cols:] == 7.0).all() and y.guards_intact()
 
 
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_every_bf16_value(dt):
+    """Each of the 2^16 patterns beside a larger one by 2^0 to 2^9 and a half more, in rows without gaps and with."""
+    import torch
+    z = zr()
+    v = (np.arange(1 << 16, dtype=np.uint32) << 16).view(np.float32)
+    with np.errstate(all="ignore"):
+        most = (np.abs(v)[:, None] * 2.0 ** np.arange(10, dtype=np.float32) * np.float32(1.5)).astype(np.float32)
+    most[most > 3.0e38] = 3.0e38
+    x = np.zeros((1 << 16, 10, 32), np.float32)
+    x[:, :, 7], x[:, :, 30] = v[:, None], bf16(most)
+    x = x.reshape(1 << 15, 640)
+    code = z.ZR_BF16 if dt == "bf16" else z.ZR_FP32
+    want = pk.pack(x.astype(np.float64), pk.E2M1)
+    for gap, shift in ((0, 0), (0, 3), (5, 0)):
+        g = upload(x, dt, 640 + gap, shift)
+        out = buffer(1 << 15, 640, pk.E2M1)
+        z.zr_ckpt_pack(g.ptr(), 1 << 15, 640, out, format=pk.E2M1, dtype=code, ld=640 + gap)
+        got = out.cpu().numpy()
+        assert np.array_equal(got[:want.size], want) and (got[want.size:] == 0x55).all()
+    y = torch.empty(1 << 15, 640, dtype=torch.bfloat16 if dt == "bf16" else torch.float32, device="cuda")
+    z.zr_ckpt_unpack(out, 1 << 15, 640, y, format=pk.E2M1)
+    held = pk.unpack(want, 1 << 15, 640, pk.E2M1).astype(np.float32)
+    got, nan = y.float().cpu().numpy(), np.isnan(held)
+    assert np.array_equal(np.isnan(got), nan) and np.array_equal(bits(got)[~nan], bits(held)[~nan])
+
+
 @pytest.mark.parametrize("rows,cols", SIZES + [(4096, 70), (300, 1100)])
 def test_transposed(rows, cols):
     z = zr()
