@@ -175,25 +175,28 @@ __global__ __launch_bounds__(kThreads) void unpack_small_kernel(const char* ckpt
     }
 }
 
-// The transpose: a wave takes 64 columns of x and, in turn, `turns` blocks of 32
-// rows, a column to a lane. A lane holds a whole block, so its largest magnitude
-// needs no other lane; loads are 64 neighbouring elements of a row, and a lane
-// writes its blocks side by side. 11008x4096 of bf16 takes 44 us to e4m3 and 36.5 to
-// e2m1, 4096x4096 16 and 13: the codes of 64 rows of the result leave in pieces of
-// 32 bytes (16 of e2m1) a block, which caches collect.
-template <int DT, int FMT>
+// The transpose: a block takes 256 columns of x and TURNS blocks of 32 rows, a column
+// to a lane. A lane holds a whole block, so its largest magnitude needs no other lane;
+// loads are 64 neighbouring elements of a row, and a lane writes its blocks' codes at
+// once, 64 bytes of a row of the result. (A block at a time the pieces met in the caches
+// only while they held all rows' lines: 16384x16384 of bf16 378 us to e4m3, 224 so; with
+// 128 bytes the registers leave two waves a SIMD, 249.) 11008x4096 of bf16
+// takes 37 us to e4m3 and 34 to e2m1, 4096x4096 15 and 12.
+template <int DT, int FMT, int TURNS>
 __global__ __launch_bounds__(kThreads) void pack_t_kernel(const void* x, int64_t ld, int64_t rows, int64_t cols, char* ckpt,
-                                                          int turns, int64_t tiles_c, int64_t tiles) {
+                                                          int64_t tiles_c, int64_t tiles) {
+    constexpr int WORDS = FMT == kE2m1 ? 1 : 2;           // of 16 bytes, of a block's codes
     const int64_t blocks = ckpt_pitch(rows) / kCkptBlock;  // of an output row
     const int64_t codes = code_bytes<FMT>(rows);
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-        const int64_t tr = t / tiles_c, c = ((t - tr * tiles_c) * (kThreads / 64) + wave) * 64 + lane;
+        const int64_t tr = t / tiles_c, c = (t - tr * tiles_c) * kThreads + threadIdx.x, first = tr * TURNS;
         if (c >= cols) continue;
-#pragma unroll 1
-        for (int b = 0; b < turns; ++b) {
-            const int64_t block = tr * turns + b, row = block * kCkptBlock;
-            if (block >= blocks) break;
+        u32x4 q[TURNS][WORDS];
+        uint32_t s[TURNS];
+#pragma unroll
+        for (int b = 0; b < TURNS; ++b) {
+            const int64_t row = (first + b) * kCkptBlock;
+            if (first + b >= blocks) break;
             // rows behind the last are read from it, and are zeros
             float f[kCkptBlock];
             const int have = rows - row < kCkptBlock ? (int)(rows - row) : kCkptBlock;
@@ -215,35 +218,52 @@ __global__ __launch_bounds__(kThreads) void pack_t_kernel(const void* x, int64_t
                 const uint32_t m = __float_as_uint(f[k]) & 0x7FFFFFFFu;
                 amax = m > amax ? m : amax;
             }
-            const uint32_t s = format_byte<FMT>(amax);
-            u32x4* out = (u32x4*)(ckpt + c * codes + block * (FMT == kE2m1 ? 16 : 32));
+            s[b] = format_byte<FMT>(amax);
             if constexpr (FMT == kE2m1) {
-                *out = u32x4{e2m1_encode8(f, s), e2m1_encode8(f + 8, s), e2m1_encode8(f + 16, s), e2m1_encode8(f + 24, s)};
+                q[b][0] = u32x4{e2m1_encode8(f, s[b]), e2m1_encode8(f + 8, s[b]), e2m1_encode8(f + 16, s[b]),
+                                e2m1_encode8(f + 24, s[b])};
             } else {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const u32x2 lo = ckpt_encode8(f + 16 * h, s, FMT == kE4m3), hi = ckpt_encode8(f + 16 * h + 8, s, FMT == kE4m3);
-                    out[h] = u32x4{lo.x, lo.y, hi.x, hi.y};
+                    const u32x2 lo = ckpt_encode8(f + 16 * h, s[b], FMT == kE4m3), hi = ckpt_encode8(f + 16 * h + 8, s[b], FMT == kE4m3);
+                    q[b][h] = u32x4{lo.x, lo.y, hi.x, hi.y};
                 }
             }
-            ((uint8_t*)ckpt)[cols * codes + c * blocks + block] = (uint8_t)s;
+        }
+        u32x4* const out = (u32x4*)(ckpt + c * codes) + first * WORDS;
+        uint8_t* const scales = (uint8_t*)ckpt + cols * codes + c * blocks + first;
+#pragma unroll
+        for (int b = 0; b < TURNS; ++b) {
+            if (first + b >= blocks) break;
+#pragma unroll
+            for (int h = 0; h < WORDS; ++h) out[b * WORDS + h] = q[b][h];
+            scales[b] = (uint8_t)s[b];
         }
     }
 }
 
-template <int DT>
-void pack_t_run(const void* x, int64_t ld, int64_t rows, int64_t cols, char* ckpt, zr_dtype fmt, hipStream_t stream) {
+template <int DT, int FMT>
+void pack_t_run(const void* x, int64_t ld, int64_t rows, int64_t cols, char* ckpt, hipStream_t stream) {
     const int64_t tiles_c = (cols + kThreads - 1) / kThreads, blocks = (rows + kCkptBlock - 1) / kCkptBlock;
-    // four blocks to a lane (a line of codes) where that leaves enough for the chip
-    const int turns = tiles_c * blocks >= 4096 ? 4 : 1;
-    const int64_t tiles = tiles_c * ((blocks + turns - 1) / turns);
+    // 64 bytes of codes to a lane where that leaves enough for the chip
+    constexpr int TURNS = FMT == kE2m1 ? 4 : 2;
+    const bool many = tiles_c * blocks >= 4096;
+    const int64_t tiles = tiles_c * (many ? (blocks + TURNS - 1) / TURNS : blocks);
     const dim3 grid(grid_for(tiles, kThreads)), block(kThreads);
-    if (fmt == ZR_CKPT_E2M1)
-        pack_t_kernel<DT, kE2m1><<<grid, block, 0, stream>>>(x, ld, rows, cols, ckpt, turns, tiles_c, tiles);
-    else if (fmt == ZR_CKPT_E4M3)
-        pack_t_kernel<DT, kE4m3><<<grid, block, 0, stream>>>(x, ld, rows, cols, ckpt, turns, tiles_c, tiles);
+    if (many)
+        pack_t_kernel<DT, FMT, TURNS><<<grid, block, 0, stream>>>(x, ld, rows, cols, ckpt, tiles_c, tiles);
     else
-        pack_t_kernel<DT, kInt8><<<grid, block, 0, stream>>>(x, ld, rows, cols, ckpt, turns, tiles_c, tiles);
+        pack_t_kernel<DT, FMT, 1><<<grid, block, 0, stream>>>(x, ld, rows, cols, ckpt, tiles_c, tiles);
+}
+
+template <int DT>
+void pack_t_pick(const void* x, int64_t ld, int64_t rows, int64_t cols, char* ckpt, zr_dtype fmt, hipStream_t stream) {
+    if (fmt == ZR_CKPT_E2M1)
+        pack_t_run<DT, kE2m1>(x, ld, rows, cols, ckpt, stream);
+    else if (fmt == ZR_CKPT_E4M3)
+        pack_t_run<DT, kE4m3>(x, ld, rows, cols, ckpt, stream);
+    else
+        pack_t_run<DT, kInt8>(x, ld, rows, cols, ckpt, stream);
 }
 
 int64_t tiles_of(int64_t rows, int64_t cols) { return (rows * (ckpt_pitch(cols) / 8) + kTile - 1) / kTile; }
@@ -285,9 +305,9 @@ hipError_t launch_unpack_small(const void* ckpt, int64_t rows, int64_t cols, voi
 hipError_t launch_pack_t(const void* x, zr_dtype dt, int64_t rows, int64_t cols, int64_t ld, void* ckpt, zr_dtype fmt,
                          hipStream_t stream) {
     if (dt == ZR_BF16)
-        pack_t_run<kBf16>(x, ld, rows, cols, (char*)ckpt, fmt, stream);
+        pack_t_pick<kBf16>(x, ld, rows, cols, (char*)ckpt, fmt, stream);
     else
-        pack_t_run<kFp32>(x, ld, rows, cols, (char*)ckpt, fmt, stream);
+        pack_t_pick<kFp32>(x, ld, rows, cols, (char*)ckpt, fmt, stream);
     return hipGetLastError();
 }
 
