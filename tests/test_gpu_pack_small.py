@@ -106,6 +106,24 @@ def test_transposed(rows, cols):
             assert np.array_equal(got[:want.size], want) and (got[want.size:] == 0x55).all()
 
 
+@pytest.mark.parametrize("rows,cols", [(2070, 16200), (4100, 8200), (2 * 32 * 2049, 250)])
+def test_transposed_large(rows, cols):
+    """Enough tiles that a lane takes several blocks, the last lanes fewer: as the transpose packed by rows."""
+    import torch
+    z = zr()
+    g = torch.Generator("cuda").manual_seed(rows)
+    for dt in (torch.bfloat16, torch.float32):
+        x = (torch.randn(rows, cols + 3, generator=g, device="cuda") * torch.exp(2 * torch.randn(rows, 1, generator=g, device="cuda"))).to(dt)
+        x[5, 7], x[rows - 1, cols - 1] = float("nan"), float("inf")
+        x, xt = x[:, :cols], x[:, :cols].t().contiguous()
+        for fmt in (pk.E2M1, pk.E4M3, z.ZR_CKPT_INT8):
+            n = z.zr_ckpt_format_bytes(cols, rows, fmt)
+            got, want = (torch.full((n + 64,), 0x55, dtype=torch.uint8, device="cuda") for _ in range(2))
+            z.zr_ckpt_pack_t(x, rows, cols, got, format=fmt, ld=cols + 3)
+            z.zr_ckpt_pack(xt, cols, rows, want, format=fmt)
+            assert torch.equal(got, want)
+
+
 def test_special_values():
     """Zeros of both signs, subnormals, the largest values, NaN and infinities, ties, each in a block of its own."""
     import torch
