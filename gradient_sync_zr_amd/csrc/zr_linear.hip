@@ -470,22 +470,18 @@ __global__ __launch_bounds__(kThreads) void linear_join_kernel(LinArgs a) {
 // -------------------------------------------------------------- few rows
 // Up to 64 tokens: the weight's bytes count, and each goes from memory to the
 // matrix instruction's registers once. A block of 8 waves takes 16 outputs; its
-// waves take every 8th step of 128 columns, with the loads of 4 steps in flight,
-// and are added in LDS. (Rows of codes too long for the tiled form's 32-bit
+// waves take every 8th turn of 512 columns, in 4 steps whose loads are in flight
+// at once, with a turn's exponents in one load, and are added in LDS. (Rows of codes too long for the tiled form's 32-bit
 // offsets come here too, 64 tokens at a time.) One token by 4096x4096 of e4m3 takes 5.4
 // to 5.9 us: 16.8 MB at 3.0 TB/s, of which a launch alone is 3.6.
-template <int FMT, bool EXACT>
 struct Piece {  // a row's 128 codes, one lane's quarter
     u32x4 p, q;
-    uint32_t s, s2;
 };
 
 template <int FMT, bool EXACT>
-__device__ __forceinline__ Piece<FMT, EXACT> piece(const char* row, const uint8_t* exps, int64_t bytes, int64_t sp, int64_t s,
-                                                   int g) {
-    Piece<FMT, EXACT> v;
+__device__ __forceinline__ Piece piece(const char* row, int64_t bytes, int64_t s, int g) {
+    Piece v;
     auto within = [&](int64_t at, int n) { return at < bytes - n ? at : bytes - n; };
-    auto byte = [&](int64_t b) { return b < sp ? (uint32_t)exps[b] : 0u; };
     if constexpr (FMT == kE2m1 && !EXACT) {
         v.p = *(const u32x4*)(row + within(s * 64 + g * 16, 16));
         v.q = u32x4{0, 0, 0, 0};
@@ -497,14 +493,24 @@ __device__ __forceinline__ Piece<FMT, EXACT> piece(const char* row, const uint8_
         v.p = *(const u32x4*)(row + within(s * 128 + g * 16, 16));
         v.q = *(const u32x4*)(row + within(s * 128 + 64 + g * 16, 16));
     }
-    if constexpr (EXACT) {
-        v.s = byte(s * 4 + g / 2);
-        v.s2 = byte(s * 4 + 2 + g / 2);
-    } else {
-        v.s = byte(s * 4 + g);
-        v.s2 = 0;
-    }
     return v;
+}
+
+// A lane's exponents of a row's turn, a byte for each of its 4 steps: of block g, or,
+// where operands are decoded, of the blocks of its two pieces.
+template <bool EXACT>
+struct Exps {
+    uint32_t p, q;
+};
+template <bool EXACT>
+__device__ __forceinline__ Exps<EXACT> turn_exps(const uint8_t* exps, int64_t row, int64_t rows, int64_t sp, int64_t turn, int g) {
+    const int64_t left = (rows - row) * sp;  // to the buffer's end
+    const u32x4 v = exponents16(exps + row * sp, 0, (int)turn * 16, (int)sp, left < (1 << 30) ? (int)left : 1 << 30);
+    auto column = [&](int b) {
+        const uint32_t sel = 0x0c0c0400u + 0x0101u * (uint32_t)b;
+        return __builtin_amdgcn_perm(v.y, v.x, sel) | __builtin_amdgcn_perm(v.w, v.z, sel) << 16;
+    };
+    return EXACT ? Exps<EXACT>{column(g / 2), column(2 + g / 2)} : Exps<EXACT>{column(g), 0};
 }
 
 template <int FW, int FX, bool EXACT, int NG>
@@ -516,45 +522,59 @@ __global__ __launch_bounds__(512) void linear_few_kernel(LinArgs a) {
         const int64_t tt = item / a.tiles_o, t0 = tt * (NG * 16), o0 = (item - tt * a.tiles_o) * 16;
         const int64_t o = o0 + r < a.out ? o0 + r : a.out - 1;
         const char* const w = a.w + o * a.wrow;
-        const uint8_t* const ws = a.ws + o * a.sp;
         f32x4 acc[NG];
 #pragma unroll
         for (int n = 0; n < NG; ++n) acc[n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        for (int64_t s = wave; s < a.turns * (kLinearGroup / 128); s += 8 * U) {
-            Piece<FW, EXACT> fw[U];
-            Piece<FX, EXACT> fx[U][NG];
+        for (int64_t turn = wave; turn < a.turns; turn += 8) {
+            const Exps<EXACT> ew = turn_exps<EXACT>(a.ws, o, a.out, a.sp, turn, g);
+            int64_t t[NG];
+            Exps<EXACT> ex[NG];
 #pragma unroll
-            for (int u = 0; u < U; ++u) fw[u] = piece<FW, EXACT>(w, ws, a.wrow, a.sp, s + 8 * u, g);
+            for (int n = 0; n < NG; ++n) {
+                t[n] = t0 + n * 16 + r < a.rows ? t0 + n * 16 + r : a.rows - 1;
+                ex[n] = turn_exps<EXACT>(a.xs, t[n], a.rows, a.sp, turn, g);
+            }
+            auto half = [&](auto U0) {
+                constexpr int u0 = decltype(U0)::value;
+                Piece fw[U], fx[U][NG];
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+                for (int u = 0; u < U; ++u) fw[u] = piece<FW, EXACT>(w, a.wrow, turn * 4 + u0 + u, g);
 #pragma unroll
-                for (int n = 0; n < NG; ++n) {
-                    const int64_t t = t0 + n * 16 + r < a.rows ? t0 + n * 16 + r : a.rows - 1;
-                    fx[u][n] = piece<FX, EXACT>(a.x + t * a.xrow, a.xs + t * a.sp, a.xrow, a.sp, s + 8 * u, g);
-                }
+                for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+                    for (int n = 0; n < NG; ++n) fx[u][n] = piece<FX, EXACT>(a.x + t[n] * a.xrow, a.xrow, turn * 4 + u0 + u, g);
+                auto step = [&](auto UU) {
+                    constexpr int u = decltype(UU)::value, k = u0 + u;  // of the turn
 #pragma unroll
-                for (int n = 0; n < NG; ++n) {
-                    const auto &p = fw[u];
-                    const auto &q = fx[u][n];
-                    if constexpr (EXACT) {
-                        bf16x8 x[2], y[2];
-                        decode16<FW>(p.p, scale_of(p.s), x);
-                        decode16<FX>(q.p, scale_of(q.s), y);
-                        acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[0], y[0], acc[n], 0, 0, 0);
-                        acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[1], y[1], acc[n], 0, 0, 0);
-                        decode16<FW>(p.q, scale_of(p.s2), x);
-                        decode16<FX>(q.q, scale_of(q.s2), y);
-                        acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[0], y[0], acc[n], 0, 0, 0);
-                        acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[1], y[1], acc[n], 0, 0, 0);
-                    } else {
-                        const i32x8 x = {(int)p.p.x, (int)p.p.y, (int)p.p.z, (int)p.p.w, (int)p.q.x, (int)p.q.y, (int)p.q.z, (int)p.q.w};
-                        const i32x8 y = {(int)q.p.x, (int)q.p.y, (int)q.p.z, (int)q.p.w, (int)q.q.x, (int)q.q.y, (int)q.q.z, (int)q.q.w};
-                        acc[n] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, acc[n], FW == kE2m1 ? 4 : 0, FX == kE2m1 ? 4 : 0,
-                                                                                  0, (int)p.s, 0, (int)q.s);
+                    for (int n = 0; n < NG; ++n) {
+                        const Piece &p = fw[u], &q = fx[u][n];
+                        if constexpr (EXACT) {
+                            bf16x8 x[2], y[2];
+                            decode16<FW>(p.p, scale_of((ew.p >> (8 * k)) & 255), x);
+                            decode16<FX>(q.p, scale_of((ex[n].p >> (8 * k)) & 255), y);
+                            acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[0], y[0], acc[n], 0, 0, 0);
+                            acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[1], y[1], acc[n], 0, 0, 0);
+                            decode16<FW>(p.q, scale_of((ew.q >> (8 * k)) & 255), x);
+                            decode16<FX>(q.q, scale_of((ex[n].q >> (8 * k)) & 255), y);
+                            acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[0], y[0], acc[n], 0, 0, 0);
+                            acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[1], y[1], acc[n], 0, 0, 0);
+                        } else {
+                            const i32x8 x = {(int)p.p.x, (int)p.p.y, (int)p.p.z, (int)p.p.w, (int)p.q.x, (int)p.q.y, (int)p.q.z, (int)p.q.w};
+                            const i32x8 y = {(int)q.p.x, (int)q.p.y, (int)q.p.z, (int)q.p.w, (int)q.q.x, (int)q.q.y, (int)q.q.z, (int)q.q.w};
+                            acc[n] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, acc[n], FW == kE2m1 ? 4 : 0,
+                                                                                      FX == kE2m1 ? 4 : 0, k, (int)ew.p, k, (int)ex[n].p);
+                        }
                     }
+                };
+                step(std::integral_constant<int, 0>{});
+                step(std::integral_constant<int, 1>{});
+                if constexpr (U == 4) {
+                    step(std::integral_constant<int, 2>{});
+                    step(std::integral_constant<int, 3>{});
                 }
+            };
+            half(std::integral_constant<int, 0>{});
+            if constexpr (U == 2) half(std::integral_constant<int, 2>{});
         }
 #pragma unroll
         for (int n = 0; n < NG; ++n) red[wave][n][lane] = acc[n];
