@@ -15,6 +15,11 @@ spills. A kernel may still reserve a small frame that no instruction uses:
 the compiler keeps one when it parks scalar registers in vector-register
 lanes (generic-K variants under high scalar pressure); that costs nothing and
 is allowed.
+
+It also fails if a load to LDS follows too closely on what it reads from scalar
+registers. The compiler keeps these distances for its own instructions and not
+for those inside an asm statement: one wait state from a scalar write of M0, five
+from a vector instruction's write of the address's registers.
 """
 import concurrent.futures as cf
 import os
@@ -75,6 +80,42 @@ def scratch_access_kernels(asm: str):
     return bad
 
 
+_LDS_LOAD = re.compile(r"(?:global|buffer|scratch)_load_(?:lds_\w+|\w+\s.*\blds\b)")
+_SGPRS = re.compile(r"s(?:(\d+)|\[(\d+):(\d+)\])$")
+
+
+def _sgprs(operand: str):
+    m = _SGPRS.match(operand.strip())
+    if not m:
+        return set()
+    return {int(m.group(1))} if m.group(1) else set(range(int(m.group(2)), int(m.group(3)) + 1))
+
+
+def unwaited_lds_loads(asm: str):
+    """(line, instruction) of every load to LDS in the device assembly that stands less than one wait state
+    behind a scalar write of M0, or less than five behind a vector instruction's write of a scalar register
+    that it reads. Instructions are taken in their order in the file, as one wait state each (s_nop n: n + 1)."""
+    bad, seen = [], []
+    for number, line in enumerate(asm.split("\n"), 1):
+        text = line.split(";")[0].strip()
+        if not text or text.startswith((".", "#", "//")) or text.endswith(":"):
+            continue
+        name, _, rest = text.partition(" ")
+        operands = rest.split(",")
+        if _LDS_LOAD.match(text):
+            reads = set().union(*(_sgprs(o.split()[0]) for o in operands if o.split()))
+            waits = 0
+            for op, args in reversed(seen):
+                first = args[0].strip() if args else ""
+                if (waits < 1 and op.startswith("s_") and first == "m0") or \
+                        (waits < 5 and op.startswith("v_") and _sgprs(first) & reads):
+                    bad.append((number, text))
+                    break
+                waits += int(first, 0) + 1 if op == "s_nop" else 1
+        seen = (seen + [(name, operands)])[-6:]
+    return bad
+
+
 def _compile(src, verbose):
     stem = os.path.splitext(src)[0]
     out = os.path.join(OBJ, stem + ".o")
@@ -93,9 +134,14 @@ def _compile(src, verbose):
             raise RuntimeError(f"{src}: kernels that spill VGPRs:\n{listing}")
         asm_path = os.path.join(OBJ, f"{stem}-hip-amdgcn-amd-amdhsa-{ARCH}.s")
         with open(asm_path) as fh:
-            bad = scratch_access_kernels(fh.read())
+            asm = fh.read()
+        bad = scratch_access_kernels(asm)
         if bad:
             raise RuntimeError(f"{src}: kernels that access scratch memory:\n  " + "\n  ".join(bad))
+        bad = unwaited_lds_loads(asm)
+        if bad:
+            raise RuntimeError(f"{src}: loads to LDS without the wait states in front of them:\n" +
+                               "\n".join(f"  line {n}: {i}" for n, i in bad[:20]))
         # the other temporaries are not needed
         for f in os.listdir(OBJ):
             if (f.startswith(stem + "-") or f.startswith(stem + ".hip-")) and \

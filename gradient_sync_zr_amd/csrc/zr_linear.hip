@@ -144,9 +144,12 @@ typedef __attribute__((address_space(3))) char* lptr;
 // plus `down` plus 16 times the lane. Written in assembly because the compiler, which cannot
 // tell the stages apart, waits for its own such loads before every read of LDS;
 // the kernel waits once, in front of the barrier that publishes a stage. There
-// is no register that the load still writes to.
+// is no register that the load still writes to. A scalar write of M0 has to be one wait
+// state ahead of a load to LDS, which takes its place from M0; nobody else puts it in
+// (the compiler inserts nothing inside an asm, and uses M0 for nothing else here), and
+// the build reads the unit's machine code for it.
 __device__ __forceinline__ void load_lds16(const char* base, uint32_t offset, uint32_t to, int down) {
-    asm volatile("s_add_u32 m0, %0, %3\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(offset), "s"(base), "i"(down)
+    asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(offset), "s"(base), "i"(down)
                  : "m0", "scc", "memory");
 }
 
