@@ -178,6 +178,14 @@ __device__ __forceinline__ void wait_loads() {
     asm volatile("s_waitcnt vmcnt(%0)" ::"i"(N) : "memory");
 }
 
+// Orders what a wave's lanes wrote to LDS before what its other lanes read behind this,
+// for the compiler: a wave's LDS accesses are carried out in their order, so it costs no
+// instruction.
+__device__ __forceinline__ void wave_lds_order() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
 // A tile's product. Eight (four) waves have WO outputs of WT tokens each; the
 // weight's rows are the matrix instructions' A, so that a lane ends with one token
 // and neighbouring outputs.
@@ -436,6 +444,7 @@ __global__ __launch_bounds__((BO / WO) * (BT / WT) * 64, 2) void linear_kernel(L
                     *(f32x4*)(own + rr * (WO * 4) + ((c ^ (rr & (CH - 1))) << 4)) =
                         f32x4{acc[m][n][4 * k], acc[m][n][4 * k + 1], acc[m][n][4 * k + 2], acc[m][n][4 * k + 3]};
                 }
+            wave_lds_order();
             __builtin_amdgcn_sched_barrier(0);
             const int64_t o = o0 + wo * WO + (ol % LANES) * 8;
 #pragma unroll 1
@@ -448,6 +457,7 @@ __global__ __launch_bounds__((BO / WO) * (BT / WT) * 64, 2) void linear_kernel(L
                 const float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
                 put8(a, mine, tok, o, v);
             }
+            wave_lds_order();
             __builtin_amdgcn_sched_barrier(0);
         }
     }

@@ -1,5 +1,5 @@
-"""Loads to LDS stand far enough behind the writes of the scalar registers that they read: the build's check of
-its machine code, on listings and on the product's own, compiled here."""
+"""Loads to LDS stand far enough behind the writes of the scalar registers that they read (the build's check of
+its machine code, on listings and on the product's own, compiled here), and results exchanged over LDS are ordered."""
 import os
 import subprocess
 
@@ -49,3 +49,26 @@ def test_product(product):
     writes = [x for x in product.split("\n") if "m0" in x.split(";")[0].replace(",", " ").split()]
     assert loads and len(writes) == len(loads)      # M0 is used for nothing else
     assert _build.unwaited_lds_loads(product) == []
+
+
+def test_results_exchanged_over_lds_are_ordered(tmp_path):
+    """The tiled product's results go through LDS within a wave: between one lane's writes and another's reads, and
+    between those and the next writes, the compiler has a fence in every form."""
+    out = tmp_path / "zr_linear.ll"
+    cmd = [_build.HIPCC] + [f for f in _build.FLAGS if f != "-fPIC"] + \
+          ["--offload-device-only", "-emit-llvm", "-S", os.path.join(_build.CSRC, "zr_linear.hip"), "-o", str(out)]
+    r = subprocess.run(cmd, capture_output=True, text=True, timeout=900)
+    assert r.returncode == 0, r.stderr[-3000:]
+    forms = [f for f in out.read_text().split("\ndefine ")[1:] if "13linear_kernel" in f.split("\n", 1)[0]]
+    assert len(forms) == 14
+    for form in forms:
+        order = ""
+        for line in form.split("\n}", 1)[0].split("\n"):
+            if "store <4 x float>" in line and "ptr addrspace(3)" in line:
+                order += "w"
+            elif "load <4 x float>, ptr addrspace(3)" in line:
+                order += "r"
+            elif 'fence syncscope("wavefront")' in line:
+                order += "|"
+        groups = [{*g} for g in order.split("|") if g]
+        assert len(groups) == 4 and all(len(g) == 1 for g in groups), order
