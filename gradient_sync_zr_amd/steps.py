@@ -266,9 +266,12 @@ class PackedNormLinear:
                 layers that run one after another on a stream may share it, others
                 must not
 
-        pack_weight(W)                                   after every update of W
-        forward(x, norm_weight, z, residual=r, h=h)      z = norm(x + r) W^T + b
-        backward(dz, norm_weight, dx)                    the flat gradient, and dx
+        pack_weight(W)                                        after every update of W
+        forward(x, norm_weight, z, residual=r, h=h, bias=b)   z = norm(x + r) W^T + b
+        backward(dz, norm_weight, dx)                         the flat gradient, and dx
+
+    forward takes a bias where the layer was made with `bias` (the default), and only
+    there: its gradient's place in the flat gradient is written by every backward pass.
 
     dx is the gradient of h = x + r, so of x and of the residual; with add_dx it is
     added to what passed by the norm. h is kept as an 8-bit checkpoint: h, x and the
@@ -324,6 +327,9 @@ class PackedNormLinear:
         """z (rows x out_cols) of x and the residual, whose sum goes to h."""
         if not self._packed:
             raise ValueError("forward before pack_weight")
+        if (bias is not None) != (self.db is not None):
+            raise ValueError("the flat gradient has a place for the bias's gradient, and forward has no bias" if bias is None
+                             else "forward has a bias, and the layer was made with bias=False")
         zr_rmsnorm_fwd(x, self.rows, self.cols, None, norm_weight, eps=self.eps, residual=residual, h=h,
                        rstd=self.rstd, ckpt_h=self.ckpt_h, ckpt_y=self.ckpt_y, stream=stream)
         zr_ckpt_linear(self.ckpt_y, self.w, self.rows, self.cols, self.out_cols, z, bias=bias,
