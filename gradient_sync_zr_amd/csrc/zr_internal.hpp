@@ -337,7 +337,7 @@ struct GradNorm {
     void* workspace;  // of grad_norm_parts() doubles
 };
 ZR_KERNELS hipError_t launch_grad_norm(const GradNorm& f, hipStream_t stream);
-inline int64_t grad_norm_parts(int n) { return (int64_t)((n + kNormPer - 1) / kNormPer) * kNormBlocks; }
+inline int64_t grad_norm_parts(int n) { return ((int64_t)n + kNormPer - 1) / kNormPer * kNormBlocks; }
 
 struct GradScale {
     int n;

@@ -124,3 +124,10 @@ def test_tensors_are_checked():
         zr.zr_grad_norm(t, [5, 6, 8], B, workspace=(C, 1 << 20), stream=0)
     with pytest.raises(ValueError, match="dtype argument"):
         zr.zr_grad_norm(t, [5, 6, 7], B, workspace=(C, 1 << 20), dtype=BF, stream=0)
+
+
+def test_workspace_of_the_longest_lists():
+    """No size is formed in 32 bits on the way."""
+    top = 2 ** 31 - 1
+    for n in (top, top - 190, top - 191, 1 << 30):
+        assert zr.zr_grad_norm_workspace_bytes(n) == -(-n // 192) * 2048 * 8
