@@ -684,7 +684,8 @@ zr_status zr_ckpt_wgrad(const void* dy, zr_dtype dy_dt, int64_t ld_dy, const voi
  * RMS norm with the residual's addition, forward. For every row:
  *     h = x + residual, rounded to h_dt (h = x without a residual)
  *     rstd = 1 / sqrt(sum(h^2) / cols + eps),  y = h * rstd * weight
- * in fp32 of the rounded h, y rounded once to its type.
+ * in fp32 of the rounded h, y rounded once to its type. A row whose squares' sum
+ * passes fp32 (a value of 2^64 alone does) has rstd 0 and y 0.
  *
  *  x          as in zr_layernorm_fwd: values, or a checkpoint
  *  residual   rows x cols of h_dt (ZR_BF16 or ZR_FP32), row stride ld_res, or NULL
