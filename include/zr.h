@@ -698,7 +698,8 @@ zr_status zr_ckpt_wgrad(const void* dy, zr_dtype dy_dt, int64_t ld_dy, const voi
  *  rstd       fp32, rows elements, or NULL
  *  ckpt_h     NULL, or a checkpoint that receives h (not where h is the checkpoint x)
  *  ckpt_y     NULL, or a checkpoint that receives y as rounded to y_dt (with y NULL
- *             too): y in 8 bits with scales, what zr_ckpt_linear and zr_ckpt_wgrad read
+ *             too): y in 8 bits with scales, what zr_ckpt_wgrad reads and, in e4m3,
+ *             zr_ckpt_linear
  *  ckpt_format    ZR_CKPT_E4M3 or ZR_CKPT_INT8, of ckpt_h and ckpt_y
  * At least one output, if there are rows; outputs overlap neither each other nor
  * an input, but h or y may be x or the residual (same address, type and row
