@@ -338,8 +338,6 @@ bool mats_overlap(const Mat& a, const Mat& b) {
     return gap < a.width || gap + b.width > a.pitch;
 }
 
-// Buffers of a call: outputs must be disjoint from each other and from the
-// inputs, but for the pairs that `same` allows at equal address and shape.
 // An output that may lie where an input does (same address, row stride and width), if
 // `ok`: the elements are of one type.
 struct Place {
@@ -347,6 +345,8 @@ struct Place {
     bool ok;
 };
 
+// Buffers of a call: outputs must be disjoint from each other and from the
+// inputs, but for the pairs that `disjoint` is told of.
 struct Buffers {
     struct List {  // no call has more than 8 of either
         Mat m[8];

@@ -72,8 +72,7 @@ __device__ __forceinline__ void e2m1_decode8(uint32_t q, float scale, float f[8]
     for (int e = 0; e < 8; ++e) f[e] *= scale;
 }
 
-// Exponent byte and codes of 8 values by a format known at compile time: one word
-// (e2m1) or two.
+// Exponent byte of a block, by a format known at compile time.
 template <int FMT>
 __device__ __forceinline__ uint32_t format_byte(uint32_t amax) {
     return FMT == kE2m1 ? e2m1_byte(amax) : ckpt_byte(amax, FMT == kE4m3);

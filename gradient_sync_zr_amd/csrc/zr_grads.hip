@@ -59,7 +59,7 @@ __device__ __forceinline__ void put_norm(const NormOut& o, double sum) {
     if (o.coef) *o.coef = (float)coef;
 }
 
-// Vectors of a lane in a tile: of 16 bytes (16 of 4 elements, or 8 of 8).
+// Vectors of a lane in a tile, of 16 bytes: 8 of 4 fp32 elements, or 4 of 8 bf16.
 template <typename T>
 constexpr int kNormVecs = kNormTile / kThreads / (16 / (int)sizeof(T));
 

@@ -412,7 +412,8 @@ ZR_KERNELS hipError_t launch_linear(const Linear& f, hipStream_t stream);
 // best measured (decoded; 10% else), and 1% in the mean:
 //  - a tile takes kStart, which has the results' writing in it, and kTurn for every turn,
 //    the first of each with few blocks on the chip, the second with all places taken
-//    (512 of form 1, 256 of form 2), in us;
+//    (512 of form 1, 256 of form 2: of a whole MI355X, whatever the current device has,
+//    because the workspace's size follows from the cut and is asked for on the host), in us;
 //  - joining costs 4 us and 0.4 us per MB of parts;
 //  - form 0 reads the tokens again for every 16 outputs: 4.5 us, and kFew for every turn
 //    of up to 16, 32 and 64 tokens (half of the first for a single one), more beyond
