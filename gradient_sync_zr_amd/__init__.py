@@ -93,7 +93,7 @@ NORM_EXPORTS = ("zr_ckpt_pack", "zr_ckpt_unpack", "zr_layernorm_fwd", "zr_layern
                 "zr_ckpt_bytes", "zr_layernorm_workspace_bytes", "zr_ckpt_wgrad_workspace_bytes")
 RMS_EXPORTS = ("zr_rmsnorm_fwd", "zr_rmsnorm_bwd", "zr_ckpt_pack_t", "zr_ckpt_linear", "zr_ckpt_format_bytes",
                "zr_rmsnorm_workspace_bytes", "zr_ckpt_linear_workspace_bytes")
-GRAD_EXPORTS = ("zr_grad_norm", "zr_grad_scale", "zr_adamw", "zr_grad_norm_workspace_bytes")
+GRAD_EXPORTS = ("zr_grad_norm", "zr_grad_scale", "zr_adamw", "zr_adamw_counted", "zr_grad_norm_workspace_bytes")
 EXPORTS = ("zr_last_error", "zr_version", "zr_workspace_bytes", "zr_flatten_bucket", "zr_reduce_scatter_avg",
            "zr_reduce_scatter_frags", "zr_all_gather", "zr_allreduce", "zr_plan_buckets", "zr_sched_create",
            "zr_sched_acquire", "zr_sched_submit_rs", "zr_sched_flush",
@@ -225,6 +225,7 @@ def lib() -> ctypes.CDLL:
         L.zr_grad_norm.argtypes = [_i32, _vp, _vp, _i32, _d, _d, _vp, _vp, _vp, _sz, _vp]
         L.zr_grad_scale.argtypes = [_i32, _vp, _vp, _i32, _vp, _i32, _vp, _vp]
         L.zr_adamw.argtypes = [_i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp] + [_d] * 5 + [_i64, _vp, _vp]
+        L.zr_adamw_counted.argtypes = L.zr_adamw.argtypes[:-1] + [_vp, _vp]
         L.zr_grad_norm_workspace_bytes.argtypes = [_i32]
         L.zr_grad_norm_workspace_bytes.restype = _sz
         for f in ("zr_cost_ring_allreduce", "zr_cost_ring_reduce_scatter",
@@ -1148,6 +1149,15 @@ def _scalar(x, name):
     return _vector(x, 1, ZR_FP32, name)[0]
 
 
+def _counter(x, name):
+    """Address of one int64 on the device: a tensor of one element, or an address."""
+    if x.__class__ is int:
+        return x
+    if x.numel() != 1 or x.element_size() != 8 or x.is_floating_point():
+        raise ValueError(f"{name} is not 1 element of int64")
+    return x.data_ptr()
+
+
 def zr_grad_norm_workspace_bytes(n: int) -> int:
     return lib().zr_grad_norm_workspace_bytes(n)
 
@@ -1181,17 +1191,23 @@ def zr_grad_scale(grads, numels: Sequence[int], coef, outs=None, dtype=None, out
 
 def zr_adamw(grads, numels: Sequence[int], params, exp_avg, exp_avg_sq, step: int, lr: float, beta1: float = 0.9,
              beta2: float = 0.999, eps: float = 1e-8, weight_decay: float = 0.01, shards=None, coef=None, dtype=None,
-             stream=None) -> None:
+             stream=None, left_out=None) -> None:
     """One AdamW update of the fp32 params and their moments from coef * grads
     (coef: one fp32 on the GPU, of zr_grad_norm; the update is left out where it
     is not finite); shards, if given, receive the params in bf16. Lists as in
-    zr_grad_norm; `dtype` is that of grads given as addresses."""
+    zr_grad_norm; `dtype` is that of grads given as addresses. left_out: one int64
+    on the GPU that counts the updates left out; this one's number is then `step`
+    less those (zr_adamw_counted)."""
     gpus, sizes = [], _sizes(numels)
     t, dt = _many(grads, numels, sizes, dtype, "grads", gpus)
     p, m, v = (_many(xs, numels, sizes, ZR_FP32, name, gpus)[0]
                for xs, name in ((params, "params"), (exp_avg, "exp_avg"), (exp_avg_sq, "exp_avg_sq")))
     s = None if shards is None else _many(shards, numels, sizes, ZR_BF16, "shards", gpus)[0]
-    st = lib().zr_adamw(len(numels), _at(t), dt, _at(sizes), _at(p), _at(m), _at(v), None if s is None else _at(s), lr,
-                        beta1, beta2, eps, weight_decay, step, _scalar(coef, "coef"), _run_on_gpus(stream, gpus, coef))
+    args = (len(numels), _at(t), dt, _at(sizes), _at(p), _at(m), _at(v), None if s is None else _at(s), lr, beta1, beta2,
+            eps, weight_decay, step, _scalar(coef, "coef"))
+    if left_out is None:
+        st = lib().zr_adamw(*args, _run_on_gpus(stream, gpus, coef))
+    else:
+        st = lib().zr_adamw_counted(*args, _counter(left_out, "left_out"), _run_on_gpus(stream, gpus, coef, left_out))
     if st:
         _check(st)

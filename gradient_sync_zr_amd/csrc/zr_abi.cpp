@@ -1497,6 +1497,14 @@ zr_status zr_grad_scale(int n, const void* const* grads, const int64_t* numels, 
 zr_status zr_adamw(int n, const void* const* grads, zr_dtype grad_dt, const int64_t* numels, void* const* params,
                    void* const* exp_avg, void* const* exp_avg_sq, void* const* shards, double lr, double beta1,
                    double beta2, double eps, double weight_decay, int64_t step, const float* coef, void* stream) {
+    return zr_adamw_counted(n, grads, grad_dt, numels, params, exp_avg, exp_avg_sq, shards, lr, beta1, beta2, eps,
+                            weight_decay, step, coef, nullptr, stream);
+}
+
+zr_status zr_adamw_counted(int n, const void* const* grads, zr_dtype grad_dt, const int64_t* numels,
+                           void* const* params, void* const* exp_avg, void* const* exp_avg_sq, void* const* shards,
+                           double lr, double beta1, double beta2, double eps, double weight_decay, int64_t step,
+                           const float* coef, int64_t* left_out, void* stream) {
     return zr::guarded([&]() -> zr_status {
         if (!dt_valid(grad_dt)) return fail(ZR_ERR_UNSUPPORTED, "dtype %d not supported", (int)grad_dt);
         ZR_TRY(check_tensors(n, grads, numels));
@@ -1506,20 +1514,23 @@ zr_status zr_adamw(int n, const void* const* grads, zr_dtype grad_dt, const int6
             return fail(ZR_ERR_INVALID, "lr=%g, eps=%g or weight_decay=%g is not >= 0 and finite", lr, eps, weight_decay);
         if (step < 1) return fail(ZR_ERR_INVALID, "step=%lld is below 1", (long long)step);
         Ranges r;
-        r.items.reserve((size_t)n * 5 + 1);
+        r.items.reserve((size_t)n * 5 + 2);
         ZR_TRY(check_list(&r, false, grads, numels, n, dt_bytes(grad_dt), "grads"));
         ZR_TRY(check_list(&r, true, (const void* const*)params, numels, n, 4, "params"));
         ZR_TRY(check_list(&r, true, (const void* const*)exp_avg, numels, n, 4, "exp_avg"));
         ZR_TRY(check_list(&r, true, (const void* const*)exp_avg_sq, numels, n, 4, "exp_avg_sq"));
         if (shards) ZR_TRY(check_list(&r, true, (const void* const*)shards, numels, n, 2, "shards"));
         ZR_TRY(check_scalar(&r, false, coef, "coef"));
+        if ((uintptr_t)left_out & 7)
+            return fail(ZR_ERR_ALIGN, "left_out=%p is not aligned to 8 bytes", (const void*)left_out);
+        r.add(true, left_out, left_out ? 1 : 0, 8, "left_out", 0);
         ZR_TRY(r.disjoint());
         ZR_TRY(have(launch_adamw, "AdamW"));
         AdamW f{};
         f.n = n; f.grads = grads; f.numels = numels; f.grad_dt = grad_dt;
         f.params = params; f.exp_avg = exp_avg; f.exp_avg_sq = exp_avg_sq; f.shards = shards;
         f.lr = lr; f.beta1 = beta1; f.beta2 = beta2; f.eps = eps; f.weight_decay = weight_decay;
-        f.step = step; f.coef = coef;
+        f.step = step; f.coef = coef; f.left_out = left_out;
         return launched(launch_adamw(f, (hipStream_t)stream), (hipStream_t)stream, "AdamW launch");
     });
 }

@@ -5,7 +5,9 @@
 //     v  = beta2 * v + (1 - beta2) * g'^2
 //     p  = (1 - lr * decay) * p - lr / (1 - beta1^t) * m / (sqrt(v / (1 - beta2^t)) + eps)
 // in fp32, and p rounded to bf16 as the shard that the all-gather takes. A
-// coefficient that is not finite leaves everything as it was.
+// coefficient that is not finite leaves everything as it was. Steps so left out may be
+// counted on the device: t is then the step less those, and the corrections come from
+// there, as the host does not know of them.
 //
 // A stream of 30 bytes per element (fp32 gradients, shards written), read and
 // written past the caches: 2^26 elements take 359 us (5.6 TB/s), 335 (5.6) from bf16
@@ -25,13 +27,38 @@ typedef Multi<5, kAdamPer> AdamTable;
 
 struct AdamArgs {
     const float* coef;
+    int64_t* left_out;  // steps left out so far, or null
+    int64_t step;
+    double lr, b1, b2;
     float beta1, rest1, beta2, rest2, keep, rate, inv2, eps;
+    int count;  // this launch counts the step that it leaves out
 };
+
+// b^t by squaring, t >= 1: off by less than t roundings of fp64.
+__device__ double power(double b, int64_t t) {
+    double r = 1.0;
+#pragma unroll 1
+    for (; t > 0; t >>= 1) {
+        if (t & 1) r *= b;
+        b *= b;
+    }
+    return r;
+}
 
 template <typename T>
 __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamTable t5, AdamArgs a, int shards) {
     const float coef = a.coef ? *a.coef : 1.0f;
-    if (!(__builtin_fabsf(coef) < __builtin_inff())) return;
+    if (!(__builtin_fabsf(coef) < __builtin_inff())) {
+        // nobody reads it in a step that is left out
+        if (a.count && blockIdx.x == 0 && threadIdx.x == 0) *a.left_out += 1;
+        return;
+    }
+    const int64_t less = a.left_out ? *a.left_out : 0;
+    if (less > 0) {  // the same for all; otherwise the host's corrections hold
+        const int64_t t = a.step - less > 1 ? a.step - less : 1;
+        a.rate = (float)(a.lr / (1.0 - power(a.b1, t)));
+        a.inv2 = (float)(1.0 / (1.0 - power(a.b2, t)));
+    }
     int slot = 0;
     const int tiles = t5.tile0[t5.count];
     for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
@@ -82,6 +109,10 @@ hipError_t launch_adamw(const AdamW& f, hipStream_t stream) {
                                          (const void* const*)f.exp_avg_sq, (const void* const*)f.shards};
     AdamArgs a{};
     a.coef = f.coef;
+    a.left_out = f.left_out;
+    a.step = f.step;
+    a.lr = f.lr; a.b1 = f.beta1; a.b2 = f.beta2;
+    a.count = f.left_out != nullptr;
     a.beta1 = (float)f.beta1; a.rest1 = (float)(1.0 - f.beta1);
     a.beta2 = (float)f.beta2; a.rest2 = (float)(1.0 - f.beta2);
     a.keep = (float)(1.0 - f.lr * f.weight_decay);
@@ -97,6 +128,7 @@ hipError_t launch_adamw(const AdamW& f, hipStream_t stream) {
             adamw_kernel<float><<<grid, kThreads, 0, stream>>>(m, a, f.shards != nullptr);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
+        a.count = 0;
     }
     return hipSuccess;
 }

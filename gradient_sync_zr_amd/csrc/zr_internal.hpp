@@ -358,6 +358,7 @@ struct AdamW {
     double lr, beta1, beta2, eps, weight_decay;
     int64_t step;
     const float* coef;
+    int64_t* left_out;  // may be null
 };
 ZR_KERNELS hipError_t launch_adamw(const AdamW& f, hipStream_t stream);
 

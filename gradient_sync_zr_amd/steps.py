@@ -366,9 +366,11 @@ class ClipAdamW:
     scale      : the gradients stand for scale * grads (1 / micro-steps, 1 / loss
                  scale)
 
-    step() counts the updates that it enqueues. `norm` and `coef` hold the last
-    step's; where the gradients are not finite, coef is not, and the step leaves the
-    parameters as they are (it counts all the same). The buffers keep their
+    step() counts the updates that it enqueues in `steps`. `norm` and `coef` hold the
+    last step's; where the gradients are not finite, coef is not, and the step leaves
+    the parameters as they are. `left_out`, one int64 on the device, counts those: the
+    corrections of the moments go by the updates that were made, steps - left_out. (A
+    program that goes on from a checkpoint sets both.) The buffers keep their
     addresses; on another stream than the one that is current when it is made, the
     object has to outlive what step() enqueues.
     """
@@ -385,7 +387,7 @@ class ClipAdamW:
         dev = params[0].device
         self.norm, self.coef = torch.zeros(1, device=dev), torch.zeros(1, device=dev)
         self._workspace = torch.empty(zr_grad_norm_workspace_bytes(len(self.numels)), dtype=torch.uint8, device=dev)
-        self.steps = 0
+        self.steps, self.left_out = 0, torch.zeros(1, dtype=torch.int64, device=dev)
 
     def step(self, lr: Optional[float] = None, stream=None) -> None:
         """One update, at rate lr (default: the object's)."""
@@ -394,5 +396,5 @@ class ClipAdamW:
                      workspace=self._workspace, stream=stream)
         zr_adamw(g, self.numels, p, m, v, self.steps + 1, self.lr if lr is None else lr, beta1=self.beta1,
                  beta2=self.beta2, eps=self.eps, weight_decay=self.weight_decay, shards=self._shards,
-                 coef=self.coef, stream=stream)
+                 coef=self.coef, left_out=self.left_out, stream=stream)
         self.steps += 1

@@ -845,11 +845,19 @@ zr_status zr_grad_scale(int n, const void* const* grads, const int64_t* numels, 
  *             arguments: a captured graph repeats them
  *  coef       one fp32 on the device (of zr_grad_norm), or NULL (1). Where it is
  *             not finite the step is left out: nothing is written
+ *  left_out   one int64 on the device, or NULL (as in zr_adamw): how many of the
+ *             steps before this one were left out. The update's number is then
+ *             step - *left_out (at least 1); a step that is left out adds 1 to it
+ *             (if there is an element to update)
  */
 zr_status zr_adamw(int n, const void* const* grads, zr_dtype grad_dt, const int64_t* numels, void* const* params,
                    void* const* exp_avg, void* const* exp_avg_sq, void* const* shards, double lr, double beta1,
                    double beta2, double eps, double weight_decay, int64_t step, const float* coef,
                    void* stream);
+zr_status zr_adamw_counted(int n, const void* const* grads, zr_dtype grad_dt, const int64_t* numels,
+                           void* const* params, void* const* exp_avg, void* const* exp_avg_sq, void* const* shards,
+                           double lr, double beta1, double beta2, double eps, double weight_decay, int64_t step,
+                           const float* coef, int64_t* left_out, void* stream);
 
 #ifdef __cplusplus
 }

@@ -131,3 +131,14 @@ def test_workspace_of_the_longest_lists():
     top = 2 ** 31 - 1
     for n in (top, top - 190, top - 191, 1 << 30):
         assert zr.zr_grad_norm_workspace_bytes(n) == -(-n // 192) * 2048 * 8
+
+
+def test_adamw_counter_refusals():
+    for bad in (G + 12, B + 8, A + 2 * GAP + 8, D + 2 * GAP + 3992):
+        expect(zr.ZR_ERR_ALIGN if bad == G + 12 else zr.ZR_ERR_ALIAS, adamw, left_out=bad)
+    expect(zr.ZR_ERR_ALIAS, adamw, left_out=G, coef=G + 4)
+    expect(zr.ZR_ERR_INVALID, adamw, left_out=G + 8, step=0)
+    import torch
+    for bad in (torch.zeros(1), torch.zeros(2, dtype=torch.int64), torch.zeros(1, dtype=torch.float64)):
+        with pytest.raises(ValueError, match="left_out is not 1"):
+            adamw(left_out=bad)
