@@ -409,17 +409,20 @@ ZR_KERNELS hipError_t launch_linear(const Linear& f, hipStream_t stream);
 // How a product of packed matrices is cut: form 0 for few rows, tiles of 128 x 128
 // (1) or 256 x 256 (2), and the columns in `parts` of `share` turns of 512, joined
 // from the workspace. The fastest by a model fitted to sweeps of 20 shapes (70 to 16384
-// rows) in both forms and up to 22 parts; its choices took at most 13% longer than the
-// best measured (decoded; 10% else), and 1% in the mean:
+// rows) in both forms of tiles and up to 22 parts, where its choices took at most 13%
+// longer than the best measured (decoded; 10% else), and 1% in the mean, and of 10 shapes
+// of up to 64 rows in all forms, where they took 3% longer in the mean and up to 41% (8
+// outer shapes that it was not fitted to: 2.5% and 49%, a single row by 100000x640):
 //  - a tile takes kStart, which has the results' writing in it, and kTurn for every turn,
 //    the first of each with few blocks on the chip, the second with all places taken
 //    (512 of form 1, 256 of form 2: of a whole MI355X, whatever the current device has,
 //    because the workspace's size follows from the cut and is asked for on the host), in us;
 //  - joining costs 4 us and 0.4 us per MB of parts;
-//  - form 0 reads the tokens again for every 16 outputs: 4.5 us, and kFew for every turn
-//    of up to 16, 32 and 64 tokens (half of the first for a single one), more beyond
-//    4096 outputs, which are more blocks than the chip has places (33 to 64 tokens of
-//    11008x4096 took 47 us where tiles take 23; of 777x1000 9 for 13).
+//  - form 0 reads the tokens again for every 16 outputs: 3.4 us, 0.44 for every 4096
+//    outputs, and kFew for every turn of 16, 32 and 64 tokens (a little over half of it is
+//    there without any), by as many times 4096 outputs as there are, for more blocks than
+//    the chip has CUs (64 tokens of 11008x4096 took 34 us where tiles take 17; 17 tokens of
+//    4096x11008 in 4 bits 10.4 for 13.8, and of 777x1000 in 8 bits 5.3 for 8.1).
 constexpr int kLinearGroup = 512;         // columns of a turn, of a load of exponents
 constexpr int64_t kLinearWide = 1 << 23;  // columns up to which a tile's rows lie within 32-bit offsets
 // What multiplies: scaled instructions with e4m3 on a side, or with e2m1 on both, or
@@ -434,12 +437,14 @@ inline LinearCut linear_cut(int64_t rows, int64_t out, int64_t in, LinearKind ki
                                               {{8.2f, 8.2f}, {8.7f, 8.7f}, {8.0f, 16.0f}, {8.0f, 16.0f}}};
     static constexpr float kTurn[2][4][2] = {{{1.5f, 4.2f}, {0.7f, 2.4f}, {2.4f, 6.6f}, {0.7f, 2.8f}},
                                              {{3.6f, 6.5f}, {1.9f, 4.0f}, {5.2f, 12.5f}, {1.7f, 4.2f}}};
-    static constexpr float kFew[4][3] = {{0.5f, 0.9f, 1.45f}, {0.26f, 0.5f, 0.95f}, {0.75f, 1.2f, 2.1f}, {0.26f, 0.5f, 0.95f}};
+    static constexpr float kFew[4][3] = {{0.38f, 0.60f, 1.09f}, {0.23f, 0.34f, 0.62f}, {0.50f, 0.70f, 1.25f}, {0.22f, 0.33f, 0.61f}};
     const int64_t turns = (in + kLinearGroup - 1) / kLinearGroup;
     LinearCut best{0, 1, turns, turns};
     if (in > kLinearWide) return best;
-    const float token = kFew[kind][rows <= 16 ? 0 : (rows <= 32 ? 1 : 2)] * (rows < 16 ? 0.5f + (float)rows / 32.0f : 1.0f);
-    const float few = 4.5f + (float)turns * token * (out > 4096 ? 1.25f * (float)out / 4096.0f : 1.0f);
+    const int most = rows <= 16 ? 0 : (rows <= 32 ? 1 : 2);
+    const float token = kFew[kind][most] * (0.57f + 0.43f * (float)rows / (float)(16 << most));
+    const float wide = (float)out / 4096.0f, blocks = wide > 1.0f ? wide : 1.0f;
+    const float few = 3.4f + 0.44f * blocks + (float)turns * token * (1.1f * wide > 1.0f ? 1.1f * wide : 1.0f);
     float least = rows <= 64 ? few : 3e38f;
     for (int f = 0; f < 2; ++f) {
         const int64_t edge = f ? 256 : 128, places = f ? 256 : 512;

@@ -112,3 +112,16 @@ print(json.dumps(out))
     assert got[11] == [("adamw_kernel", 64, 256)]
     assert got[12] == [("adamw_kernel", 128, 256)] * 2 + [("adamw_kernel", 4, 256)]
     assert len(got[13]) == 1 and all(b * t < 1 << 32 for g in got for _, b, t in g)
+
+
+def test_forms_of_up_to_64_rows():
+    """The border between the form of few rows and tiles, at sizes where one was measured to take a third less and more."""
+    b, c, d, e = (FAR * (i + 8) for i in range(1, 5))
+    lin = lambda rows, inn, out, x, w, z=BF: ("zr_ckpt_linear", [b, x, c, w, rows, inn, out, None, BF, d, z, out, 0, e, FAR, None])  # noqa: E731
+    few = [lin(17, 11008, 4096, E2, E2), lin(24, 11008, 4096, E2, E2), lin(33, 4096, 4096, E2, E2), lin(17, 4096, 512, E4, E4),
+           lin(8, 8192, 1024, E4, E4, FP), lin(24, 8192, 1024, E2, E2, FP), lin(17, 1000, 777, E4, E4), lin(40, 2560, 640, E4, E4, FP),
+           lin(1, 16384, 8192, E4, E2)]
+    tiles = [lin(64, 4096, 11008, E4, E4), lin(64, 4096, 11008, E2, E2), lin(8, 1024, 32768, E2, E2), lin(64, 16384, 8192, E4, E4),
+             lin(64, 2048, 16384, E4, E4), lin(33, 1024, 32768, E4, E4, FP)]
+    assert [k[0][0] for k in launches(few)] == ["linear_few_kernel"] * len(few)
+    assert [k[0][0] for k in launches(tiles)] == ["linear_kernel"] * len(tiles)
