@@ -28,7 +28,7 @@ from __future__ import annotations
 
 from typing import Callable, List, Optional, Sequence
 
-from . import (ZR_BF16, ZR_CKPT_E4M3, ZR_FP32, ZR_ORDER_RING, Sched, tensor_table, zr_adamw, zr_all_gather,
+from . import (ZR_BF16, ZR_CKPT_E2M1, ZR_CKPT_E4M3, ZR_FP32, ZR_ORDER_RING, Sched, tensor_table, zr_adamw, zr_all_gather,
                zr_ckpt_bytes, zr_ckpt_format_bytes, zr_ckpt_linear, zr_ckpt_linear_workspace_bytes, zr_ckpt_pack,
                zr_ckpt_pack_t, zr_ckpt_wgrad, zr_ckpt_wgrad_workspace_bytes, zr_grad_norm,
                zr_grad_norm_workspace_bytes, zr_layernorm_bwd, zr_layernorm_fwd, zr_layernorm_workspace_bytes,
@@ -285,6 +285,8 @@ class PackedNormLinear:
     def __init__(self, flat_grad, offset: int, rows: int, cols: int, out_cols: int, scratch=None,
                  weight_format: int = ZR_CKPT_E4M3, eps: float = 1e-5, bias: bool = True):
         import torch
+        if weight_format not in (ZR_CKPT_E4M3, ZR_CKPT_E2M1):
+            raise ValueError(f"weight_format {weight_format} is not one of the products', e4m3 or e2m1")
         self.rows, self.cols, self.out_cols = rows, cols, out_cols
         self.weight_format, self.eps = weight_format, eps
         sizes = [cols, out_cols * cols] + ([out_cols] if bias else [])

@@ -23,3 +23,13 @@ def test_bias_of_the_layer_and_of_the_call_agree():
         with pytest.raises(ValueError, match="not on the GPU"):  # the call itself
             made.forward(x, w, z, bias=bias)
         assert not made._ran
+
+
+def test_weight_formats():
+    """Of a format that no product takes, a layer would pack its weight, run its norm, and fail there."""
+    import gradient_sync_zr_amd as zr
+    for good in (zr.ZR_CKPT_E4M3, zr.ZR_CKPT_E2M1):
+        layer(weight_format=good)
+    for bad in (zr.ZR_CKPT_INT8, zr.ZR_BF16, 9):
+        with pytest.raises(ValueError, match="weight_format"):
+            layer(weight_format=bad)
