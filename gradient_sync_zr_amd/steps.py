@@ -382,8 +382,9 @@ class ClipAdamW:
                  eps: float = 1e-8, weight_decay: float = 0.01, max_norm: float = 1.0, scale: float = 1.0):
         import torch
         self.numels = [g.numel() for g in grads]
-        self._tables = [tensor_table(xs, self.numels) for xs in (grads, params, exp_avg, exp_avg_sq)]
-        self._shards = None if shards is None else tensor_table(shards, self.numels)
+        self._tables = [tensor_table(grads, self.numels)] + [tensor_table(xs, self.numels, ZR_FP32)
+                                                             for xs in (params, exp_avg, exp_avg_sq)]
+        self._shards = None if shards is None else tensor_table(shards, self.numels, ZR_BF16)
         self.lr, self.beta1, self.beta2, self.eps, self.weight_decay = lr, beta1, beta2, eps, weight_decay
         self.max_norm, self.scale = max_norm, scale
         dev = params[0].device

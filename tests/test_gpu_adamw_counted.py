@@ -69,3 +69,14 @@ def test_counted_and_plain():
             want, lim = adam64(*(x[i].astype(np.float64) for x in host), 1.0, step=number, **HYPER)
             for j in range(3):
                 assert (np.abs(got[j][i].astype(np.float64) - want[j]) <= lim[j]).all(), (step, left, i, j)
+
+
+def test_types_are_checked_when_the_step_is_made():
+    """Not behind its first norm."""
+    import torch
+    from gradient_sync_zr_amd.steps import ClipAdamW
+    f, b = (torch.zeros(8, dtype=dt, device="cuda") for dt in (torch.float32, torch.bfloat16))
+    ClipAdamW([b], [f], [f.clone()], [f.clone()], [b.clone()])
+    for bad in ([[f], [b], [f], [f]], [[f], [f], [b], [f]], [[f], [f], [f], [b]], [[f], [f], [f], [f], [f]]):
+        with pytest.raises(ValueError, match="dtype"):
+            ClipAdamW(*bad)
