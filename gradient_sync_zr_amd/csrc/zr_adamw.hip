@@ -7,7 +7,7 @@
 // in fp32, and p rounded to bf16 as the shard that the all-gather takes. A
 // coefficient that is not finite leaves everything as it was. Steps so left out may be
 // counted on the device: t is then the step less those, and the corrections come from
-// there, as the host does not know of them.
+// there, as the host does not know of them (hidden: 337 us for 335 of 2^26 from bf16).
 //
 // A stream of 30 bytes per element (fp32 gradients, shards written), read and
 // written past the caches: 2^26 elements take 359 us (5.6 TB/s), 335 (5.6) from bf16

@@ -11,17 +11,24 @@
 //    not), which is below what a bf16 result keeps and not below fp32's. So bf16
 //    results take the scaled instructions, and for fp32 results both operands are
 //    decoded to bf16 on their way from LDS (every held value is exact there) and
-//    go through the bf16 instructions, which sum in fp32.
+//    go through the bf16 instructions, which sum in fp32. Against 64 bits a bf16 result
+//    is then off by as much as one that is summed in fp32 (1.66e-3 of the result's norm
+//    both, 1x4096x4096 and 8192x4096x4096; one or two elements in a hundred are the other
+//    neighbour of a border). Decoding would take 1.8 times as long, and for few rows up to
+//    a sixth longer of weights in 8 bits and a third in 4 (one token by 4096x11008 12.6
+//    us for 11.3, and 10.0 for 7.7).
 //
 // Reached, in TFLOP/s (with what the same instructions reach alone, held by the card's
-// power): e2m1 2,900 to 3,490 at 16384x11008x4096 and 3,120 to 3,820 at 8192^3 (6,500),
-// e4m3 2,130 to 2,400 (3,400 to 3,700), decoded 1,190 to 1,360 (bf16: 1,390 to 1,620);
-// the library's bf16 product reaches 1,235 and 1,375. The clock is at 1.8 to 1.95 GHz of
-// 2.4 meanwhile and the matrix units are busy 38% (e2m1) to 61% of the time. Of a
-// stage's 1.27 us 0.95 remain without the loads to LDS, and a tile costs 5 us in
-// front of its loop and behind it. Four waves of 128x128 instead of eight of 128x64
-// took 463 us for 424 (16384x11008x4096 of e2m1), operands read 3 or 4 steps ahead
-// and two stages of 128-byte rows the same.
+// power): e2m1 2,980 to 3,180 at 16384x11008x4096 and 3,870 to 3,960 at 8192^3 (6,500),
+// e4m3 2,260 to 2,500 (3,400 to 3,700), decoded 1,250 to 1,340 (bf16: 1,390 to 1,620);
+// the library's bf16 product reaches 1,235 and 1,375. The matrix units are busy 45 to 50%
+// (e2m1) and 56 to 64% (e4m3) of the time, at a clock of 1.7 to 1.8 GHz of 2.4, where the
+// instructions alone keep them busy throughout at a lower one; LDS is busy 37 to 43%,
+// and waves wait 30 to 34% of their cycles. Of a stage's 1.27 us 0.95 remain without the
+// loads to LDS, and a tile costs 5 us in front of its loop and behind it. Four waves of
+// 128x128 instead of eight of 128x64 took 463 us for 424 (16384x11008x4096 of e2m1, the
+// product behind its packing), operands read 3 or 4 steps ahead and two stages of 128-byte
+// rows the same.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -107,7 +114,7 @@ __device__ __forceinline__ void put8(const LinArgs& a, float* part, int64_t t, i
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] += old[e];
     }
-    store8<true>(z, a.z_dt, 0, n, f);  // past the caches: 16384x11008x4096 of e2m1 475 us without, 431 with
+    store8<true>(z, a.z_dt, 0, n, f);  // past the caches: 16384x11008x4096 of e2m1, behind its packing, 475 us without, 431 with
 }
 
 // ------------------------------------------------------------- tiled form
@@ -115,7 +122,9 @@ __device__ __forceinline__ void put8(const LinArgs& a, float* part, int64_t t, i
 // (two rows or four), two lines across its 64 banks. A chunk's place in its line is
 // exchanged by the number of the pair of lines, so that the 16 chunks of 16
 // neighbouring rows, which a read takes at once, lie in different banks. (Exchanged by
-// the line's number, half of the reads' cycles were conflicts.) The loads write LDS
+// the line's number, half of the reads' cycles were conflicts. What is left is the
+// exponents': a word of each row at a stride of 16 bytes, 288 of LDS's 768 cycles for a
+// 256 x 256 tile's 128 columns of e2m1, beside 1,024 of the matrix units.) The loads write LDS
 // directly, a wave's 64 chunks in a row, so the exchange is made in the addresses
 // that the lanes load from. 32 rows further down it is the same.
 template <int RB>
@@ -484,9 +493,10 @@ __global__ __launch_bounds__(kThreads) void linear_join_kernel(LinArgs a) {
 // Up to 64 tokens: the weight's bytes count, and each goes from memory to the
 // matrix instruction's registers once. A block of 8 waves takes 16 outputs; its
 // waves take every 8th turn of 512 columns, in 4 steps whose loads are in flight
-// at once, with a turn's exponents in one load, and are added in LDS. (Rows of codes too long for the tiled form's 32-bit
-// offsets come here too, 64 tokens at a time.) One token by 4096x4096 of e4m3 takes 5.4
-// to 5.9 us, of which a launch alone is 3.6, by 32768x8192 51 us (5.4 TB/s; of e2m1 38).
+// at once, with a turn's exponents in one load, and are added in LDS. (Rows of codes too
+// long for the tiled form's 32-bit offsets come here too, 64 tokens at a time.) One token
+// by 4096x4096 of e4m3 takes 6.2 us (of e2m1 5.0 to 5.7), of which a launch alone is 3.6, by
+// 32768x8192 46 to 51 us (5.4 to 6.0 TB/s; of e2m1 34 to 38).
 struct Piece {  // a row's 128 codes, one lane's quarter
     u32x4 p, q;
 };
