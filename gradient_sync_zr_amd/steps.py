@@ -390,7 +390,8 @@ class ClipAdamW:
         dev = params[0].device
         self.norm, self.coef = torch.zeros(1, device=dev), torch.zeros(1, device=dev)
         self._workspace = torch.empty(zr_grad_norm_workspace_bytes(len(self.numels)), dtype=torch.uint8, device=dev)
-        self.steps, self.left_out = 0, torch.zeros(1, dtype=torch.int64, device=dev)
+        # copied from the host, so that it is there for a first step on any stream
+        self.steps, self.left_out = 0, torch.zeros(1, dtype=torch.int64).to(dev)
 
     def step(self, lr: Optional[float] = None, stream=None) -> None:
         """One update, at rate lr (default: the object's)."""

@@ -80,3 +80,28 @@ def test_types_are_checked_when_the_step_is_made():
     for bad in ([[f], [b], [f], [f]], [[f], [f], [b], [f]], [[f], [f], [f], [b]], [[f], [f], [f], [f], [f]]):
         with pytest.raises(ValueError, match="dtype"):
             ClipAdamW(*bad)
+
+
+def test_first_step_on_another_stream():
+    """The count of steps left out is there before the constructor returns, whatever the current stream has in front."""
+    import torch
+    from gradient_sync_zr_amd.steps import ClipAdamW
+    sides = []
+    for busy in (False, True):
+        g, p, m, v = (torch.full((5000,), x, device="cuda") for x in (0.5, 1.0, 0.0, 0.0))
+        old = torch.full((1,), 1 << 40, device="cuda")  # what the count's memory may hold
+        a = torch.ones(4096, 4096, device="cuda")
+        stream = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        if busy:
+            for _ in range(20):
+                a = a @ a * 1e-4
+        del old
+        opt = ClipAdamW([g], [p], [m], [v], lr=0.1)
+        opt.steps = 6
+        with torch.cuda.stream(stream):
+            opt.step()
+        torch.cuda.synchronize()
+        assert int(opt.left_out) == 0 and opt.steps == 7
+        sides.append([p, m, v])
+    assert all(torch.equal(x, y) for x, y in zip(*sides))
